@@ -90,6 +90,13 @@ SIGNATURES = {
     "moe_combine_shared": ([_SP, _P, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
     "moe_router_topk": ([_SP, _P, _P, _P, _P], ctypes.c_int),
     "moe_silu_mul_quant": ([_SP, ctypes.c_int32, _P, _P, _P, _P, _P, _P], ctypes.c_int),
+    "moe_ffn_workspace_size": ([_SP, ctypes.c_int32], _S),
+    "moe_ffn": ([_SP, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P], ctypes.c_int),
+    "moe_ffn_backward": ([_SP, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P],
+                         ctypes.c_int),
+    "moe_combine_backward": ([_SP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
+    "moe_clip_workspace_size": ([], _S),
+    "moe_clip_grad_norm": ([_P, ctypes.c_int32, ctypes.c_float, _P, _P, _S, _P], ctypes.c_int),
     "moe_plan_dispatch": ([_SP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P], ctypes.c_int),
 }
 
@@ -250,6 +257,76 @@ def silu_mul_quant(shape: Shape, intermediate: int, expert_h, expert_num_tokens,
                                            _ptr(expert_num_tokens), _ptr(act_q), _ptr(act_scale),
                                            _ptr(workspace), _stream(stream))
     return _check(st, "moe_silu_mul_quant", check)
+
+
+def ffn_workspace_size(shape: Shape, intermediate: int) -> int:
+    return load_library().moe_ffn_workspace_size(ctypes.byref(shape), intermediate)
+
+
+def ffn(shape: Shape, intermediate: int, expert_x, w_gate_up, w_down, expert_num_tokens, expert_h,
+        expert_act, expert_y, workspace, stream=None, check=True) -> Status:
+    """moe_ffn: the experts' gated feed-forward; ``expert_h`` (kept for the
+    backward pass) and ``expert_num_tokens`` (every row exists) may be None."""
+    st = load_library().moe_ffn(ctypes.byref(shape), intermediate, _ptr(expert_x), _ptr(w_gate_up),
+                                _ptr(w_down), _ptr(expert_num_tokens), _ptr(expert_h),
+                                _ptr(expert_act), _ptr(expert_y), _ptr(workspace),
+                                workspace.numel() * workspace.element_size(), _stream(stream))
+    return _check(st, "moe_ffn", check)
+
+
+def ffn_backward(shape: Shape, intermediate: int, d_expert_y, expert_x, expert_h, w_gate_up, w_down,
+                 expert_num_tokens, expert_act, d_expert_h, d_expert_x, d_w_gate_up, d_w_down,
+                 workspace, stream=None, check=True) -> Status:
+    """moe_ffn_backward; each of ``d_expert_x``, ``d_w_gate_up`` and
+    ``d_w_down`` may be None (not computed)."""
+    st = load_library().moe_ffn_backward(ctypes.byref(shape), intermediate, _ptr(d_expert_y),
+                                         _ptr(expert_x), _ptr(expert_h), _ptr(w_gate_up),
+                                         _ptr(w_down), _ptr(expert_num_tokens), _ptr(expert_act),
+                                         _ptr(d_expert_h), _ptr(d_expert_x), _ptr(d_w_gate_up),
+                                         _ptr(d_w_down), _ptr(workspace),
+                                         workspace.numel() * workspace.element_size(),
+                                         _stream(stream))
+    return _check(st, "moe_ffn_backward", check)
+
+
+def combine_backward(shape: Shape, d_y, expert_y, topk_idx, slot_of, topk_weights, d_expert_y,
+                     d_weights, d_logits, workspace, stream=None, check=True) -> Status:
+    """moe_combine_backward; ``d_logits`` may be None."""
+    st = load_library().moe_combine_backward(ctypes.byref(shape), _ptr(d_y), _ptr(expert_y),
+                                             _ptr(topk_idx), _ptr(slot_of), _ptr(topk_weights),
+                                             _ptr(d_expert_y), _ptr(d_weights), _ptr(d_logits),
+                                             _ptr(workspace), _stream(stream))
+    return _check(st, "moe_combine_backward", check)
+
+
+def clip_workspace_size() -> int:
+    return load_library().moe_clip_workspace_size()
+
+
+def clip_grad_norm(grads, outs, max_norm: float, total_norm, workspace, stream=None,
+                   check=True) -> Status:
+    """moe_clip_grad_norm over lists of contiguous bf16 or fp32 tensors;
+    ``outs`` may be ``grads`` (in place).  A tensor of another type raises
+    MoEError(INVALID_ARG)."""
+    import numpy as np
+    import torch
+    table = np.zeros((len(grads), 4), np.int64)           # moe_grad_tensor, 32 bytes each
+    if len(grads) != len(outs):
+        return _check(Status.INVALID_ARG, "moe_clip_grad_norm", check)
+    if grads:
+        codes = {torch.bfloat16: 0, torch.float32: 1}
+        table[:, 0] = [t.data_ptr() for t in grads]
+        table[:, 1] = table[:, 0] if outs is grads else [t.data_ptr() for t in outs]
+        table[:, 2] = [t.numel() for t in grads]
+        table[:, 3] = [codes.get(t.dtype, 0x7FFFFFFF) for t in grads]
+        if outs is not grads and any(o.dtype != g.dtype or o.numel() != g.numel()
+                                     for o, g in zip(outs, grads)):
+            return _check(Status.INVALID_ARG, "moe_clip_grad_norm", check)
+    st = load_library().moe_clip_grad_norm(table.ctypes.data, len(grads), max_norm, _ptr(total_norm),
+                                           _ptr(workspace),
+                                           workspace.numel() * workspace.element_size(),
+                                           _stream(stream))
+    return _check(st, "moe_clip_grad_norm", check)
 
 
 def read_status(workspace, stream=None) -> Status:

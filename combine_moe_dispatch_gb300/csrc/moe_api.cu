@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "moe_common.cuh"
+#include "moe_ffn.cuh"
 
 namespace moe {
 
@@ -361,6 +362,146 @@ moe_status moe_silu_mul_quant(const moe_shape *shape, int32_t intermediate, cons
   p.I = intermediate;
   p.scale_t = shape->payload == MOE_PAYLOAD_FP8_E4M3_TSCALE;
   return from_cuda(launch_silu_quant(p, (cudaStream_t)stream));
+}
+
+// Checks that moe_ffn and moe_ffn_backward share.
+static moe_status ffn_check(const moe_shape *shape, int32_t intermediate, const void *workspace,
+                            size_t workspace_bytes) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if (intermediate <= 0) return MOE_ERR_INVALID_ARG;
+  if (shape->payload != MOE_PAYLOAD_BF16 || intermediate % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  const int64_t rows = (int64_t)shape->num_experts * shape->capacity, lim = (int64_t)1 << 46;
+  // rows < 2^31 and the widths < 2^32: no product here passes 2^63
+  if (rows * 2 * intermediate >= lim || rows * shape->hidden >= lim ||
+      (int64_t)4 * intermediate >= ((int64_t)1 << 40) / shape->hidden)
+    return MOE_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < moe_ffn_workspace_size(shape, intermediate))
+    return MOE_ERR_WORKSPACE;
+  return aligned(workspace, 16) ? MOE_OK : MOE_ERR_ALIGNMENT;
+}
+
+size_t moe_ffn_workspace_size(const moe_shape *shape, int32_t intermediate) {
+  if (intermediate <= 0) return 0;
+  return moe_workspace_size(shape);
+}
+
+moe_status moe_ffn(const moe_shape *shape, int32_t intermediate, const void *expert_x,
+                   const void *w_gate_up, const void *w_down, const int32_t *expert_num_tokens,
+                   void *expert_h, void *expert_act, void *expert_y, void *workspace,
+                   size_t workspace_bytes, void *stream) {
+  const moe_status st = ffn_check(shape, intermediate, workspace, workspace_bytes);
+  if (st != MOE_OK && st != MOE_ERR_WORKSPACE && st != MOE_ERR_ALIGNMENT) return st;
+  if (!expert_x || !w_gate_up || !w_down || !expert_act || !expert_y) return MOE_ERR_INVALID_ARG;
+  if (st != MOE_OK) return st;
+  if (!aligned(expert_x, 16) || !aligned(w_gate_up, 16) || !aligned(w_down, 16) ||
+      !aligned(expert_h, 16) || !aligned(expert_act, 16) || !aligned(expert_y, 16) ||
+      !aligned(expert_num_tokens, 4))
+    return MOE_ERR_ALIGNMENT;
+  FfnParams f = {};
+  f.counts = expert_num_tokens;
+  f.hdr = header(workspace);
+  f.E = shape->num_experts;
+  f.cap = shape->capacity;
+  f.H = shape->hidden;
+  f.I = intermediate;
+  f.x = static_cast<const uint16_t *>(expert_x);
+  f.w_gate_up = static_cast<const uint16_t *>(w_gate_up);
+  f.w_down = static_cast<const uint16_t *>(w_down);
+  f.h = static_cast<uint16_t *>(expert_h);
+  f.act = static_cast<uint16_t *>(expert_act);
+  f.y = static_cast<uint16_t *>(expert_y);
+  return from_cuda(launch_ffn(f, (cudaStream_t)stream));
+}
+
+moe_status moe_ffn_backward(const moe_shape *shape, int32_t intermediate, const void *d_expert_y,
+                            const void *expert_x, const void *expert_h, const void *w_gate_up,
+                            const void *w_down, const int32_t *expert_num_tokens, void *expert_act,
+                            void *d_expert_h, void *d_expert_x, void *d_w_gate_up, void *d_w_down,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+  const moe_status st = ffn_check(shape, intermediate, workspace, workspace_bytes);
+  if (st != MOE_OK && st != MOE_ERR_WORKSPACE && st != MOE_ERR_ALIGNMENT) return st;
+  if (!d_expert_y || !expert_x || !expert_h || !w_gate_up || !w_down || !expert_act || !d_expert_h)
+    return MOE_ERR_INVALID_ARG;
+  if (st != MOE_OK) return st;
+  if (!aligned(d_expert_y, 16) || !aligned(expert_x, 16) || !aligned(expert_h, 16) ||
+      !aligned(w_gate_up, 16) || !aligned(w_down, 16) || !aligned(expert_act, 16) ||
+      !aligned(d_expert_h, 16) || !aligned(d_expert_x, 16) || !aligned(d_w_gate_up, 16) ||
+      !aligned(d_w_down, 16) || !aligned(expert_num_tokens, 4))
+    return MOE_ERR_ALIGNMENT;
+  FfnParams f = {};
+  f.counts = expert_num_tokens;
+  f.hdr = header(workspace);
+  f.E = shape->num_experts;
+  f.cap = shape->capacity;
+  f.H = shape->hidden;
+  f.I = intermediate;
+  f.dy = static_cast<const uint16_t *>(d_expert_y);
+  f.x = static_cast<const uint16_t *>(expert_x);
+  f.h = const_cast<uint16_t *>(static_cast<const uint16_t *>(expert_h));
+  f.w_gate_up = static_cast<const uint16_t *>(w_gate_up);
+  f.w_down = static_cast<const uint16_t *>(w_down);
+  f.act = static_cast<uint16_t *>(expert_act);
+  f.dh = static_cast<uint16_t *>(d_expert_h);
+  f.dx = static_cast<uint16_t *>(d_expert_x);
+  f.dw_gate_up = static_cast<uint16_t *>(d_w_gate_up);
+  f.dw_down = static_cast<uint16_t *>(d_w_down);
+  return from_cuda(launch_ffn_backward(f, (cudaStream_t)stream));
+}
+
+moe_status moe_combine_backward(const moe_shape *shape, const void *d_y, const void *expert_y,
+                                const int32_t *topk_idx, const int32_t *slot_of,
+                                const float *topk_weights, void *d_expert_y, float *d_weights,
+                                float *d_logits, void *workspace, void *stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if (shape->tokens_per_rank == 0) return MOE_OK;   // empty batch: nothing to read or write
+  if (!d_y || !expert_y || !topk_idx || !slot_of || !topk_weights || !d_expert_y || !d_weights)
+    return MOE_ERR_INVALID_ARG;
+  if (!workspace) return MOE_ERR_WORKSPACE;
+  if (!aligned(d_y, 16) || !aligned(expert_y, 16) || !aligned(d_expert_y, 16) ||
+      !aligned(topk_idx, 4) || !aligned(slot_of, 4) || !aligned(topk_weights, 4) ||
+      !aligned(d_weights, 4) || !aligned(d_logits, 4) || !aligned(workspace, 16))
+    return MOE_ERR_ALIGNMENT;
+  CombineBackwardParams p;
+  p.d_y = static_cast<const uint16_t *>(d_y);
+  p.expert_y = static_cast<const uint16_t *>(expert_y);
+  p.topk_idx = topk_idx;
+  p.slot_of = slot_of;
+  p.topk_weights = topk_weights;
+  p.d_expert_y = static_cast<uint16_t *>(d_expert_y);
+  p.d_weights = d_weights;
+  p.d_logits = d_logits;
+  p.hdr = header(workspace);
+  p.N = shape->num_ranks * shape->tokens_per_rank;
+  p.H = shape->hidden;
+  p.E = shape->num_experts;
+  p.K = shape->top_k;
+  p.cap = shape->capacity;
+  return from_cuda(launch_combine_backward(p, (cudaStream_t)stream));
+}
+
+size_t moe_clip_workspace_size(void) { return clip_workspace_bytes(); }
+
+moe_status moe_clip_grad_norm(const moe_grad_tensor *tensors, int32_t num_tensors, float max_norm,
+                              float *total_norm, void *workspace, size_t workspace_bytes,
+                              void *stream) {
+  if (num_tensors < 0 || (num_tensors > 0 && !tensors) || !total_norm || !(max_norm >= 0.0f))
+    return MOE_ERR_INVALID_ARG;
+  bool misaligned = !aligned(total_norm, 4);
+  for (int32_t i = 0; i < num_tensors; ++i) {
+    const moe_grad_tensor &t = tensors[i];
+    if (t.numel < 0 || (t.dtype != MOE_DTYPE_BF16 && t.dtype != MOE_DTYPE_FP32) ||
+        (t.numel > 0 && (!t.grad || !t.out)))
+      return MOE_ERR_INVALID_ARG;
+    if (t.numel >= ((int64_t)1 << 46)) return MOE_ERR_UNSUPPORTED;
+    const uintptr_t size = t.dtype == MOE_DTYPE_FP32 ? 4 : 2;
+    if (t.numel > 0 && (!aligned(t.grad, size) || !aligned(t.out, size))) misaligned = true;
+  }
+  if (!workspace || workspace_bytes < clip_workspace_bytes()) return MOE_ERR_WORKSPACE;
+  if (misaligned || !aligned(workspace, 16)) return MOE_ERR_ALIGNMENT;
+  return from_cuda(launch_clip(tensors, num_tensors, max_norm, total_norm, workspace,
+                               (cudaStream_t)stream));
 }
 
 moe_status moe_read_status(const void *workspace, void *stream, moe_status *out) {

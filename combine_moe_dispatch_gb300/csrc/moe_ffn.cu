@@ -1,0 +1,671 @@
+// moe_ffn.cu -- the experts' gated feed-forward over the dispatched rows, and
+// its backward pass, as grouped matrix products on the tensor cores.
+//
+// What it computes, for expert e and its count[e] rows x:
+//   h = x Wgu^T (gate | up),  a = SiLU(gate) * up,  y = a Wd^T
+// and, from dy and the kept h, with s = sigmoid(gate):
+//   da = dy Wd,  dgate = da up s (1 + gate (1 - s)),  dup = da gate s,
+//   dx = dh Wgu,  dWgu = dh^T x,  dWd = dy^T a.
+//
+// How: each of these six products is one launch of pair_kernel<MODE>.  A
+// cluster of two CTAs (the two SMs of a pair) computes a tile of 256 rows x
+// up to 256 columns with tcgen05.mma.cta_group::2: each CTA stages its half
+// of both operands (128 rows of A, half the columns of B, 64 k at a time) by
+// TMA in a ring of 6 stages, one thread of the leading CTA issues the matrix
+// instructions, and the accumulators stay in tensor memory, two tiles deep,
+// so that four epilogue warps per CTA write one tile while the next is
+// multiplied.
+//  - Products over the hidden or intermediate size ("row" modes) put the
+//    weights' output features on the 256-row side and the expert's tokens on
+//    the column side: the column count of a matrix instruction can be any
+//    multiple of 32, so an expert with 40 tokens costs 64 columns and not a
+//    whole tile of 256.  An expert's tokens are cut into equal tiles of at
+//    most 256.
+//  - Weight gradients ("weight" modes) contract over the expert's tokens;
+//    both operands are then read with the contraction as the outer dimension
+//    (MN-major shared-memory tiles).  Rows past count[e] are not the
+//    expert's and may hold anything, NaN included, so the last block of 64
+//    tokens is zeroed in shared memory past the count before it is used.
+// Counts are read on the device: nothing waits for the host, and the call can
+// be captured in a CUDA graph.  Tiles go to the pairs round robin.
+//
+// Rounding: the operands are bf16, every product and sum is accumulated in
+// binary32; a, dh and the results are rounded to bf16 once each (the matrix
+// instructions take 16-bit operands; the kept h is never re-rounded).
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <mutex>
+
+#include "moe_ffn.cuh"
+#include "moe_tc.cuh"
+
+namespace moe {
+
+namespace {
+
+enum Mode { kGateUp = 0, kDown = 1, kActGrad = 2, kInGrad = 3, kWeightGrad = 4 };
+
+constexpr int kPairThreads = 256;      // warps: 0 TMA, 1 MMA, 2 zeroes tails, 4-7 epilogue
+constexpr int kStages = 6;
+constexpr int kBlockK = 64;            // one 128-byte swizzled line of bf16
+constexpr uint32_t kHalfBytes = 128 * kBlockK * 2;       // a CTA's half of one operand: 16 KB
+constexpr uint32_t kStageBytes = 2 * kHalfBytes;
+constexpr uint32_t kStagingBytes = 2 * 16384;            // epilogue, two buffers
+constexpr uint32_t kBarOff = kStages * kStageBytes + kStagingBytes;
+constexpr uint32_t kPairSmem = kBarOff + 256 + 1024;     // + alignment slack
+static_assert(kPairSmem <= 232448, "shared memory of one CTA");
+constexpr int kTileCols = 256;
+constexpr uint32_t kTmemCols = 512;                      // two accumulators of 256 columns
+
+struct PairParams {
+  CUtensorMap a;
+  CUtensorMap b[4];        // row modes: boxes of 16, 32, 64 and 128 tokens
+  CUtensorMap out;         // weight modes: the gradient, stored by TMA
+  const int32_t *counts;   // [E], or null (cap rows each)
+  WsHeader *hdr;
+  uint16_t *o0, *o1;       // row modes: outputs (kGateUp: a, h or null; kActGrad: a, dh)
+  const uint16_t *h;       // kActGrad: kept gate | up
+  int E, cap;
+  int M, N, K;             // features; weight modes: output columns; row modes: contraction
+  int mt;                  // tiles of 256 accumulator rows (kGateUp: of 128 features)
+};
+
+__device__ __forceinline__ int rows_of(const PairParams &p, int e) {
+  if (!p.counts) return p.cap;
+  const int c = __ldg(p.counts + e);
+  return c < 0 ? 0 : (c > p.cap ? p.cap : c);
+}
+
+// Columns per tile of `rows` tokens: equal tiles, a multiple of 32.
+__device__ __forceinline__ int tile_cols(int rows) {
+  const int n = (rows + kTileCols - 1) / kTileCols;
+  const int c = (rows + n - 1) / n;
+  return (c + 31) & ~31;
+}
+__device__ __forceinline__ int token_tiles(int rows) {
+  if (rows == 0) return 0;
+  const int c = tile_cols(rows);
+  return (rows + c - 1) / c;
+}
+
+struct Tile {
+  int e, rows;             // expert, its tokens
+  int m;                   // tile of 256 accumulator rows
+  int n0, n;               // first column, columns of the matrix instruction
+  int cols;                // row modes: tokens in the tile
+  int nk;                  // blocks of 64 in the contraction (0: result is zero)
+};
+
+// Tile t of the launch, tiles ordered by expert; called by whole warps with
+// increasing t.  32 experts' tiles are counted at a time, one per lane.
+template <int MODE>
+struct Schedule {
+  const PairParams &p;
+  int64_t base, incl;
+  int e0, rows;
+  __device__ __forceinline__ explicit Schedule(const PairParams &p_) : p(p_), base(0), incl(0), e0(0), rows(0) {
+    if constexpr (MODE != kWeightGrad) count();
+  }
+  __device__ __forceinline__ void count() {
+    const int lane = threadIdx.x & 31, e = e0 + lane;
+    rows = e < p.E ? rows_of(p, e) : 0;
+    int64_t v = (int64_t)token_tiles(rows) * p.mt;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+      if (lane >= d) v += o;
+    }
+    incl = base + v;
+  }
+  __device__ __forceinline__ bool find(int64_t t, Tile &o) {
+    if constexpr (MODE == kWeightGrad) {
+      const int nt = (p.N + kTileCols - 1) / kTileCols;
+      const int64_t per = (int64_t)p.mt * nt;
+      if (t >= per * p.E) return false;
+      o.e = (int)(t / per);
+      const int r = (int)(t - o.e * per);
+      o.rows = rows_of(p, o.e);
+      o.m = r / nt;
+      o.n0 = (r - o.m * nt) * kTileCols;
+      o.n = min(kTileCols, (p.N - o.n0 + 31) & ~31);
+      o.cols = o.n;
+      o.nk = (o.rows + kBlockK - 1) / kBlockK;
+      return true;
+    } else {
+    while (true) {
+      const int64_t end = __shfl_sync(0xFFFFFFFFu, incl, 31);
+      if (t < end) break;
+      base = end;
+      e0 += 32;
+      if (e0 >= p.E) return false;
+      count();
+    }
+    const unsigned after = __ballot_sync(0xFFFFFFFFu, incl > t);
+    const int l = __ffs(after) - 1;
+    const int64_t before = __shfl_sync(0xFFFFFFFFu, incl, l > 0 ? l - 1 : 0);
+    const int r = (int)(t - (l > 0 ? before : base));
+    o.e = e0 + l;
+    o.rows = __shfl_sync(0xFFFFFFFFu, rows, l);
+    const int c = tile_cols(o.rows), nt = (o.rows + c - 1) / c;
+    o.m = r / nt;
+    o.n0 = (r - o.m * nt) * c;
+    o.cols = min(c, o.rows - o.n0);
+    o.n = (o.cols + 31) & ~31;
+    o.nk = (p.K + kBlockK - 1) / kBlockK;
+    return true;
+    }
+  }
+};
+
+// Wait for phase `parity` of the barrier, for `limit` ns at most and a
+// bounded number of polls.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t limit) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 0; it < (1u << 26); ++it) {
+    if (tc::mbar_try_cluster(bar, parity)) return true;
+    if ((it & 63u) == 63u) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > limit) return false;
+    }
+  }
+  return false;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint2 pack4(const float (&v)[4]) {
+  return make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+}
+__device__ __forceinline__ void unpack4(const uint2 &w, float (&v)[4]) {
+  v[0] = bf16_lo(w.x);
+  v[1] = bf16_hi(w.x);
+  v[2] = bf16_lo(w.y);
+  v[3] = bf16_hi(w.y);
+}
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+
+template <int MODE>
+__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
+pair_kernel(const __grid_constant__ PairParams p) {
+  constexpr bool kAMn = MODE == kActGrad || MODE == kInGrad || MODE == kWeightGrad;
+  constexpr bool kBMn = MODE == kWeightGrad;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t *smem_p = smem_raw + (smem - smem_u32(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_cta_rank();
+
+  const uint32_t staging = smem + kStages * kStageBytes;
+  const uint32_t bars = smem + kBarOff;
+  const uint32_t full = bars, empty = bars + 8 * kStages, tail = bars + 16 * kStages;
+  const uint32_t tm_full = bars + 24 * kStages, tm_empty = tm_full + 16;
+  const uint32_t tm_slot = tm_empty + 16;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init_at(full + 8 * s, 2);     // one arrival from each CTA, plus their bytes
+      tc::mbar_init_at(empty + 8 * s, 1);    // the commit of the stage's instructions
+      tc::mbar_init_at(tail + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init_at(tm_full + 8 * b, 1);
+      tc::mbar_init_at(tm_empty + 8 * b, 8);   // four epilogue warps in each CTA
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tc::prefetch_map(&p.a);
+    tc::prefetch_map(&p.b[0]);
+  }
+  if (warp == 2) tc::tmem_alloc_pair(tm_slot, kTmemCols);
+  tc::fence_before();
+  __syncthreads();
+  cluster_barrier();
+  tc::fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem_p + kBarOff + 24 * kStages + 32);
+
+  pdl_allow_dependents();
+  pdl_wait_for_previous();
+  // The status is read once, by every thread alike: after a plan error no
+  // tile is computed and nothing is written.
+  const bool live = read_status(p.hdr) == MOE_OK;
+  const uint64_t tmo = p.hdr->timeout_ns;
+  const uint64_t limit = tmo ? tmo : kDefaultTimeoutNs;
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  bool ok = true;
+
+  if (live && warp == 0) {
+    // ---- TMA: both CTAs load their halves; bytes complete on the leader's barrier
+    Schedule<MODE> sched(p);
+    Tile t;
+    int s = 0;
+    uint32_t ph = 0;
+    const uint32_t full0 = tc::map_rank(full, 0);
+    for (int64_t i = pair; ok && sched.find(i, t); i += pairs) {
+      if (lane == 0) {
+        const uint32_t half_n = t.n >> 1;
+        const int bsel = half_n <= 16 ? 0 : half_n <= 32 ? 1 : half_n <= 64 ? 2 : 3;
+        const uint32_t bytes = kHalfBytes + (kBMn ? kHalfBytes : (16u << bsel) * 128u);
+        const int tail_rows = MODE == kWeightGrad ? (t.rows & (kBlockK - 1)) : 0;
+        for (int kb = 0; kb < t.nk; ++kb) {
+          if (!wait_bar(empty + 8 * s, ph ^ 1u, limit)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = smem + s * kStageBytes, sb = sa + kHalfBytes;
+          const int k0 = kb * kBlockK;
+          if (MODE == kWeightGrad) {
+            const int m0 = t.m * 256 + rank * 128, n0 = t.n0 + rank * half_n;
+            if (tail_rows != 0 && kb == t.nk - 1) {
+              const uint32_t bar = tail + 8 * s;
+              tc::mbar_expect_local(bar, bytes);
+              tc::tma_load_own(sa, &p.a, bar, m0, k0, 0, t.e);
+              tc::tma_load_own(sa + 8192, &p.a, bar, m0 + 64, k0, 0, t.e);
+              tc::tma_load_own(sb, &p.b[0], bar, n0, k0, 0, t.e);
+              tc::tma_load_own(sb + 8192, &p.b[0], bar, n0 + 64, k0, 0, t.e);
+            } else {
+              const uint32_t bar = full0 + 8 * s;
+              tc::mbar_expect_cluster(bar, bytes);
+              tc::tma_load_pair(sa, &p.a, bar, m0, k0, 0, t.e);
+              tc::tma_load_pair(sa + 8192, &p.a, bar, m0 + 64, k0, 0, t.e);
+              tc::tma_load_pair(sb, &p.b[0], bar, n0, k0, 0, t.e);
+              tc::tma_load_pair(sb + 8192, &p.b[0], bar, n0 + 64, k0, 0, t.e);
+            }
+          } else {
+            const uint32_t bar = full0 + 8 * s;
+            tc::mbar_expect_cluster(bar, bytes);
+            if (MODE == kGateUp) {             // 64 gate rows, then the same 64 features of up
+              const int f0 = t.m * 128 + rank * 64;
+              tc::tma_load_pair(sa, &p.a, bar, k0, f0, 0, t.e);
+              tc::tma_load_pair(sa + 8192, &p.a, bar, k0, f0, 1, t.e);
+            } else if (kAMn) {
+              const int m0 = t.m * 256 + rank * 128;
+              tc::tma_load_pair(sa, &p.a, bar, m0, k0, 0, t.e);
+              tc::tma_load_pair(sa + 8192, &p.a, bar, m0 + 64, k0, 0, t.e);
+            } else {
+              tc::tma_load_pair(sa, &p.a, bar, k0, t.m * 256 + rank * 128, 0, t.e);
+            }
+            tc::tma_load_pair(sb, &p.b[bsel], bar, k0, t.n0 + rank * half_n, 0, t.e);
+          }
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    }
+    // the last commits on this CTA's barriers land before it may exit
+    if (lane == 0)
+      for (int i = 0; ok && i < kStages; ++i) {
+        ok = wait_bar(empty + 8 * s, ph ^ 1u, limit);
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+  } else if (live && warp == 1 && rank == 0) {
+    // ---- matrix instructions, one thread of the leading CTA
+    Schedule<MODE> sched(p);
+    Tile t;
+    int s = 0;
+    uint32_t ph = 0, it = 0;
+    for (int64_t i = pair; ok && sched.find(i, t); i += pairs) {
+      if (t.nk == 0) continue;
+      if (lane == 0) {
+        const uint32_t buf = it & 1u;
+        const uint32_t d = tmem + buf * kTileCols;
+        const uint32_t idesc = tc::instr_desc(256, t.n, kAMn, kBMn);
+        ok = wait_bar(tm_empty + 8 * buf, ((it >> 1) & 1u) ^ 1u, limit);
+        tc::fence_after();
+        for (int kb = 0; ok && kb < t.nk; ++kb) {
+          if (!wait_bar(full + 8 * s, ph, limit)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after();
+          const uint32_t sa = smem + s * kStageBytes, sb = sa + kHalfBytes;
+          const uint64_t da = tc::smem_desc(sa, kAMn ? 8192u : 16u);
+          const uint64_t db = tc::smem_desc(sb, kBMn ? 8192u : 16u);
+#pragma unroll
+          for (int k = 0; k < kBlockK / 16; ++k)
+            // 16 k on: 32 bytes of a K-major line, 16 lines (2048 bytes) MN-major
+            tc::mma_pair(d, da + (kAMn ? k * 128 : k * 2), db + (kBMn ? k * 128 : k * 2), idesc,
+                         kb > 0 || k > 0);
+          tc::mma_commit_pair(empty + 8 * s);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (ok) tc::mma_commit_pair(tm_full + 8 * buf);
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      ++it;
+    }
+  } else if (live && warp == 2 && MODE == kWeightGrad) {
+    // ---- zero the rows past the expert's count in its last block
+    Schedule<MODE> sched(p);
+    Tile t;
+    int s = 0;
+    uint32_t phases = 0;
+    const uint32_t full0 = tc::map_rank(full, 0);
+    for (int64_t i = pair; ok && sched.find(i, t); i += pairs) {
+      if (t.nk == 0) continue;
+      const int last = (s + t.nk - 1) % kStages;
+      s = (s + t.nk) % kStages;
+      const int valid = t.rows & (kBlockK - 1);
+      if (valid == 0) continue;
+      ok = wait_bar(tail + 8 * last, (phases >> last) & 1u, limit);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      phases ^= 1u << last;
+      if (!ok) break;
+      uint8_t *base = smem_p + last * kStageBytes;
+      for (int c = 0; c < 4; ++c)
+        for (int j = valid * 8 + lane; j < kBlockK * 8; j += 32)
+          *reinterpret_cast<uint4 *>(base + c * 8192 + j * 16) = make_uint4(0, 0, 0, 0);
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_cluster(full0 + 8 * last);
+    }
+  } else if (live && warp >= 4) {
+    // ---- epilogue: tensor memory -> registers -> shared memory -> results
+    Schedule<MODE> sched(p);
+    Tile t;
+    uint32_t it = 0, chunk = 0;
+    const int wq = warp - 4, tid = threadIdx.x - 128;
+    const uint32_t empty0 = tc::map_rank(tm_empty, 0);
+    for (int64_t i = pair; ok && sched.find(i, t); i += pairs) {
+      const uint32_t buf = it & 1u;
+      if (t.nk > 0) {
+        ok = wait_bar(tm_full + 8 * buf, (it >> 1) & 1u, limit);
+        tc::fence_after();
+      }
+      // all four warps agree to go on
+      ok = named_sync_and(1, 128, ok);
+      if (!ok) break;
+      const uint32_t src = tmem + ((uint32_t)(wq * 32) << 16) + buf * kTileCols;
+      if (MODE == kWeightGrad) {
+        const int row = wq * 32 + lane;
+        for (int c = 0; c < t.n; c += 64, ++chunk) {
+          const uint32_t dst = (chunk & 1u) * 16384u;
+          uint32_t v[32], w[32];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            if (t.nk > 0 && c + hf * 32 < t.n) {
+              tc::tmem_ld32(v, src + c + hf * 32);
+              tc::tmem_ld_wait();
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[hf * 16 + j] = pack2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+          }
+          if (t.nk > 0 && c + 64 >= t.n) {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(empty0 + 8 * buf);
+          }
+          // the store of two chunks ago has read its buffer
+          if (tid == 0) tc::store_wait_read<1>();
+          named_sync(1, 128);
+          uint8_t *q = smem_p + kStages * kStageBytes + dst + row * 128;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4 *>(q + ((j ^ (row & 7)) * 16)) =
+                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          tc::fence_async_smem();
+          named_sync(1, 128);
+          const int m0 = t.m * 256 + (int)rank * 128;
+          if (tid == 0 && m0 < p.M && t.n0 + c < p.N) {
+            tc::tma_store(&p.out, staging + dst, t.n0 + c, m0, 0, t.e);
+          }
+          if (tid == 0) tc::store_commit();
+        }
+      } else {
+        const int i4 = tid & 15, r8 = tid >> 4;
+        const int f0 = MODE == kGateUp ? t.m * 128 + (int)rank * 64 + 4 * i4
+                                       : t.m * 256 + (int)rank * 128 + 4 * i4;
+        const int64_t row0 = (int64_t)t.e * p.cap + t.n0;
+        for (int c = 0; c < t.n; c += 32, ++chunk) {
+          uint2 g[4][2], u[4][2];
+          if (MODE == kActGrad) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+                if (c + r * 8 + r8 < t.cols && f0 + 64 * hf < p.M) {
+                  const uint16_t *q = p.h + (row0 + c + r * 8 + r8) * 2 * p.M + f0 + 64 * hf;
+                  g[r][hf] = *reinterpret_cast<const uint2 *>(q);
+                  u[r][hf] = *reinterpret_cast<const uint2 *>(q + p.M);
+                }
+          }
+          uint32_t v[32];
+          tc::tmem_ld32(v, src + c);
+          tc::tmem_ld_wait();
+          if (c + 32 >= t.n) {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(empty0 + 8 * buf);
+          }
+          float *st = reinterpret_cast<float *>(smem_p + kStages * kStageBytes + (chunk & 1u) * 16384u);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) st[j * 128 + wq * 32 + lane] = __uint_as_float(v[j]);
+          named_sync(1, 128);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int tok = r * 8 + r8;
+            if (c + tok >= t.cols) continue;
+            const float4 lo4 = *reinterpret_cast<const float4 *>(st + tok * 128 + 4 * i4);
+            const float4 hi4 = *reinterpret_cast<const float4 *>(st + tok * 128 + 64 + 4 * i4);
+            const float lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
+            const int64_t row = row0 + c + tok;
+            if (MODE == kGateUp) {
+              if (f0 < p.M) {
+                float a[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a[j] = lo[j] * sigmoid(lo[j]) * hi[j];
+                *reinterpret_cast<uint2 *>(p.o0 + row * p.M + f0) = pack4(a);
+                if (p.o1) {
+                  *reinterpret_cast<uint2 *>(p.o1 + row * 2 * p.M + f0) = pack4(lo);
+                  *reinterpret_cast<uint2 *>(p.o1 + row * 2 * p.M + p.M + f0) = pack4(hi);
+                }
+              }
+            } else if (MODE == kActGrad) {
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf)
+                if (f0 + 64 * hf < p.M) {
+                  float gv[4], uv[4], a[4], dg[4], du[4];
+                  unpack4(g[r][hf], gv);
+                  unpack4(u[r][hf], uv);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    const float da = hf ? hi[j] : lo[j];
+                    const float sg = sigmoid(gv[j]), silu = gv[j] * sg;
+                    a[j] = silu * uv[j];
+                    du[j] = da * silu;
+                    dg[j] = da * uv[j] * (sg + silu * (1.0f - sg));
+                  }
+                  *reinterpret_cast<uint2 *>(p.o0 + row * p.M + f0 + 64 * hf) = pack4(a);
+                  uint16_t *q = p.o1 + row * 2 * p.M + f0 + 64 * hf;
+                  *reinterpret_cast<uint2 *>(q) = pack4(dg);
+                  *reinterpret_cast<uint2 *>(q + p.M) = pack4(du);
+                }
+            } else {
+              if (f0 < p.M) *reinterpret_cast<uint2 *>(p.o0 + row * p.M + f0) = pack4(lo);
+              if (f0 + 64 < p.M) *reinterpret_cast<uint2 *>(p.o0 + row * p.M + f0 + 64) = pack4(hi);
+            }
+          }
+        }
+      }
+      if (t.nk > 0) ++it;
+    }
+    if (MODE == kWeightGrad && tid == 0) tc::store_wait_all();
+  }
+
+  if (!ok) {
+    // a wait ran out: report it, and give the copies and products that are
+    // already issued (microseconds of work) time to land before the exit
+    if (lane == 0) {
+      report_status(p.hdr, MOE_ERR_TIMEOUT);
+      for (int i = 0; i < 1000; ++i) __nanosleep(10000);
+    }
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  cluster_barrier();
+  if (warp == 2) tc::tmem_free_pair(tmem, kTmemCols);
+}
+
+// --- host --------------------------------------------------------------------
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static EncodeFn fn = [] {
+    void *q = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &r) !=
+            cudaSuccess || r != cudaDriverEntryPointSuccess)
+      q = nullptr;
+    return reinterpret_cast<EncodeFn>(q);
+  }();
+  return fn;
+}
+
+// [d3][d2][d1][d0] bf16, dense; boxes of 64 x rows elements, 128-byte swizzle.
+bool make_map(CUtensorMap *m, const void *base, int64_t d0, int64_t d1, int64_t d2, int64_t d3,
+              int rows) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2, (cuuint64_t)d3};
+  const cuuint64_t strides[3] = {(cuuint64_t)d0 * 2, (cuuint64_t)(d0 * d1) * 2,
+                                 (cuuint64_t)(d0 * d1 * d2) * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE>
+cudaError_t launch_pair(const PairParams &p, int64_t tiles, cudaStream_t stream) {
+  static std::once_flag once[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t attr = cudaSuccess;
+  std::call_once(once[dev & 63], [&] {
+    attr = cudaFuncSetAttribute(pair_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)kPairSmem);
+  });
+  if (attr != cudaSuccess) return attr;
+  const int64_t most = device_sm_count() / 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(2 * (tiles < most ? tiles : most)));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, pair_kernel<MODE>, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+PairParams base_params(const FfnParams &f) {
+  PairParams p = {};
+  p.counts = f.counts;
+  p.hdr = f.hdr;
+  p.E = f.E;
+  p.cap = f.cap;
+  return p;
+}
+
+bool token_maps(PairParams &p, const void *rows, int64_t width) {
+  for (int i = 0; i < 4; ++i)
+    if (!make_map(&p.b[i], rows, width, p.cap, 1, p.E, 16 << i)) return false;
+  return true;
+}
+
+}  // namespace
+
+cudaError_t launch_ffn(const FfnParams &f, cudaStream_t stream) {
+  const int64_t nt = f.E * cdiv(f.cap, kTileCols);      // most token tiles
+  PairParams p = base_params(f);
+  if (!make_map(&p.a, f.w_gate_up, f.H, f.I, 2, f.E, 64) || !token_maps(p, f.x, f.H))
+    return cudaErrorInvalidValue;
+  p.o0 = f.act;
+  p.o1 = f.h;
+  p.M = f.I;
+  p.K = f.H;
+  p.mt = (int)cdiv(f.I, 128);
+  cudaError_t e = launch_pair<kGateUp>(p, p.mt * nt, stream);
+  if (e != cudaSuccess) return e;
+  p = base_params(f);
+  if (!make_map(&p.a, f.w_down, f.I, f.H, 1, f.E, 128) || !token_maps(p, f.act, f.I))
+    return cudaErrorInvalidValue;
+  p.o0 = f.y;
+  p.M = f.H;
+  p.K = f.I;
+  p.mt = (int)cdiv(f.H, 256);
+  return launch_pair<kDown>(p, p.mt * nt, stream);
+}
+
+cudaError_t launch_ffn_backward(const FfnParams &f, cudaStream_t stream) {
+  const int64_t nt = f.E * cdiv(f.cap, kTileCols);
+  const int64_t I2 = 2 * (int64_t)f.I;
+  // dh and a
+  PairParams p = base_params(f);
+  if (!make_map(&p.a, f.w_down, f.I, f.H, 1, f.E, 64) || !token_maps(p, f.dy, f.H))
+    return cudaErrorInvalidValue;
+  p.o0 = f.act;
+  p.o1 = f.dh;
+  p.h = f.h;
+  p.M = f.I;
+  p.K = f.H;
+  p.mt = (int)cdiv(f.I, 256);
+  cudaError_t e = launch_pair<kActGrad>(p, p.mt * nt, stream);
+  if (e != cudaSuccess) return e;
+  if (f.dx) {
+    p = base_params(f);
+    if (!make_map(&p.a, f.w_gate_up, f.H, I2, 1, f.E, 64) || !token_maps(p, f.dh, I2))
+      return cudaErrorInvalidValue;
+    p.o0 = f.dx;
+    p.M = f.H;
+    p.K = (int)I2;
+    p.mt = (int)cdiv(f.H, 256);
+    e = launch_pair<kInGrad>(p, p.mt * nt, stream);
+    if (e != cudaSuccess) return e;
+  }
+  for (int w = 0; w < 2; ++w) {
+    uint16_t *out = w ? f.dw_down : f.dw_gate_up;
+    if (!out) continue;
+    const int64_t M = w ? f.H : I2, N = w ? f.I : f.H;
+    p = base_params(f);
+    if (!make_map(&p.a, w ? (const void *)f.dy : f.dh, M, f.cap, 1, f.E, 64) ||
+        !make_map(&p.b[0], w ? (const void *)f.act : f.x, N, f.cap, 1, f.E, 64) ||
+        !make_map(&p.out, out, N, M, 1, f.E, 128))
+      return cudaErrorInvalidValue;
+    p.M = (int)M;
+    p.N = (int)N;
+    p.mt = (int)cdiv(M, 256);
+    e = launch_pair<kWeightGrad>(p, p.mt * cdiv(N, kTileCols) * f.E, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace moe

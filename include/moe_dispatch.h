@@ -326,6 +326,128 @@ moe_status moe_silu_mul_quant(const moe_shape *shape, int32_t intermediate, cons
                               const int32_t *expert_num_tokens, void *act_q, float *act_scale,
                               void *workspace, void *stream);
 
+/* The experts' gated feed-forward over the dispatched rows, driven by the
+ * routing counts: for expert e and row s < clamp(expert_num_tokens[e], 0, cap),
+ *   h = x Wgu^T           (2I features: gate, then up)
+ *   a = SiLU(gate) * up   (from h in binary32)
+ *   y = a Wd^T
+ *
+ * Stands between moe_dispatch (bf16 payload) and moe_combine: "Lower latency
+ * and higher throughput with multi-node DeepSeek deployment", GroupGEMM and
+ * Quantization (grouped products over the experts' contiguous rows that read
+ * the per-expert token counts, not the buffer sizes, so that they stay valid
+ * in a CUDA graph).  Two launches on the tensor cores; operands bf16, sums in
+ * binary32, one rounding to bf16 of a, of y and of the kept h.
+ * In:   expert_x  [E, cap, H] bf16 (from moe_dispatch); rows from the count
+ *                 on are never used, whatever they hold;
+ *       w_gate_up [E, 2*intermediate, H] bf16, w_down [E, H, intermediate] bf16;
+ *       expert_num_tokens [E] int32 (from moe_plan), or NULL: every expert has
+ *                 cap rows (with E = 1, a dense feed-forward such as the
+ *                 shared expert's).
+ * Out:  expert_h  [E, cap, 2*intermediate] bf16, kept for moe_ffn_backward, or
+ *                 NULL; expert_act [E, cap, intermediate] bf16, always written
+ *                 (y is computed from it); expert_y [E, cap, H] bf16.  Rows
+ *                 below the count only; other rows are not touched.
+ * Work: the workspace of the plan that produced the counts, of at least
+ *       moe_ffn_workspace_size(shape, intermediate) bytes (which is never less
+ *       than moe_workspace_size); nothing is written if its status word is
+ *       set, and a wait inside a kernel that runs out sets it to TIMEOUT.
+ * Limits: payload BF16; intermediate % 8 == 0; E * cap * 2 * intermediate and
+ *       E * cap * H < 2^46; 4 * intermediate * H < 2^40 bytes.  All bf16 arrays
+ *       16-byte aligned.  No output may overlap an input.
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA. */
+size_t moe_ffn_workspace_size(const moe_shape *shape, int32_t intermediate);
+moe_status moe_ffn(const moe_shape *shape, int32_t intermediate, const void *expert_x,
+                   const void *w_gate_up, const void *w_down, const int32_t *expert_num_tokens,
+                   void *expert_h, void *expert_act, void *expert_y, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/* Backward pass of moe_ffn.  With s = sigmoid(gate), for the rows below the
+ * count:
+ *   da = dy Wd,  dgate = da * up * s * (1 + gate * (1 - s)),  dup = da * gate * s,
+ *   dx = dh Wgu (dh = dgate | dup),  dWgu = dh^T x,  dWd = dy^T a.
+ * The pages describe serving only; this is the derivative of moe_ffn, with
+ * the same arithmetic: bf16 operands, sums in binary32 (da is not rounded
+ * before the activation's derivative), one rounding of a, dh and each result.
+ * In:   d_expert_y [E, cap, H] (from moe_combine_backward), expert_x, expert_h
+ *       (as moe_ffn kept it), the weights and the counts of the forward call.
+ * Out:  expert_act [E, cap, intermediate] and d_expert_h [E, cap, 2*intermediate]
+ *       bf16 (computed here, read by the products that follow; rows below the
+ *       count); d_expert_x [E, cap, H] bf16 (rows below the count);
+ *       d_w_gate_up [E, 2*intermediate, H] and d_w_down [E, H, intermediate]
+ *       bf16, every element written: 0 for an expert without rows.  Each of
+ *       d_expert_x, d_w_gate_up and d_w_down may be NULL: not computed.
+ * Four launches at most.  Work, limits, errors: as moe_ffn. */
+moe_status moe_ffn_backward(const moe_shape *shape, int32_t intermediate, const void *d_expert_y,
+                            const void *expert_x, const void *expert_h, const void *w_gate_up,
+                            const void *w_down, const int32_t *expert_num_tokens, void *expert_act,
+                            void *d_expert_h, void *d_expert_x, void *d_w_gate_up, void *d_w_down,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward pass of moe_combine, down to the router's logits: for every routed
+ * entry (g, k) with row (e, s) = (topk_idx[g,k], slot_of[g,k]),
+ *   d_expert_y[e][s] = bf16( topk_weights[g,k] * d_y[g] )
+ *   d_weights[g,k]   = sum over h of d_y[g][h] * expert_y[e][s][h]
+ *   d_logits[g][e]   = w_k * (d_weights[g,k] - sum over j of w_j * d_weights[g,j])
+ * (moe_router_topk's softmax over the chosen logits; every other logit of the
+ * token gets 0, an expert chosen twice the sum of its entries).
+ *
+ * The gradient of the dispatched rows goes back to the tokens by moe_combine
+ * itself, with weights of 1: d_x[g] = sum over k of d_expert_x[e][s].  With
+ * moe_combine_shared, the shared expert's output has the gradient d_y.
+ * In:   d_y [N, H] bf16, expert_y [E, cap, H] bf16 (16-byte aligned);
+ *       topk_idx, slot_of, topk_weights [N, K] as moe_combine.
+ * Out:  d_expert_y [E, cap, H] bf16, the routed rows only; d_weights [N, K]
+ *       fp32, 0 for entries that are not routed; d_logits [N, E] fp32, every
+ *       element written, or NULL.
+ * Work: the workspace moe_plan used; nothing is written if its status word
+ *       is set; entries out of range are skipped and set it; entries with
+ *       slot_of = -1 (not routed) are skipped silently.
+ * Host errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA. */
+moe_status moe_combine_backward(const moe_shape *shape, const void *d_y, const void *expert_y,
+                                const int32_t *topk_idx, const int32_t *slot_of,
+                                const float *topk_weights, void *d_expert_y, float *d_weights,
+                                float *d_logits, void *workspace, void *stream);
+
+typedef enum {
+  MOE_DTYPE_BF16 = 0,
+  MOE_DTYPE_FP32 = 1
+} moe_dtype;
+
+/* One gradient of moe_clip_grad_norm: `numel` elements at `grad` (device
+ * memory, aligned to its type), their clipped values to `out`: `grad` itself,
+ * or an array that overlaps no gradient.  numel = 0: both are ignored. */
+typedef struct {
+  const void *grad;
+  void *out;
+  int64_t numel;
+  int32_t dtype;            /* a moe_dtype value */
+  int32_t reserved;         /* 0 */
+} moe_grad_tensor;
+
+/* Global gradient norm over many tensors, and clipping:
+ *   total_norm = sqrt( sum over all tensors and elements of g^2 )
+ *   out        = g * min(1, max_norm / (total_norm + 1e-6)), in g's type.
+ * The pages describe serving only; this is the step between the backward pass
+ * and the optimiser.  Squares are summed in binary32 over at most 128 elements
+ * and in binary64 above, in an order that depends on the sizes, the addresses
+ * modulo 16 and the device alone: the same inputs give the same bits.  A norm
+ * that is NaN or infinite goes through the formula as it stands (NaN: every
+ * output is NaN).  Where out is grad and nothing is clipped, nothing is
+ * written.
+ * In:   tensors [num_tensors], a HOST array (read before the call returns);
+ *       num_tensors >= 0; max_norm >= 0.
+ * Out:  total_norm [1] fp32, 4-byte aligned; the `out` arrays.
+ * Work: moe_clip_workspace_size() bytes, 16-byte aligned, zeroed once before
+ *       its first use (moe_workspace_init).
+ * Errors: INVALID_ARG (null pointer, negative size, unknown dtype, max_norm
+ *       negative or NaN), UNSUPPORTED (numel >= 2^46), ALIGNMENT, WORKSPACE,
+ *       CUDA. */
+size_t moe_clip_workspace_size(void);
+moe_status moe_clip_grad_norm(const moe_grad_tensor *tensors, int32_t num_tensors, float max_norm,
+                              float *total_norm, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
 /* Synchronise `stream` and read the workspace status word into *out (MOE_OK
  * or a device error).  The only call that waits for the device; meant for
  * tests and error handling, not for the hot path.

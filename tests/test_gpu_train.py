@@ -1,0 +1,213 @@
+"""moe_combine_backward and moe_clip_grad_norm through the C ABI against the
+formulas in 64 bits.
+
+Tolerances.  Combine: w * dy is one binary32 product (2^-24) and one rounding
+to bf16 (2^-8): (2^-8 + 2^-23) |w dy|.  A dot product over H elements in
+binary32 is off by at most H 2^-24 of the sum of its terms' magnitudes (its
+products are exact).  d_logits: the dot products' errors, weighted, and K + 4
+binary32 operations on them.  Norm: binary32 over at most 128 squares
+(2^-24 each), half of it through the root, and one rounding: 2^-16 relative.
+Clipped values: the norm's error, three binary32 operations and the
+rounding to the tensor's type."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+D = torch.float64
+SENTINEL = -12345.0
+U24 = 2.0 ** -24
+U8 = 2.0 ** -8
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _normal(shape, std, seed, dtype=torch.bfloat16):
+    return torch.empty(shape, dtype=dtype, device="cuda").normal_(0.0, std, generator=_gen(seed))
+
+
+def _near(got, want, tol, what):
+    err = (got.to(D) - want).abs()
+    bad = ~(err <= tol)
+    assert not bool(bad.any()), (f"{what}: {int(bad.sum())} of {bad.numel()} off, worst "
+                                 f"{float((err / tol.clamp_min(1e-300)).max()):.3g} tolerances")
+
+
+# R, T, H, E, K: one token; one warp's row and less; rows of one block; K that
+# is not a power of two, more than one group of 8, and the largest; a row that
+# ends inside a block's step
+SHAPES = [(1, 1, 8, 1, 1), (1, 3, 256, 8, 2), (2, 70, 512, 16, 3), (1, 40, 520, 16, 4),
+          (2, 33, 1032, 64, 6), (1, 300, 7168, 32, 8), (1, 21, 2056, 40, 11), (1, 9, 72, 64, 32),
+          (1, 5, 4096, 33, 32)]
+
+
+@pytest.mark.parametrize("R,T,H,E,K", SHAPES)
+@pytest.mark.parametrize("masked", [0.0, 0.4])
+@pytest.mark.parametrize("logits", [True, False])
+def test_combine_backward(R, T, H, E, K, masked, logits):
+    import combine_moe_dispatch_gb300 as moe
+    N = R * T
+    shape = moe.make_shape(R, T, H, E, K, N)
+    idx = torch.rand((N, E), device="cuda", generator=_gen(1)).argsort(1)[:, :K].int().contiguous()
+    if masked:
+        idx[torch.rand((N, K), device="cuda", generator=_gen(2)) < masked] = -1
+        idx[N // 2] = -1                                   # a token with nothing routed
+    b = moe.Buffers(shape, expert_x=False, expert_y=False)
+    b.plan_masked(idx)
+    w = torch.softmax(_normal((N, K), 1.0, 3, torch.float32), 1)
+    if masked:
+        w[idx < 0] = float("nan")                          # weights of such entries are not used
+    dy, ey = _normal((N, H), 1.0, 4), _normal((E, N, H), 1.0, 5)
+    for e, n in enumerate(b.expert_num_tokens.tolist()):
+        ey[e, n:] = float("nan")
+    dey = torch.full((E, N, H), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    dw = torch.full((N, K), SENTINEL, dtype=torch.float32, device="cuda")
+    dl = torch.full((N, E), SENTINEL, dtype=torch.float32, device="cuda")
+    moe.combine_backward(shape, dy, ey, idx, b.slot_of, w, dey, dw, dl if logits else None, b.workspace)
+    assert moe.read_status(b.workspace) == moe.Status.OK
+    routed = b.slot_of >= 0
+    e = torch.where(routed, idx, 0).long()
+    s = torch.where(routed, b.slot_of, 0).long()
+    rows = torch.where(routed[:, :, None], ey[e, s].to(D), 0.0)
+    w64 = torch.where(routed, w.to(D), 0.0)
+    want = w64[:, :, None] * dy.to(D)[:, None, :]
+    _near(dey[e, s][routed], want[routed], (U8 + 2 * U24) * want[routed].abs() + 1e-40, "d_expert_y")
+    for i, n in enumerate(b.expert_num_tokens.tolist()):
+        assert bool((dey[i, n:] == SENTINEL).all()), "rows past the count were written"
+    dw64 = (rows * dy.to(D)[:, None, :]).sum(2)
+    mag = (rows * dy.to(D)[:, None, :]).abs().sum(2)
+    tol = H * U24 * mag
+    _near(dw, dw64, tol, "d_weights")
+    if not logits:
+        assert bool((dl == SENTINEL).all())
+        return
+    mean = (w64 * dw64).sum(1, keepdim=True)
+    dl64 = torch.zeros((N, E), dtype=D, device="cuda").scatter_add_(1, e, w64 * (dw64 - mean))
+    spread = (w64 * (dw64.abs() + tol)).sum(1, keepdim=True)
+    t = w64 * (tol + (w64 * tol).sum(1, keepdim=True) + (K + 4) * U24 * (dw64.abs() + tol + spread))
+    tol_l = torch.zeros((N, E), dtype=D, device="cuda").scatter_add_(1, e, t)
+    _near(dl, dl64, tol_l, "d_logits")
+
+
+def test_combine_backward_twice_chosen_and_out_of_range():
+    """An expert chosen twice by a token gets the sum in d_logits; entries out
+    of range are skipped and reported; after an error nothing is written."""
+    import combine_moe_dispatch_gb300 as moe
+    N, H, E, K = 6, 64, 4, 3
+    shape = moe.make_shape(1, N, H, E, K, 2 * N)
+    idx = torch.tensor([[1, 1, 3]] * N, dtype=torch.int32, device="cuda")
+    b = moe.Buffers(shape, expert_x=False, expert_y=False)
+    b.plan(idx)
+    w = torch.softmax(_normal((N, K), 1.0, 6, torch.float32), 1)
+    dy, ey = _normal((N, H), 1.0, 7), _normal((E, 2 * N, H), 1.0, 8)
+    dey = torch.full((E, 2 * N, H), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    dw = torch.full((N, K), SENTINEL, dtype=torch.float32, device="cuda")
+    dl = torch.full((N, E), SENTINEL, dtype=torch.float32, device="cuda")
+    moe.combine_backward(shape, dy, ey, idx, b.slot_of, w, dey, dw, dl, b.workspace)
+    rows = ey[idx.long(), b.slot_of.long()].to(D)
+    dw64 = (rows * dy.to(D)[:, None, :]).sum(2)
+    own = w.to(D) * (dw64 - (w.to(D) * dw64).sum(1, keepdim=True))
+    dl64 = torch.zeros((N, E), dtype=D, device="cuda").scatter_add_(1, idx.long(), own)
+    mag = (rows * dy.to(D)[:, None, :]).abs().sum(2).max()
+    _near(dl, dl64, torch.full_like(dl64, 4 * H * U24 * float(mag)), "d_logits")
+    bad = idx.clone()
+    bad[2, 1] = E
+    dey.fill_(SENTINEL)
+    moe.combine_backward(shape, dy, ey, bad, b.slot_of, w, dey, dw, dl, b.workspace)
+    assert moe.read_status(b.workspace) == moe.Status.BAD_EXPERT
+    dey.fill_(SENTINEL)
+    dw.fill_(SENTINEL)
+    moe.combine_backward(shape, dy, ey, idx, b.slot_of, w, dey, dw, dl, b.workspace)
+    torch.cuda.synchronize()
+    assert bool((dey == SENTINEL).all()) and bool((dw == SENTINEL).all())
+
+
+def _clip(grads, outs, max_norm, ws=None):
+    import combine_moe_dispatch_gb300 as moe
+    norm = torch.full((1,), SENTINEL, dtype=torch.float32, device="cuda")
+    if ws is None:
+        ws = torch.zeros(moe.clip_workspace_size(), dtype=torch.uint8, device="cuda")
+    moe.clip_grad_norm(grads, outs, max_norm, norm, ws)
+    return norm
+
+
+def _clip_check(grads, max_norm, inplace, ws=None):
+    outs = grads if inplace else [torch.full_like(g, SENTINEL) for g in grads]
+    before = [g.clone() for g in grads]
+    norm = _clip(grads, outs, max_norm, ws)
+    want = sum(float(g.to(D).square().sum()) for g in before) ** 0.5
+    assert abs(float(norm) - want) <= 2.0 ** -16 * want
+    coef = min(1.0, max_norm / (want + 1e-6))
+    for o, g in zip(outs, before):
+        u = U24 if g.dtype == torch.float32 else U8
+        _near(o, g.to(D) * coef, (u + 2.0 ** -15) * (g.to(D) * coef).abs() + 1e-40, "clipped")
+    if not inplace:
+        for a, g in zip(before, grads):
+            assert torch.equal(a, g)
+    return norm
+
+
+SIZES = [[1], [7, 1, 9], [4096], [16384, 16385, 3], [100003, 5, 262144, 31], [0, 12, 0], [8192] * 40]
+
+
+@pytest.mark.parametrize("sizes", SIZES, ids=[str(s[:3]) for s in SIZES])
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "mixed"])
+@pytest.mark.parametrize("max_norm,inplace", [(0.5, False), (0.5, True), (1e6, False), (1e6, True), (0.0, False)])
+def test_clip(sizes, kind, max_norm, inplace):
+    types = {"bf16": [torch.bfloat16], "fp32": [torch.float32], "mixed": [torch.bfloat16, torch.float32]}[kind]
+    grads = [_normal((n,), 1.0, i, types[i % len(types)]) for i, n in enumerate(sizes)]
+    _clip_check(grads, max_norm, inplace)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_clip_any_alignment(dtype):
+    """Views at every offset of a 16-byte group, in and out offset alike and
+    differently; what lies beside a view is not written."""
+    n, pad = 40000, 16
+    step = 16 // torch.empty((), dtype=dtype).element_size()
+    flat = _normal((step * (n + 2 * pad),), 1.0, 9, dtype)
+    for shift in (0, 1, 3):
+        grads, outs, at = [], [], []
+        out = torch.full_like(flat, SENTINEL)
+        for i in range(step):
+            a = i * (n + 2 * pad) + pad + i
+            grads.append(flat[a:a + n - 2 * step])
+            outs.append(out[a + shift:a + shift + n - 2 * step])
+            at.append((a + shift, a + shift + n - 2 * step))
+        norm = _clip(grads, outs, 3.0)
+        want = sum(float(g.to(D).square().sum()) for g in grads) ** 0.5
+        assert abs(float(norm) - want) <= 2.0 ** -16 * want
+        u = U24 if dtype == torch.float32 else U8
+        for o, g in zip(outs, grads):
+            w = g.to(D) * (3.0 / (want + 1e-6))
+            _near(o, w, (u + 2.0 ** -15) * w.abs() + 1e-40, "clipped")
+        free = torch.ones(flat.shape, dtype=torch.bool, device="cuda")
+        for a, z in at:
+            free[a:z] = False
+        assert bool((out[free] == SENTINEL).all())
+
+
+def test_clip_many_tensors_repeats_and_special_values():
+    """More tensors than one launch takes; the same bits every time, from a
+    workspace that is used again; no tensor at all; NaN and infinity."""
+    import combine_moe_dispatch_gb300 as moe
+    ws = torch.zeros(moe.clip_workspace_size(), dtype=torch.uint8, device="cuda")
+    grads = [_normal((1 + 37 * (i % 50),), 1.0, i, torch.bfloat16 if i % 3 else torch.float32)
+             for i in range(1300)]
+    first = _clip_check(grads, 1.0, False, ws)
+    for _ in range(3):
+        assert torch.equal(_clip_check(grads, 1.0, False, ws), first)
+    assert float(_clip([], [], 1.0, ws)) == 0.0
+    zero = [torch.zeros(100, device="cuda")]
+    assert float(_clip_check(zero, 1.0, False, ws)) == 0.0
+    g = [_normal((1000,), 1.0, 1, torch.float32), _normal((500,), 1.0, 2)]
+    g[1][77] = float("nan")
+    outs = [torch.empty_like(t) for t in g]
+    assert bool(torch.isnan(_clip(g, outs, 1.0, ws)).all())
+    assert all(bool(torch.isnan(o).all()) for o in outs)
+    g[1][77] = float("inf")
+    assert bool(torch.isinf(_clip(g, outs, 1.0, ws)).all())
+    assert bool((outs[0] == 0).all()) and bool(torch.isnan(outs[1][77]))
