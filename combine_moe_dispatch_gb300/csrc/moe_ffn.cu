@@ -163,7 +163,7 @@ struct Schedule {
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t limit) {
   uint64_t t0 = 0;
   for (uint32_t it = 0; it < (1u << 26); ++it) {
-    if (tc::mbar_try_cluster(bar, parity)) return true;
+    if (tc::mbar_try(bar, parity)) return true;
     if ((it & 63u) == 63u) {
       const uint64_t now = global_timer_ns();
       if (t0 == 0) t0 = now;
@@ -193,6 +193,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
 pair_kernel(const __grid_constant__ PairParams p) {
   constexpr bool kAMn = MODE == kActGrad || MODE == kInGrad || MODE == kWeightGrad;
   constexpr bool kBMn = MODE == kWeightGrad;
+  // A stage is full after one arrival, the leader's, and the bytes of both
+  // CTAs; a stage whose tail is zeroed, after each CTA's zeroing warp.
+  constexpr uint32_t kFullArrivals = MODE == kWeightGrad ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t *smem_p = smem_raw + (smem - smem_u32(smem_raw));
@@ -207,7 +210,7 @@ pair_kernel(const __grid_constant__ PairParams p) {
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      tc::mbar_init_at(full + 8 * s, 2);     // one arrival from each CTA, plus their bytes
+      tc::mbar_init_at(full + 8 * s, kFullArrivals);
       tc::mbar_init_at(empty + 8 * s, 1);    // the commit of the stage's instructions
       tc::mbar_init_at(tail + 8 * s, 1);
     }
@@ -267,7 +270,10 @@ pair_kernel(const __grid_constant__ PairParams p) {
               tc::tma_load_own(sb + 8192, &p.b[0], bar, n0 + 64, k0, 0, t.e);
             } else {
               const uint32_t bar = full0 + 8 * s;
-              tc::mbar_expect_cluster(bar, bytes);
+              if (rank == 0) {
+                tc::mbar_expect_local(full + 8 * s, 2 * bytes);
+                tc::mbar_arrive_local(full + 8 * s);
+              }
               tc::tma_load_pair(sa, &p.a, bar, m0, k0, 0, t.e);
               tc::tma_load_pair(sa + 8192, &p.a, bar, m0 + 64, k0, 0, t.e);
               tc::tma_load_pair(sb, &p.b[0], bar, n0, k0, 0, t.e);
@@ -275,7 +281,7 @@ pair_kernel(const __grid_constant__ PairParams p) {
             }
           } else {
             const uint32_t bar = full0 + 8 * s;
-            tc::mbar_expect_cluster(bar, bytes);
+            if (rank == 0) tc::mbar_expect_local(full + 8 * s, 2 * bytes);
             if (MODE == kGateUp) {             // 64 gate rows, then the same 64 features of up
               const int f0 = t.m * 128 + rank * 64;
               tc::tma_load_pair(sa, &p.a, bar, k0, f0, 0, t.e);
@@ -326,6 +332,8 @@ pair_kernel(const __grid_constant__ PairParams p) {
             ok = false;
             break;
           }
+          // zeroed by ordinary stores in either CTA: acquire those too
+          if (MODE == kWeightGrad && kb == t.nk - 1) tc::mbar_try_cluster(full + 8 * s, ph);
           tc::fence_after();
           const uint32_t sa = smem + s * kStageBytes, sb = sa + kHalfBytes;
           const uint64_t da = tc::smem_desc(sa, kAMn ? 8192u : 16u);
@@ -369,7 +377,7 @@ pair_kernel(const __grid_constant__ PairParams p) {
           *reinterpret_cast<uint4 *>(base + c * 8192 + j * 16) = make_uint4(0, 0, 0, 0);
       tc::fence_async_smem();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive_cluster(full0 + 8 * last);
+      if (lane == 0) tc::mbar_release_cluster(full0 + 8 * last);
     }
   } else if (live && warp >= 4) {
     // ---- epilogue: tensor memory -> registers -> shared memory -> results
@@ -409,7 +417,7 @@ pair_kernel(const __grid_constant__ PairParams p) {
           if (t.nk > 0 && c + 64 >= t.n) {
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(empty0 + 8 * buf);
+            if (lane == 0) tc::mbar_arrive_remote(empty0 + 8 * buf);
           }
           // the store of two chunks ago has read its buffer
           if (tid == 0) tc::store_wait_read<1>();
@@ -451,7 +459,7 @@ pair_kernel(const __grid_constant__ PairParams p) {
           if (c + 32 >= t.n) {
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(empty0 + 8 * buf);
+            if (lane == 0) tc::mbar_arrive_remote(empty0 + 8 * buf);
           }
           float *st = reinterpret_cast<float *>(smem_p + kStages * kStageBytes + (chunk & 1u) * 16384u);
 #pragma unroll
