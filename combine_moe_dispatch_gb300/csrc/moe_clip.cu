@@ -35,10 +35,11 @@ struct ClipTensor {
   int64_t numel;
 };
 
+template <int BATCH>
 struct ClipParams {
-  ClipTensor t[kClipBatch];
-  int64_t first[kClipBatch];                  // chunks before this tensor
-  uint32_t f32[kClipBatch / 32];              // bit i: tensor i is fp32
+  ClipTensor t[BATCH];
+  int64_t first[BATCH];                       // chunks before this tensor
+  uint32_t f32[BATCH / 32];                   // bit i: tensor i is fp32
   int num;
   int64_t chunks;
   ClipHeader *hdr;
@@ -49,7 +50,8 @@ struct ClipParams {
 };
 
 // The chunk's tensor: the last one whose first chunk is not after it.
-__device__ __forceinline__ int tensor_of(const ClipParams &p, int64_t chunk) {
+template <int BATCH>
+__device__ __forceinline__ int tensor_of(const ClipParams<BATCH> &p, int64_t chunk) {
   int lo = 0, hi = p.num;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -106,25 +108,24 @@ __device__ __forceinline__ float chunk_squares(const ClipTensor &t, int64_t inde
   const Chunk<T> c(t, index);
   constexpr int U = kChunkGroups / kClipThreads;
   float s = 0.0f;
-  uint4 v[U];
-  bool whole[U];
+  if (c.whole(c.g0) && c.whole(c.g0 + kChunkGroups - 1)) {
+    const uint4 *in4 = reinterpret_cast<const uint4 *>(c.base) + c.g0 + threadIdx.x;
+    uint4 v[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t g = c.g0 + u * kClipThreads + threadIdx.x;
-    whole[u] = g < c.g1 && c.whole(g);
-    v[u] = whole[u] ? __ldg(reinterpret_cast<const uint4 *>(c.base) + g) : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < U; ++u) v[u] = __ldg(in4 + u * kClipThreads);
+#pragma unroll
+    for (int u = 0; u < U; ++u) s += squares(v[u], T());
+    return s;
   }
-#pragma unroll
-  for (int u = 0; u < U; ++u) s += squares(v[u], T());
-  // the groups that the tensor fills in part: its first and its last
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t g = c.g0 + u * kClipThreads + threadIdx.x;
-    if (g < c.g1 && !whole[u])
+  for (int64_t g = c.g0 + threadIdx.x; g < c.g1; g += kClipThreads) {
+    if (c.whole(g)) {
+      s += squares(__ldg(reinterpret_cast<const uint4 *>(c.base) + g), T());
+    } else {
       for (int64_t i = max(g * c.VE, c.lead); i < min((g + 1) * c.VE, c.end); ++i) {
         const float x = to_float(c.base[i]);
         s = fmaf(x, x, s);
       }
+    }
   }
   return s;
 }
@@ -140,7 +141,9 @@ __device__ __forceinline__ double block_sum(double v, double *s_part) {
   return r;                                   // thread 0 has it
 }
 
-__global__ void __launch_bounds__(kClipThreads, 4) clip_norm_kernel(const __grid_constant__ ClipParams p) {
+template <int BATCH>
+__global__ void __launch_bounds__(kClipThreads, 4)
+clip_norm_kernel(const __grid_constant__ ClipParams<BATCH> p) {
   __shared__ double s_part[kClipThreads / 32];
   __shared__ bool s_last;
   pdl_wait_for_previous();
@@ -179,42 +182,50 @@ __global__ void __launch_bounds__(kClipThreads, 4) clip_norm_kernel(const __grid
 }
 
 template <typename T>
+__device__ __forceinline__ uint4 scaled(const uint4 &v, float coef) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (sizeof(T) == 4) {
+      w[i] = __float_as_uint(__uint_as_float(w[i]) * coef);
+    } else {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(bf16_lo(w[i]) * coef, bf16_hi(w[i]) * coef);
+      w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T>
 __device__ __forceinline__ void chunk_scale(const ClipTensor &t, int64_t index, float coef) {
   const Chunk<T> c(t, index);
   constexpr int U = kChunkGroups / kClipThreads;
   T *out = static_cast<T *>(t.out) - c.lead;
   const bool vec = (reinterpret_cast<uintptr_t>(out) & (kGroupBytes - 1)) == 0;
-  uint4 v[U];
-  bool whole[U];
+  if (vec && c.whole(c.g0) && c.whole(c.g0 + kChunkGroups - 1)) {
+    // a chunk inside the tensor: nothing to check per group
+    const uint4 *in4 = reinterpret_cast<const uint4 *>(c.base) + c.g0 + threadIdx.x;
+    uint4 *out4 = reinterpret_cast<uint4 *>(out) + c.g0 + threadIdx.x;
+    uint4 v[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t g = c.g0 + u * kClipThreads + threadIdx.x;
-    whole[u] = vec && g < c.g1 && c.whole(g);
-    if (whole[u]) v[u] = __ldcs(reinterpret_cast<const uint4 *>(c.base) + g);
+    for (int u = 0; u < U; ++u) v[u] = __ldcs(in4 + u * kClipThreads);
+#pragma unroll
+    for (int u = 0; u < U; ++u) __stcs(out4 + u * kClipThreads, scaled<T>(v[u], coef));
+    return;
   }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t g = c.g0 + u * kClipThreads + threadIdx.x;
-    if (whole[u]) {
-      uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (sizeof(T) == 4) {
-          w[i] = __float_as_uint(__uint_as_float(w[i]) * coef);
-        } else {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(bf16_lo(w[i]) * coef, bf16_hi(w[i]) * coef);
-          w[i] = *reinterpret_cast<const uint32_t *>(&b);
-        }
-      }
-      __stcs(reinterpret_cast<uint4 *>(out) + g, make_uint4(w[0], w[1], w[2], w[3]));
-    } else if (g < c.g1) {
+  for (int64_t g = c.g0 + threadIdx.x; g < c.g1; g += kClipThreads) {
+    if (vec && c.whole(g)) {
+      reinterpret_cast<uint4 *>(out)[g] = scaled<T>(reinterpret_cast<const uint4 *>(c.base)[g], coef);
+    } else {
       for (int64_t i = max(g * c.VE, c.lead); i < min((g + 1) * c.VE, c.end); ++i)
         store_as(out + i, to_float(c.base[i]) * coef);
     }
   }
 }
 
-__global__ void __launch_bounds__(kClipThreads, 3) clip_scale_kernel(const __grid_constant__ ClipParams p) {
+template <int BATCH>
+__global__ void __launch_bounds__(kClipThreads, 4)
+clip_scale_kernel(const __grid_constant__ ClipParams<BATCH> p) {
   pdl_wait_for_previous();
   const float coef = p.hdr->coef;
   for (int64_t k = blockIdx.x; k < p.chunks; k += gridDim.x) {
@@ -233,6 +244,47 @@ int64_t chunks_of(const moe_grad_tensor &t) {
   return (bytes + (int64_t)kChunkGroups * kGroupBytes - 1) / ((int64_t)kChunkGroups * kGroupBytes);
 }
 
+template <int BATCH>
+cudaError_t launch_batches(const moe_grad_tensor *tensors, int num, float max_norm, float *norm,
+                           void *workspace, cudaStream_t stream) {
+  ClipParams<BATCH> p;
+  p.hdr = static_cast<ClipHeader *>(workspace);
+  p.partial = reinterpret_cast<double *>(static_cast<char *>(workspace) + sizeof(ClipHeader));
+  p.norm = norm;
+  p.max_norm = max_norm;
+  const int64_t most = (int64_t)device_sm_count() * 4;
+  const int64_t cap = most < kClipMaxBlocks ? most : kClipMaxBlocks;
+  const int batches = num > 0 ? (num + BATCH - 1) / BATCH : 1;
+  for (int k = 0; k < 2 * batches; ++k) {
+    // the scaling pass takes the batches backwards too
+    const bool scale = k >= batches;
+    const int at = (scale ? 2 * batches - 1 - k : k) * BATCH;
+    if (k != batches || batches > 1) {        // one batch: the norm's table serves both
+      const int n = num - at < BATCH ? num - at : BATCH;
+      p.chunks = 0;
+      p.num = 0;
+      for (int i = 0; i < BATCH / 32; ++i) p.f32[i] = 0;
+      for (int i = 0; i < n; ++i) {
+        const moe_grad_tensor &t = tensors[at + i];
+        if (t.numel == 0) continue;
+        p.t[p.num] = ClipTensor{t.grad, t.out, t.numel};
+        p.first[p.num] = p.chunks;
+        if (t.dtype == MOE_DTYPE_FP32) p.f32[p.num >> 5] |= 1u << (p.num & 31);
+        p.chunks += chunks_of(t);
+        ++p.num;
+      }
+    }
+    p.begin = k == 0;
+    p.end = k == batches - 1;
+    const int64_t grid = p.chunks < cap ? p.chunks : cap;
+    if (scale && grid == 0) continue;
+    const cudaError_t e = launch_after_previous(scale ? clip_scale_kernel<BATCH> : clip_norm_kernel<BATCH>,
+                                                (int)(grid < 1 ? 1 : grid), kClipThreads, p, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
 }  // namespace
 
 size_t clip_workspace_bytes() {
@@ -241,42 +293,9 @@ size_t clip_workspace_bytes() {
 
 cudaError_t launch_clip(const moe_grad_tensor *tensors, int num, float max_norm, float *norm,
                         void *workspace, cudaStream_t stream) {
-  ClipParams p;
-  p.hdr = static_cast<ClipHeader *>(workspace);
-  p.partial = reinterpret_cast<double *>(static_cast<char *>(workspace) + sizeof(ClipHeader));
-  p.norm = norm;
-  p.max_norm = max_norm;
-  const int64_t most = (int64_t)device_sm_count() * 4;
-  const int64_t cap = most < kClipMaxBlocks ? most : kClipMaxBlocks;
-  for (int pass = 0; pass < 2; ++pass) {
-    // the scaling pass takes the batches backwards too
-    const int batches = num > 0 ? (num + kClipBatch - 1) / kClipBatch : 1;
-    for (int b = 0; b < batches; ++b) {
-      const int at = (pass ? batches - 1 - b : b) * kClipBatch;
-      p.num = num - at < kClipBatch ? num - at : kClipBatch;
-      p.chunks = 0;
-      for (int i = 0; i < kClipBatch / 32; ++i) p.f32[i] = 0;
-      int used = 0;
-      for (int i = 0; i < p.num; ++i) {
-        const moe_grad_tensor &t = tensors[at + i];
-        if (t.numel == 0) continue;
-        p.t[used] = ClipTensor{t.grad, t.out, t.numel};
-        p.first[used] = p.chunks;
-        if (t.dtype == MOE_DTYPE_FP32) p.f32[used >> 5] |= 1u << (used & 31);
-        p.chunks += chunks_of(t);
-        ++used;
-      }
-      p.num = used;
-      p.begin = b == 0;
-      p.end = b == batches - 1;
-      const int64_t grid = p.chunks < cap ? p.chunks : cap;
-      if (pass && grid == 0) continue;
-      const cudaError_t e = launch_after_previous(pass ? clip_scale_kernel : clip_norm_kernel,
-                                                  (int)(grid < 1 ? 1 : grid), kClipThreads, p, stream);
-      if (e != cudaSuccess) return e;
-    }
-  }
-  return cudaSuccess;
+  // the table of tensors is copied with every launch: no larger than needed
+  if (num <= 32) return launch_batches<32>(tensors, num, max_norm, norm, workspace, stream);
+  return launch_batches<kClipBatch>(tensors, num, max_norm, norm, workspace, stream);
 }
 
 }  // namespace moe

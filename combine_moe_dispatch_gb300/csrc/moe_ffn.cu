@@ -44,34 +44,52 @@ namespace moe {
 
 namespace {
 
-enum Mode { kGateUp = 0, kDown = 1, kActGrad = 2, kInGrad = 3, kWeightGrad = 4 };
+// What one launch computes.  kRest: dx, dWgu and dWd, which need nothing of
+// one another, as one list of tiles.
+enum Kind { kGateUp = 0, kDown = 1, kActGrad = 2, kRest = 3 };
 
-constexpr int kPairThreads = 256;      // warps: 0 TMA, 1 MMA, 2 zeroes tails, 4-7 epilogue
+constexpr int kPairThreads = 256;      // warps: 0 TMA, 1 MMA, 2 zeroes tails, 3 scheduling, 4-7 epilogue
 constexpr int kStages = 6;
 constexpr int kBlockK = 64;            // one 128-byte swizzled line of bf16
 constexpr uint32_t kHalfBytes = 128 * kBlockK * 2;       // a CTA's half of one operand: 16 KB
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
 constexpr uint32_t kStagingBytes = 2 * 16384;            // epilogue, two buffers
 constexpr uint32_t kBarOff = kStages * kStageBytes + kStagingBytes;
-constexpr uint32_t kPairSmem = kBarOff + 256 + 1024;     // + alignment slack
+constexpr int kRing = 4;                                 // tiles announced ahead
+constexpr uint32_t kRingOff = kBarOff + 256;
+constexpr uint32_t kPairSmem = kRingOff + kRing * 64 + 1024;   // + alignment slack
 static_assert(kPairSmem <= 232448, "shared memory of one CTA");
 constexpr int kTileCols = 256;
 constexpr uint32_t kTmemCols = 512;                      // two accumulators of 256 columns
+// A contraction is cut into at most kMaxSplit parts, when the launch has at
+// most kMaxTickets tiles and the parts' sums at most kPartCols columns of 256.
+constexpr int kMaxSplit = 8;
+constexpr int kMaxTickets = 1024;
+constexpr int kPartCols = 16384;
 
-struct PairParams {
+struct Job {
   CUtensorMap a;
-  CUtensorMap b[4];        // row modes: boxes of 16, 32, 64 and 128 tokens
-  CUtensorMap out;         // weight modes: the gradient, stored by TMA
-  const int32_t *counts;   // [E], or null (cap rows each)
-  WsHeader *hdr;
-  uint16_t *o0, *o1;       // row modes: outputs (kGateUp: a, h or null; kActGrad: a, dh)
+  CUtensorMap b[4];        // row products: boxes of 16, 32, 64 and 128 tokens
+  CUtensorMap out;         // weight gradients: stored by TMA
+  uint16_t *o0, *o1;       // row products: outputs (kGateUp: a, h or null; kActGrad: a, dh)
   const uint16_t *h;       // kActGrad: kept gate | up
-  int E, cap;
-  int M, N, K;             // features; weight modes: output columns; row modes: contraction
-  int mt;                  // tiles of 256 accumulator rows (kGateUp: of 128 features)
+  int M, N, K;             // features; weight gradients: output columns; row products: contraction
+  int mt;                  // tiles of 256 accumulator rows (kGateUp: of 128 features); 0: no job
 };
 
-__device__ __forceinline__ int rows_of(const PairParams &p, int e) {
+template <int KIND>
+struct PairParams {
+  static constexpr int kJobs = KIND == kRest ? 3 : 1;
+  Job job[kJobs];          // kRest: dx, dWgu, dWd
+  const int32_t *counts;   // [E], or null (cap rows each)
+  WsHeader *hdr;
+  float *part;             // partial sums of split contractions
+  uint32_t *tickets;       // one per tile and CTA of the pair; zero between calls
+  int E, cap;
+};
+
+template <class P>
+__device__ __forceinline__ int rows_of(const P &p, int e) {
   if (!p.counts) return p.cap;
   const int c = __ldg(p.counts + e);
   return c < 0 ? 0 : (c > p.cap ? p.cap : c);
@@ -89,28 +107,39 @@ __device__ __forceinline__ int token_tiles(int rows) {
   return (rows + c - 1) / c;
 }
 
-struct Tile {
-  int e, rows;             // expert, its tokens
+struct alignas(16) Tile {
+  int valid;               // 0: no more work
+  int job, e, rows;        // product, expert, its tokens
   int m;                   // tile of 256 accumulator rows
   int n0, n;               // first column, columns of the matrix instruction
-  int cols;                // row modes: tokens in the tile
-  int nk;                  // blocks of 64 in the contraction (0: result is zero)
+  int cols;                // row products: tokens in the tile
+  int k0, nk;              // blocks of 64 of the contraction: [k0, k0 + nk); nk = 0: the result is 0
+  int split, part;         // parts of the tile's contraction, and which this is
+  int slot;                // split > 1: tile of the launch
+  int part_cols;           // and columns that each part's sums have room for
+  int reserved[2];
 };
+static_assert(sizeof(Tile) == 64, "a tile's record is 64 bytes");
 
-// Tile t of the launch, tiles ordered by expert; called by whole warps with
-// increasing t.  32 experts' tiles are counted at a time, one per lane.
-template <int MODE>
+// The launch's units of work in order: tiles of the row product by expert
+// (each `split` times, once per part of the contraction), then the weight
+// gradients' tiles.  Called by one whole warp with increasing unit.  32 experts'
+// tiles are counted at a time, one expert per lane.
+template <int KIND>
 struct Schedule {
-  const PairParams &p;
+  const PairParams<KIND> &p;
   int64_t base, incl;
   int e0, rows;
-  __device__ __forceinline__ explicit Schedule(const PairParams &p_) : p(p_), base(0), incl(0), e0(0), rows(0) {
-    if constexpr (MODE != kWeightGrad) count();
+  int split, part_cols;    // parts of a contraction, columns of a part's sums
+  __device__ __forceinline__ explicit Schedule(const PairParams<KIND> &p_)
+      : p(p_), base(0), incl(0), e0(0), rows(0), split(1), part_cols(0) {
+    count();
+    if constexpr (KIND != kRest) choose_split();
   }
   __device__ __forceinline__ void count() {
     const int lane = threadIdx.x & 31, e = e0 + lane;
     rows = e < p.E ? rows_of(p, e) : 0;
-    int64_t v = (int64_t)token_tiles(rows) * p.mt;
+    int64_t v = (int64_t)token_tiles(rows) * p.job[0].mt;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t o = __shfl_up_sync(0xFFFFFFFFu, v, d);
@@ -118,33 +147,59 @@ struct Schedule {
     }
     incl = base + v;
   }
-  __device__ __forceinline__ bool find(int64_t t, Tile &o) {
-    if constexpr (MODE == kWeightGrad) {
-      const int nt = (p.N + kTileCols - 1) / kTileCols;
-      const int64_t per = (int64_t)p.mt * nt;
-      if (t >= per * p.E) return false;
-      o.e = (int)(t / per);
-      const int r = (int)(t - o.e * per);
-      o.rows = rows_of(p, o.e);
-      o.m = r / nt;
-      o.n0 = (r - o.m * nt) * kTileCols;
-      o.n = min(kTileCols, (p.N - o.n0 + 31) & ~31);
-      o.cols = o.n;
-      o.nk = (o.rows + kBlockK - 1) / kBlockK;
-      return true;
-    } else {
+  // Few tiles for the SMs and a long contraction: cut it into parts.  The
+  // estimate is in blocks of 64: a unit costs its blocks and about kUnitCost
+  // more (filling the ring, the epilogue), a split tile the joining too.
+  __device__ __forceinline__ void choose_split() {
+    constexpr int kUnitCost = 6, kJoinCost = 8;
+    const int nk = (p.job[0].K + kBlockK - 1) / kBlockK;
+    const int pairs = gridDim.x >> 1;
+    if (nk < 16) return;
+    const int lane = threadIdx.x & 31;
+    int64_t tiles = 0;
+    int cols = 0;
+    for (int e = lane; e < p.E; e += 32) {
+      const int r = rows_of(p, e);
+      if (r == 0) continue;
+      tiles += (int64_t)token_tiles(r) * p.job[0].mt;
+      cols = max(cols, tile_cols(r));
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, d);
+      cols = max(cols, __shfl_xor_sync(0xFFFFFFFFu, cols, d));
+    }
+    if (tiles == 0 || tiles >= 4 * pairs || tiles > kMaxTickets) return;
+    part_cols = cols;
+    const int t = (int)tiles;
+    int best = (t + pairs - 1) / pairs * (nk + kUnitCost);
+    for (int s = 2; s <= kMaxSplit && s * 4 <= nk; ++s) {
+      if (t * s * cols > kPartCols) break;
+      const int cost = (t * s + pairs - 1) / pairs * ((nk + s - 1) / s + kUnitCost) + kJoinCost;
+      if (cost < best) {
+        best = cost;
+        split = s;
+      }
+    }
+  }
+  __device__ __forceinline__ bool find(int64_t unit, Tile &o) {
+    const int64_t t = split > 1 ? unit / split : unit;
     while (true) {
       const int64_t end = __shfl_sync(0xFFFFFFFFu, incl, 31);
       if (t < end) break;
       base = end;
+      if (e0 + 32 >= p.E) {
+        if constexpr (KIND == kRest) return find_weight(t - base, o);
+        else return false;
+      }
       e0 += 32;
-      if (e0 >= p.E) return false;
       count();
     }
     const unsigned after = __ballot_sync(0xFFFFFFFFu, incl > t);
     const int l = __ffs(after) - 1;
     const int64_t before = __shfl_sync(0xFFFFFFFFu, incl, l > 0 ? l - 1 : 0);
     const int r = (int)(t - (l > 0 ? before : base));
+    o.job = 0;
     o.e = e0 + l;
     o.rows = __shfl_sync(0xFFFFFFFFu, rows, l);
     const int c = tile_cols(o.rows), nt = (o.rows + c - 1) / c;
@@ -152,9 +207,45 @@ struct Schedule {
     o.n0 = (r - o.m * nt) * c;
     o.cols = min(c, o.rows - o.n0);
     o.n = (o.cols + 31) & ~31;
-    o.nk = (p.K + kBlockK - 1) / kBlockK;
-    return true;
+    const int nk = (p.job[0].K + kBlockK - 1) / kBlockK;
+    o.k0 = 0;
+    o.nk = nk;
+    o.split = split;
+    o.part = 0;
+    o.slot = 0;
+    o.part_cols = part_cols;
+    if (split > 1) {
+      o.slot = (int)t;
+      o.part = (int)(unit - t * split);
+      o.k0 = nk * o.part / split;
+      o.nk = nk * (o.part + 1) / split - o.k0;
     }
+    return true;
+  }
+  __device__ __forceinline__ bool find_weight(int64_t t, Tile &o) {
+    o.job = 1;
+    int nt = (p.job[1].N + kTileCols - 1) / kTileCols;
+    int64_t per = (int64_t)p.job[1].mt * nt;
+    if (t >= per * p.E) {
+      t -= per * p.E;
+      o.job = 2;
+      nt = (p.job[PairParams<KIND>::kJobs - 1].N + kTileCols - 1) / kTileCols;
+      per = (int64_t)p.job[PairParams<KIND>::kJobs - 1].mt * nt;
+      if (t >= per * p.E) return false;
+    }
+    const Job &j = p.job[PairParams<KIND>::kJobs == 1 ? 0 : o.job];
+    o.e = (int)(t / per);
+    const int r = (int)(t - o.e * per);
+    o.rows = rows_of(p, o.e);
+    o.m = r / nt;
+    o.n0 = (r - o.m * nt) * kTileCols;
+    o.n = min(kTileCols, (j.N - o.n0 + 31) & ~31);
+    o.cols = o.n;
+    o.k0 = 0;
+    o.nk = (o.rows + kBlockK - 1) / kBlockK;
+    o.split = 1;
+    o.part = o.slot = o.part_cols = 0;
+    return true;
   }
 };
 
@@ -173,6 +264,30 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t
   return false;
 }
 
+// A warp's view of the tiles that the scheduling warp announces.
+struct Feed {
+  const Tile *ring;
+  uint32_t full, empty;
+  uint64_t limit;
+  int s;
+  uint32_t ph;
+  __device__ __forceinline__ Feed(const Tile *ring_, uint32_t full_, uint32_t empty_, uint64_t limit_)
+      : ring(ring_), full(full_), empty(empty_), limit(limit_), s(0), ph(0) {}
+  // The next tile; false when there is none, or (ok false) when the wait ran out.
+  __device__ __forceinline__ bool next(Tile &t, bool &ok) {
+    ok = __all_sync(0xFFFFFFFFu, wait_bar(full + 8 * s, ph, limit));
+    if (!ok) return false;
+    t = ring[s];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive_local(empty + 8 * s);
+    if (++s == kRing) {
+      s = 0;
+      ph ^= 1u;
+    }
+    return t.valid != 0;
+  }
+};
+
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
@@ -188,14 +303,13 @@ __device__ __forceinline__ void unpack4(const uint2 &w, float (&v)[4]) {
 }
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
-template <int MODE>
+template <int KIND>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
-pair_kernel(const __grid_constant__ PairParams p) {
-  constexpr bool kAMn = MODE == kActGrad || MODE == kInGrad || MODE == kWeightGrad;
-  constexpr bool kBMn = MODE == kWeightGrad;
+pair_kernel(const __grid_constant__ PairParams<KIND> p) {
+  constexpr bool kAMn = KIND == kActGrad || KIND == kRest;
   // A stage is full after one arrival, the leader's, and the bytes of both
   // CTAs; a stage whose tail is zeroed, after each CTA's zeroing warp.
-  constexpr uint32_t kFullArrivals = MODE == kWeightGrad ? 2 : 1;
+  constexpr uint32_t kFullArrivals = KIND == kRest ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t *smem_p = smem_raw + (smem - smem_u32(smem_raw));
@@ -207,6 +321,10 @@ pair_kernel(const __grid_constant__ PairParams p) {
   const uint32_t full = bars, empty = bars + 8 * kStages, tail = bars + 16 * kStages;
   const uint32_t tm_full = bars + 24 * kStages, tm_empty = tm_full + 16;
   const uint32_t tm_slot = tm_empty + 16;
+  // barriers of the ring of tiles
+  const uint32_t rec_full = bars + 192, rec_empty = bars + 224;
+  Tile *ring = reinterpret_cast<Tile *>(smem_p + kRingOff);
+  volatile uint32_t *last_in = reinterpret_cast<uint32_t *>(smem_p + kBarOff + 24 * kStages + 40);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -218,9 +336,15 @@ pair_kernel(const __grid_constant__ PairParams p) {
       tc::mbar_init_at(tm_full + 8 * b, 1);
       tc::mbar_init_at(tm_empty + 8 * b, 8);   // four epilogue warps in each CTA
     }
+    for (int r = 0; r < kRing; ++r) {
+      tc::mbar_init_at(rec_full + 8 * r, 1);
+      // TMA, epilogue, and where they run the MMA and the zeroing warp
+      tc::mbar_init_at(rec_empty + 8 * r, 5 + (rank == 0 ? 1 : 0) + (KIND == kRest ? 1 : 0));
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    tc::prefetch_map(&p.a);
-    tc::prefetch_map(&p.b[0]);
+  } else if (threadIdx.x == 32 && p.job[0].mt > 0) {
+    tc::prefetch_map(&p.job[0].a);
+    tc::prefetch_map(&p.job[0].b[0]);
   }
   if (warp == 2) tc::tmem_alloc_pair(tm_slot, kTmemCols);
   tc::fence_before();
@@ -233,67 +357,88 @@ pair_kernel(const __grid_constant__ PairParams p) {
   pdl_wait_for_previous();
   // The status is read once, by every thread alike: after a plan error no
   // tile is computed and nothing is written.
-  const bool live = read_status(p.hdr) == MOE_OK;
   const uint64_t tmo = p.hdr->timeout_ns;
+  const bool live = read_status(p.hdr) == MOE_OK;
   const uint64_t limit = tmo ? tmo : kDefaultTimeoutNs;
-  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   bool ok = true;
+  Tile t;
+  Feed feed(ring, rec_full, rec_empty, limit);
 
-  if (live && warp == 0) {
+  if (live && warp == 3) {
+    // ---- scheduling: one warp finds the pair's tiles, up to kRing ahead
+    Schedule<KIND> sched(p);
+    int s = 0;
+    uint32_t ph = 0;
+    for (int64_t i = blockIdx.x >> 1; ok; i += gridDim.x >> 1) {
+      t.valid = sched.find(i, t);
+      ok = __all_sync(0xFFFFFFFFu, wait_bar(rec_empty + 8 * s, ph ^ 1u, limit));
+      if (ok && lane == 0) {
+        ring[s] = t;
+        tc::mbar_arrive_local(rec_full + 8 * s);
+      }
+      if (!t.valid) break;
+      if (++s == kRing) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+  } else if (live && warp == 0) {
     // ---- TMA: both CTAs load their halves; bytes complete on the leader's barrier
-    Schedule<MODE> sched(p);
-    Tile t;
     int s = 0;
     uint32_t ph = 0;
     const uint32_t full0 = tc::map_rank(full, 0);
-    for (int64_t i = pair; ok && sched.find(i, t); i += pairs) {
+    while (ok && feed.next(t, ok)) {
       if (lane == 0) {
+        const Job &j = p.job[KIND == kRest ? t.job : 0];
+        const bool weight = KIND == kRest && t.job > 0;
         const uint32_t half_n = t.n >> 1;
         const int bsel = half_n <= 16 ? 0 : half_n <= 32 ? 1 : half_n <= 64 ? 2 : 3;
-        const uint32_t bytes = kHalfBytes + (kBMn ? kHalfBytes : (16u << bsel) * 128u);
-        const int tail_rows = MODE == kWeightGrad ? (t.rows & (kBlockK - 1)) : 0;
+        const uint32_t bytes = kHalfBytes + (weight ? kHalfBytes : (16u << bsel) * 128u);
+        const int tail_rows = weight ? (t.rows & (kBlockK - 1)) : 0;
         for (int kb = 0; kb < t.nk; ++kb) {
           if (!wait_bar(empty + 8 * s, ph ^ 1u, limit)) {
             ok = false;
             break;
           }
           const uint32_t sa = smem + s * kStageBytes, sb = sa + kHalfBytes;
-          const int k0 = kb * kBlockK;
-          if (MODE == kWeightGrad) {
+          const int k0 = (t.k0 + kb) * kBlockK;
+          const uint32_t bar = full0 + 8 * s;
+          if (weight) {
             const int m0 = t.m * 256 + rank * 128, n0 = t.n0 + rank * half_n;
             if (tail_rows != 0 && kb == t.nk - 1) {
-              const uint32_t bar = tail + 8 * s;
-              tc::mbar_expect_local(bar, bytes);
-              tc::tma_load_own(sa, &p.a, bar, m0, k0, 0, t.e);
-              tc::tma_load_own(sa + 8192, &p.a, bar, m0 + 64, k0, 0, t.e);
-              tc::tma_load_own(sb, &p.b[0], bar, n0, k0, 0, t.e);
-              tc::tma_load_own(sb + 8192, &p.b[0], bar, n0 + 64, k0, 0, t.e);
+              const uint32_t own = tail + 8 * s;
+              tc::mbar_expect_local(own, bytes);
+              tc::tma_load_own(sa, &j.a, own, m0, k0, 0, t.e);
+              tc::tma_load_own(sa + 8192, &j.a, own, m0 + 64, k0, 0, t.e);
+              tc::tma_load_own(sb, &j.b[0], own, n0, k0, 0, t.e);
+              tc::tma_load_own(sb + 8192, &j.b[0], own, n0 + 64, k0, 0, t.e);
             } else {
-              const uint32_t bar = full0 + 8 * s;
               if (rank == 0) {
                 tc::mbar_expect_local(full + 8 * s, 2 * bytes);
                 tc::mbar_arrive_local(full + 8 * s);
               }
-              tc::tma_load_pair(sa, &p.a, bar, m0, k0, 0, t.e);
-              tc::tma_load_pair(sa + 8192, &p.a, bar, m0 + 64, k0, 0, t.e);
-              tc::tma_load_pair(sb, &p.b[0], bar, n0, k0, 0, t.e);
-              tc::tma_load_pair(sb + 8192, &p.b[0], bar, n0 + 64, k0, 0, t.e);
+              tc::tma_load_pair(sa, &j.a, bar, m0, k0, 0, t.e);
+              tc::tma_load_pair(sa + 8192, &j.a, bar, m0 + 64, k0, 0, t.e);
+              tc::tma_load_pair(sb, &j.b[0], bar, n0, k0, 0, t.e);
+              tc::tma_load_pair(sb + 8192, &j.b[0], bar, n0 + 64, k0, 0, t.e);
             }
           } else {
-            const uint32_t bar = full0 + 8 * s;
-            if (rank == 0) tc::mbar_expect_local(full + 8 * s, 2 * bytes);
-            if (MODE == kGateUp) {             // 64 gate rows, then the same 64 features of up
+            if (rank == 0) {
+              tc::mbar_expect_local(full + 8 * s, 2 * bytes);
+              if (kFullArrivals == 2) tc::mbar_arrive_local(full + 8 * s);
+            }
+            if (KIND == kGateUp) {             // 64 gate rows, then the same 64 features of up
               const int f0 = t.m * 128 + rank * 64;
-              tc::tma_load_pair(sa, &p.a, bar, k0, f0, 0, t.e);
-              tc::tma_load_pair(sa + 8192, &p.a, bar, k0, f0, 1, t.e);
+              tc::tma_load_pair(sa, &j.a, bar, k0, f0, 0, t.e);
+              tc::tma_load_pair(sa + 8192, &j.a, bar, k0, f0, 1, t.e);
             } else if (kAMn) {
               const int m0 = t.m * 256 + rank * 128;
-              tc::tma_load_pair(sa, &p.a, bar, m0, k0, 0, t.e);
-              tc::tma_load_pair(sa + 8192, &p.a, bar, m0 + 64, k0, 0, t.e);
+              tc::tma_load_pair(sa, &j.a, bar, m0, k0, 0, t.e);
+              tc::tma_load_pair(sa + 8192, &j.a, bar, m0 + 64, k0, 0, t.e);
             } else {
-              tc::tma_load_pair(sa, &p.a, bar, k0, t.m * 256 + rank * 128, 0, t.e);
+              tc::tma_load_pair(sa, &j.a, bar, k0, t.m * 256 + rank * 128, 0, t.e);
             }
-            tc::tma_load_pair(sb, &p.b[bsel], bar, k0, t.n0 + rank * half_n, 0, t.e);
+            tc::tma_load_pair(sb, &j.b[bsel], bar, k0, t.n0 + rank * half_n, 0, t.e);
           }
           if (++s == kStages) {
             s = 0;
@@ -315,16 +460,16 @@ pair_kernel(const __grid_constant__ PairParams p) {
     ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
   } else if (live && warp == 1 && rank == 0) {
     // ---- matrix instructions, one thread of the leading CTA
-    Schedule<MODE> sched(p);
-    Tile t;
     int s = 0;
     uint32_t ph = 0, it = 0;
-    for (int64_t i = pair; ok && sched.find(i, t); i += pairs) {
+    while (ok && feed.next(t, ok)) {
       if (t.nk == 0) continue;
       if (lane == 0) {
+        const bool bmn = KIND == kRest && t.job > 0;
         const uint32_t buf = it & 1u;
         const uint32_t d = tmem + buf * kTileCols;
-        const uint32_t idesc = tc::instr_desc(256, t.n, kAMn, kBMn);
+        const uint32_t idesc = tc::instr_desc(256, t.n, kAMn, bmn);
+        const uint32_t blead = bmn ? 8192u : 16u, bstep = bmn ? 128u : 2u;
         ok = wait_bar(tm_empty + 8 * buf, ((it >> 1) & 1u) ^ 1u, limit);
         tc::fence_after();
         for (int kb = 0; ok && kb < t.nk; ++kb) {
@@ -333,16 +478,15 @@ pair_kernel(const __grid_constant__ PairParams p) {
             break;
           }
           // zeroed by ordinary stores in either CTA: acquire those too
-          if (MODE == kWeightGrad && kb == t.nk - 1) tc::mbar_try_cluster(full + 8 * s, ph);
+          if (KIND == kRest && bmn && kb == t.nk - 1) tc::mbar_try_cluster(full + 8 * s, ph);
           tc::fence_after();
           const uint32_t sa = smem + s * kStageBytes, sb = sa + kHalfBytes;
           const uint64_t da = tc::smem_desc(sa, kAMn ? 8192u : 16u);
-          const uint64_t db = tc::smem_desc(sb, kBMn ? 8192u : 16u);
+          const uint64_t db = tc::smem_desc(sb, blead);
 #pragma unroll
           for (int k = 0; k < kBlockK / 16; ++k)
             // 16 k on: 32 bytes of a K-major line, 16 lines (2048 bytes) MN-major
-            tc::mma_pair(d, da + (kAMn ? k * 128 : k * 2), db + (kBMn ? k * 128 : k * 2), idesc,
-                         kb > 0 || k > 0);
+            tc::mma_pair(d, da + (kAMn ? k * 128 : k * 2), db + k * bstep, idesc, kb > 0 || k > 0);
           tc::mma_commit_pair(empty + 8 * s);
           if (++s == kStages) {
             s = 0;
@@ -354,18 +498,16 @@ pair_kernel(const __grid_constant__ PairParams p) {
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       ++it;
     }
-  } else if (live && warp == 2 && MODE == kWeightGrad) {
+  } else if (live && warp == 2 && KIND == kRest) {
     // ---- zero the rows past the expert's count in its last block
-    Schedule<MODE> sched(p);
-    Tile t;
     int s = 0;
     uint32_t phases = 0;
     const uint32_t full0 = tc::map_rank(full, 0);
-    for (int64_t i = pair; ok && sched.find(i, t); i += pairs) {
+    while (ok && feed.next(t, ok)) {
       if (t.nk == 0) continue;
       const int last = (s + t.nk - 1) % kStages;
       s = (s + t.nk) % kStages;
-      const int valid = t.rows & (kBlockK - 1);
+      const int valid = t.job > 0 ? (t.rows & (kBlockK - 1)) : 0;
       if (valid == 0) continue;
       ok = wait_bar(tail + 8 * last, (phases >> last) & 1u, limit);
       ok = __all_sync(0xFFFFFFFFu, ok);
@@ -381,25 +523,26 @@ pair_kernel(const __grid_constant__ PairParams p) {
     }
   } else if (live && warp >= 4) {
     // ---- epilogue: tensor memory -> registers -> shared memory -> results
-    Schedule<MODE> sched(p);
-    Tile t;
     uint32_t it = 0, chunk = 0;
     const int wq = warp - 4, tid = threadIdx.x - 128;
     const uint32_t empty0 = tc::map_rank(tm_empty, 0);
-    for (int64_t i = pair; ok && sched.find(i, t); i += pairs) {
+    while (true) {
+      const bool more = feed.next(t, ok);
       const uint32_t buf = it & 1u;
-      if (t.nk > 0) {
+      if (more && t.nk > 0) {
         ok = wait_bar(tm_full + 8 * buf, (it >> 1) & 1u, limit);
         tc::fence_after();
       }
-      // all four warps agree to go on
+      // all four warps agree to go on, and are done with the staging buffers
       ok = named_sync_and(1, 128, ok);
-      if (!ok) break;
+      if (!ok || !more) break;
+      const Job &j = p.job[KIND == kRest ? t.job : 0];
       const uint32_t src = tmem + ((uint32_t)(wq * 32) << 16) + buf * kTileCols;
-      if (MODE == kWeightGrad) {
-        const int row = wq * 32 + lane;
+      if (KIND == kRest && t.job > 0) {
+        // each warp on its own: 32 rows x 64 columns of bf16, swizzled, stored by TMA
+        const int m0 = t.m * 256 + (int)rank * 128 + wq * 32;
         for (int c = 0; c < t.n; c += 64, ++chunk) {
-          const uint32_t dst = (chunk & 1u) * 16384u;
+          const uint32_t dst = wq * 8192u + (chunk & 1u) * 4096u;
           uint32_t v[32], w[32];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
@@ -408,11 +551,11 @@ pair_kernel(const __grid_constant__ PairParams p) {
               tc::tmem_ld_wait();
             } else {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = 0u;
+              for (int q = 0; q < 32; ++q) v[q] = 0u;
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              w[hf * 16 + j] = pack2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            for (int q = 0; q < 16; ++q)
+              w[hf * 16 + q] = pack2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
           }
           if (t.nk > 0 && c + 64 >= t.n) {
             tc::fence_before();
@@ -420,50 +563,94 @@ pair_kernel(const __grid_constant__ PairParams p) {
             if (lane == 0) tc::mbar_arrive_remote(empty0 + 8 * buf);
           }
           // the store of two chunks ago has read its buffer
-          if (tid == 0) tc::store_wait_read<1>();
-          named_sync(1, 128);
-          uint8_t *q = smem_p + kStages * kStageBytes + dst + row * 128;
+          if (lane == 0) tc::store_wait_read<1>();
+          __syncwarp();
+          uint8_t *q = smem_p + kStages * kStageBytes + dst + lane * 128;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4 *>(q + ((j ^ (row & 7)) * 16)) =
-                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4 *>(q + ((k ^ (lane & 7)) * 16)) =
+                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
           tc::fence_async_smem();
-          named_sync(1, 128);
-          const int m0 = t.m * 256 + (int)rank * 128;
-          if (tid == 0 && m0 < p.M && t.n0 + c < p.N) {
-            tc::tma_store(&p.out, staging + dst, t.n0 + c, m0, 0, t.e);
+          __syncwarp();
+          if (lane == 0) {
+            if (m0 < j.M && t.n0 + c < j.N) tc::tma_store(&j.out, staging + dst, t.n0 + c, m0, 0, t.e);
+            tc::store_commit();
           }
-          if (tid == 0) tc::store_commit();
         }
       } else {
         const int i4 = tid & 15, r8 = tid >> 4;
-        const int f0 = MODE == kGateUp ? t.m * 128 + (int)rank * 64 + 4 * i4
+        const int f0 = KIND == kGateUp ? t.m * 128 + (int)rank * 64 + 4 * i4
                                        : t.m * 256 + (int)rank * 128 + 4 * i4;
         const int64_t row0 = (int64_t)t.e * p.cap + t.n0;
+        // A part of a split contraction leaves its sums in the workspace
+        // ([tile][part][CTA][column][128 features]); the last part to finish
+        // adds all of them, in the order of the parts.
+        const bool split = KIND != kRest && t.split > 1;
+        float *part = nullptr;
+        if (split) {
+          part = p.part + (t.slot * t.split * 2 + (int)rank) * ((int64_t)t.part_cols * 128);
+          float *own = part + (int64_t)t.part * 2 * t.part_cols * 128;
+          for (int c = 0; c < t.n; c += 32) {
+            uint32_t v[32];
+            tc::tmem_ld32(v, src + c);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              __stcg(own + (int64_t)(c + q) * 128 + wq * 32 + lane, __uint_as_float(v[q]));
+          }
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_remote(empty0 + 8 * buf);
+          ++it;
+          __threadfence();
+          named_sync(1, 128);
+          if (tid == 0) {
+            uint32_t *ticket = p.tickets + t.slot * 2 + rank;
+            const bool last = atomicAdd(ticket, 1u) == (uint32_t)t.split - 1;
+            if (last) *ticket = 0;
+            *last_in = last;
+            __threadfence();
+          }
+          named_sync(1, 128);
+          const bool last = *last_in != 0;
+          named_sync(1, 128);
+          if (!last) continue;
+          __threadfence();
+        }
         for (int c = 0; c < t.n; c += 32, ++chunk) {
           uint2 g[4][2], u[4][2];
-          if (MODE == kActGrad) {
+          if (KIND == kActGrad) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf)
-                if (c + r * 8 + r8 < t.cols && f0 + 64 * hf < p.M) {
-                  const uint16_t *q = p.h + (row0 + c + r * 8 + r8) * 2 * p.M + f0 + 64 * hf;
+                if (c + r * 8 + r8 < t.cols && f0 + 64 * hf < j.M) {
+                  const uint16_t *q = j.h + (row0 + c + r * 8 + r8) * 2 * j.M + f0 + 64 * hf;
                   g[r][hf] = *reinterpret_cast<const uint2 *>(q);
-                  u[r][hf] = *reinterpret_cast<const uint2 *>(q + p.M);
+                  u[r][hf] = *reinterpret_cast<const uint2 *>(q + j.M);
                 }
           }
           uint32_t v[32];
-          tc::tmem_ld32(v, src + c);
-          tc::tmem_ld_wait();
-          if (c + 32 >= t.n) {
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_remote(empty0 + 8 * buf);
+          if (!split) {
+            tc::tmem_ld32(v, src + c);
+            tc::tmem_ld_wait();
+            if (c + 32 >= t.n) {
+              tc::fence_before();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive_remote(empty0 + 8 * buf);
+            }
+          } else {
+            const float *q0 = part + (int64_t)c * 128 + wq * 32 + lane;
+#pragma unroll
+            for (int q = 0; q < 32; ++q) v[q] = 0u;
+            for (int s = 0; s < t.split; ++s, q0 += (int64_t)2 * t.part_cols * 128)
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                v[q] = __float_as_uint(__uint_as_float(v[q]) + __ldcg(q0 + q * 128));
           }
           float *st = reinterpret_cast<float *>(smem_p + kStages * kStageBytes + (chunk & 1u) * 16384u);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) st[j * 128 + wq * 32 + lane] = __uint_as_float(v[j]);
+          for (int q = 0; q < 32; ++q) st[q * 128 + wq * 32 + lane] = __uint_as_float(v[q]);
           named_sync(1, 128);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -473,47 +660,48 @@ pair_kernel(const __grid_constant__ PairParams p) {
             const float4 hi4 = *reinterpret_cast<const float4 *>(st + tok * 128 + 64 + 4 * i4);
             const float lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
             const int64_t row = row0 + c + tok;
-            if (MODE == kGateUp) {
-              if (f0 < p.M) {
+            if (KIND == kGateUp) {
+              if (f0 < j.M) {
                 float a[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) a[j] = lo[j] * sigmoid(lo[j]) * hi[j];
-                *reinterpret_cast<uint2 *>(p.o0 + row * p.M + f0) = pack4(a);
-                if (p.o1) {
-                  *reinterpret_cast<uint2 *>(p.o1 + row * 2 * p.M + f0) = pack4(lo);
-                  *reinterpret_cast<uint2 *>(p.o1 + row * 2 * p.M + p.M + f0) = pack4(hi);
+                for (int k = 0; k < 4; ++k) a[k] = lo[k] * sigmoid(lo[k]) * hi[k];
+                *reinterpret_cast<uint2 *>(j.o0 + row * j.M + f0) = pack4(a);
+                if (j.o1) {
+                  *reinterpret_cast<uint2 *>(j.o1 + row * 2 * j.M + f0) = pack4(lo);
+                  *reinterpret_cast<uint2 *>(j.o1 + row * 2 * j.M + j.M + f0) = pack4(hi);
                 }
               }
-            } else if (MODE == kActGrad) {
+            } else if (KIND == kActGrad) {
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf)
-                if (f0 + 64 * hf < p.M) {
+                if (f0 + 64 * hf < j.M) {
                   float gv[4], uv[4], a[4], dg[4], du[4];
                   unpack4(g[r][hf], gv);
                   unpack4(u[r][hf], uv);
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const float da = hf ? hi[j] : lo[j];
-                    const float sg = sigmoid(gv[j]), silu = gv[j] * sg;
-                    a[j] = silu * uv[j];
-                    du[j] = da * silu;
-                    dg[j] = da * uv[j] * (sg + silu * (1.0f - sg));
+                  for (int k = 0; k < 4; ++k) {
+                    const float da = hf ? hi[k] : lo[k];
+                    const float sg = sigmoid(gv[k]), silu = gv[k] * sg;
+                    a[k] = silu * uv[k];
+                    du[k] = da * silu;
+                    dg[k] = da * uv[k] * (sg + silu * (1.0f - sg));
                   }
-                  *reinterpret_cast<uint2 *>(p.o0 + row * p.M + f0 + 64 * hf) = pack4(a);
-                  uint16_t *q = p.o1 + row * 2 * p.M + f0 + 64 * hf;
+                  *reinterpret_cast<uint2 *>(j.o0 + row * j.M + f0 + 64 * hf) = pack4(a);
+                  uint16_t *q = j.o1 + row * 2 * j.M + f0 + 64 * hf;
                   *reinterpret_cast<uint2 *>(q) = pack4(dg);
-                  *reinterpret_cast<uint2 *>(q + p.M) = pack4(du);
+                  *reinterpret_cast<uint2 *>(q + j.M) = pack4(du);
                 }
             } else {
-              if (f0 < p.M) *reinterpret_cast<uint2 *>(p.o0 + row * p.M + f0) = pack4(lo);
-              if (f0 + 64 < p.M) *reinterpret_cast<uint2 *>(p.o0 + row * p.M + f0 + 64) = pack4(hi);
+              if (f0 < j.M) *reinterpret_cast<uint2 *>(j.o0 + row * j.M + f0) = pack4(lo);
+              if (f0 + 64 < j.M) *reinterpret_cast<uint2 *>(j.o0 + row * j.M + f0 + 64) = pack4(hi);
             }
           }
         }
+        if (split) continue;        // counted above
       }
       if (t.nk > 0) ++it;
     }
-    if (MODE == kWeightGrad && tid == 0) tc::store_wait_all();
+    if (KIND == kRest && lane == 0) tc::store_wait_all();
   }
 
   if (!ok) {
@@ -565,14 +753,14 @@ bool make_map(CUtensorMap *m, const void *base, int64_t d0, int64_t d1, int64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE>
-cudaError_t launch_pair(const PairParams &p, int64_t tiles, cudaStream_t stream) {
+template <int KIND>
+cudaError_t launch_pair(const PairParams<KIND> &p, int64_t tiles, cudaStream_t stream) {
   static std::once_flag once[64];
   int dev = 0;
   cudaGetDevice(&dev);
   cudaError_t attr = cudaSuccess;
   std::call_once(once[dev & 63], [&] {
-    attr = cudaFuncSetAttribute(pair_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    attr = cudaFuncSetAttribute(pair_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)kPairSmem);
   });
   if (attr != cudaSuccess) return attr;
@@ -587,93 +775,118 @@ cudaError_t launch_pair(const PairParams &p, int64_t tiles, cudaStream_t stream)
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, pair_kernel<MODE>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, pair_kernel<KIND>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-PairParams base_params(const FfnParams &f) {
-  PairParams p = {};
+template <int KIND>
+PairParams<KIND> base_params(const FfnParams &f) {
+  PairParams<KIND> p = {};
   p.counts = f.counts;
   p.hdr = f.hdr;
+  p.part = f.part;
+  p.tickets = f.tickets;
   p.E = f.E;
   p.cap = f.cap;
   return p;
 }
 
-bool token_maps(PairParams &p, const void *rows, int64_t width) {
-  for (int i = 0; i < 4; ++i)
-    if (!make_map(&p.b[i], rows, width, p.cap, 1, p.E, 16 << i)) return false;
+// Boxes of the tokens' operand: those that tiles of at most cap tokens use.
+bool token_maps(Job &j, const void *rows, int64_t width, int64_t cap, int64_t E) {
+  for (int i = 0; i < 4; ++i) {
+    if (!make_map(&j.b[i], rows, width, cap, 1, E, 16 << i)) return false;
+    if (cap <= (32 << i)) break;
+  }
   return true;
+}
+
+// Units of a row product: its most tiles, each in up to kMaxSplit parts.
+int64_t units(const Job &j, const FfnParams &f) {
+  const int64_t nk = cdiv(j.K, kBlockK);
+  return j.mt * f.E * cdiv(f.cap, kTileCols) * (nk < 16 ? 1 : kMaxSplit);
 }
 
 }  // namespace
 
+size_t ffn_scratch_bytes(int64_t E, int64_t cap, int64_t H, int64_t I) {
+  const int64_t mt = cdiv(I, 128) > cdiv(H, 256) ? cdiv(I, 128) : cdiv(H, 256);
+  const int64_t most = mt * E * cdiv(cap, kTileCols) * kMaxSplit;
+  const int64_t cols = cap < kTileCols ? (cap + 31) / 32 * 32 : kTileCols;
+  const int64_t part_cols = most < kPartCols / cols ? most * cols : kPartCols;
+  return kTicketBytes + (size_t)part_cols * 256 * sizeof(float);
+}
+
 cudaError_t launch_ffn(const FfnParams &f, cudaStream_t stream) {
-  const int64_t nt = f.E * cdiv(f.cap, kTileCols);      // most token tiles
-  PairParams p = base_params(f);
-  if (!make_map(&p.a, f.w_gate_up, f.H, f.I, 2, f.E, 64) || !token_maps(p, f.x, f.H))
+  {
+    PairParams<kGateUp> p = base_params<kGateUp>(f);
+    Job &j = p.job[0];
+    if (!make_map(&j.a, f.w_gate_up, f.H, f.I, 2, f.E, 64) || !token_maps(j, f.x, f.H, f.cap, f.E))
+      return cudaErrorInvalidValue;
+    j.o0 = f.act;
+    j.o1 = f.h;
+    j.M = f.I;
+    j.K = f.H;
+    j.mt = (int)cdiv(f.I, 128);
+    const cudaError_t e = launch_pair<kGateUp>(p, units(j, f), stream);
+    if (e != cudaSuccess) return e;
+  }
+  PairParams<kDown> p = base_params<kDown>(f);
+  Job &j = p.job[0];
+  if (!make_map(&j.a, f.w_down, f.I, f.H, 1, f.E, 128) || !token_maps(j, f.act, f.I, f.cap, f.E))
     return cudaErrorInvalidValue;
-  p.o0 = f.act;
-  p.o1 = f.h;
-  p.M = f.I;
-  p.K = f.H;
-  p.mt = (int)cdiv(f.I, 128);
-  cudaError_t e = launch_pair<kGateUp>(p, p.mt * nt, stream);
-  if (e != cudaSuccess) return e;
-  p = base_params(f);
-  if (!make_map(&p.a, f.w_down, f.I, f.H, 1, f.E, 128) || !token_maps(p, f.act, f.I))
-    return cudaErrorInvalidValue;
-  p.o0 = f.y;
-  p.M = f.H;
-  p.K = f.I;
-  p.mt = (int)cdiv(f.H, 256);
-  return launch_pair<kDown>(p, p.mt * nt, stream);
+  j.o0 = f.y;
+  j.M = f.H;
+  j.K = f.I;
+  j.mt = (int)cdiv(f.H, 256);
+  return launch_pair<kDown>(p, units(j, f), stream);
 }
 
 cudaError_t launch_ffn_backward(const FfnParams &f, cudaStream_t stream) {
-  const int64_t nt = f.E * cdiv(f.cap, kTileCols);
   const int64_t I2 = 2 * (int64_t)f.I;
-  // dh and a
-  PairParams p = base_params(f);
-  if (!make_map(&p.a, f.w_down, f.I, f.H, 1, f.E, 64) || !token_maps(p, f.dy, f.H))
-    return cudaErrorInvalidValue;
-  p.o0 = f.act;
-  p.o1 = f.dh;
-  p.h = f.h;
-  p.M = f.I;
-  p.K = f.H;
-  p.mt = (int)cdiv(f.I, 256);
-  cudaError_t e = launch_pair<kActGrad>(p, p.mt * nt, stream);
-  if (e != cudaSuccess) return e;
-  if (f.dx) {
-    p = base_params(f);
-    if (!make_map(&p.a, f.w_gate_up, f.H, I2, 1, f.E, 64) || !token_maps(p, f.dh, I2))
+  {
+    PairParams<kActGrad> p = base_params<kActGrad>(f);       // dh and a
+    Job &j = p.job[0];
+    if (!make_map(&j.a, f.w_down, f.I, f.H, 1, f.E, 64) || !token_maps(j, f.dy, f.H, f.cap, f.E))
       return cudaErrorInvalidValue;
-    p.o0 = f.dx;
-    p.M = f.H;
-    p.K = (int)I2;
-    p.mt = (int)cdiv(f.H, 256);
-    e = launch_pair<kInGrad>(p, p.mt * nt, stream);
+    j.o0 = f.act;
+    j.o1 = f.dh;
+    j.h = f.h;
+    j.M = f.I;
+    j.K = f.H;
+    j.mt = (int)cdiv(f.I, 256);
+    const cudaError_t e = launch_pair<kActGrad>(p, units(j, f), stream);
     if (e != cudaSuccess) return e;
+  }
+  // dx first: its tiles have the longest contraction
+  PairParams<kRest> p = base_params<kRest>(f);
+  int64_t tiles = 0;
+  if (f.dx) {
+    Job &j = p.job[0];
+    if (!make_map(&j.a, f.w_gate_up, f.H, I2, 1, f.E, 64) || !token_maps(j, f.dh, I2, f.cap, f.E))
+      return cudaErrorInvalidValue;
+    j.o0 = f.dx;
+    j.M = f.H;
+    j.K = (int)I2;
+    j.mt = (int)cdiv(f.H, 256);
+    tiles += j.mt * f.E * cdiv(f.cap, kTileCols);
   }
   for (int w = 0; w < 2; ++w) {
     uint16_t *out = w ? f.dw_down : f.dw_gate_up;
     if (!out) continue;
+    Job &j = p.job[1 + w];
     const int64_t M = w ? f.H : I2, N = w ? f.I : f.H;
-    p = base_params(f);
-    if (!make_map(&p.a, w ? (const void *)f.dy : f.dh, M, f.cap, 1, f.E, 64) ||
-        !make_map(&p.b[0], w ? (const void *)f.act : f.x, N, f.cap, 1, f.E, 64) ||
-        !make_map(&p.out, out, N, M, 1, f.E, 128))
+    if (!make_map(&j.a, w ? (const void *)f.dy : f.dh, M, f.cap, 1, f.E, 64) ||
+        !make_map(&j.b[0], w ? (const void *)f.act : f.x, N, f.cap, 1, f.E, 64) ||
+        !make_map(&j.out, out, N, M, 1, f.E, 32))
       return cudaErrorInvalidValue;
-    p.M = (int)M;
-    p.N = (int)N;
-    p.mt = (int)cdiv(M, 256);
-    e = launch_pair<kWeightGrad>(p, p.mt * cdiv(N, kTileCols) * f.E, stream);
-    if (e != cudaSuccess) return e;
+    j.M = (int)M;
+    j.N = (int)N;
+    j.mt = (int)cdiv(M, 256);
+    tiles += j.mt * cdiv(N, kTileCols) * f.E;
   }
-  return cudaSuccess;
+  return tiles > 0 ? launch_pair<kRest>(p, tiles, stream) : cudaSuccess;
 }
 
 }  // namespace moe

@@ -11,6 +11,8 @@ namespace moe {
 struct FfnParams {
   const int32_t *counts;         // [E] rows per expert, or null (cap each)
   WsHeader *hdr;
+  float *part;                   // scratch of ffn_scratch_bytes(): tickets, then partial sums
+  uint32_t *tickets;
   int E, cap, H, I;
   const uint16_t *x;             // [E, cap, H]
   const uint16_t *w_gate_up;     // [E, 2I, H]
@@ -24,6 +26,11 @@ struct FfnParams {
   uint16_t *dw_gate_up;          // [E, 2I, H]
   uint16_t *dw_down;             // [E, H, I]
 };
+
+// Scratch past the plan's workspace: kTicketBytes of tickets, zero between
+// calls, then the partial sums of split contractions.
+constexpr size_t kTicketBytes = 8192;
+size_t ffn_scratch_bytes(int64_t E, int64_t cap, int64_t H, int64_t I);
 
 cudaError_t launch_ffn(const FfnParams &p, cudaStream_t stream);
 cudaError_t launch_ffn_backward(const FfnParams &p, cudaStream_t stream);

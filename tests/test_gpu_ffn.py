@@ -26,7 +26,8 @@ D = torch.float64
 # empty expert, one row, a full one; more rows than one tile of 256 columns,
 # just over it, and a multiple of 64; sizes that are multiples of 8 alone;
 # more experts than a warp has lanes, most of them empty; counts below zero
-# and above cap are clamped.
+# and above cap are clamped; few tiles and contractions over 1024 and more,
+# which are cut into parts.
 SHAPES = [
     (1, 1, 8, 8, [1]),
     (3, 5, 264, 136, [0, 5, 1]),
@@ -37,6 +38,8 @@ SHAPES = [
     (3, 40, 256, 264, [-5, 99, 17]),
     (70, 2, 64, 64, [1, 0, 2] * 23 + [1]),
     (2, 130, 2056, 520, [130, 65]),
+    (3, 33, 1040, 2056, [33, 0, 7]),
+    (1, 300, 2048, 1096, [290]),
 ]
 IDS = [f"E{s[0]}-cap{s[1]}-H{s[2]}-I{s[3]}" for s in SHAPES]
 
@@ -261,6 +264,7 @@ def test_status_set_writes_nothing_and_stream_order():
     act, y = _buf(E, cap, I), _buf(E, cap, H)
     bad = torch.full((E * cap, 1), E, dtype=torch.int32, device="cuda")
     b = moe.Buffers(shape, expert_x=False, expert_y=False)
+    b.workspace = torch.zeros_like(ws)          # one workspace for the plan and the feed-forward
     b.plan(bad)
     assert moe.read_status(b.workspace) == moe.Status.BAD_EXPERT
     moe.ffn(shape, I, x, wgu, wd, cnt, None, act, y, b.workspace)
