@@ -34,6 +34,7 @@
 // instructions take 16-bit operands; the kept h is never re-rounded).
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <limits.h>
 
 #include <mutex>
 
@@ -48,12 +49,13 @@ namespace {
 // one another, as one list of tiles.
 enum Kind { kGateUp = 0, kDown = 1, kActGrad = 2, kRest = 3 };
 
-constexpr int kPairThreads = 256;      // warps: 0 TMA, 1 MMA, 2 zeroes tails, 3 scheduling, 4-7 epilogue
+constexpr int kPairThreads = 384;      // warps: 0 TMA, 1 MMA, 2 zeroes tails, 3 scheduling, 4-11 epilogue
+constexpr int kEpiWarps = 8;           // two groups of four; each takes every other chunk of columns
 constexpr int kStages = 6;
 constexpr int kBlockK = 64;            // one 128-byte swizzled line of bf16
 constexpr uint32_t kHalfBytes = 128 * kBlockK * 2;       // a CTA's half of one operand: 16 KB
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
-constexpr uint32_t kStagingBytes = 2 * 16384;            // epilogue, two buffers
+constexpr uint32_t kStagingBytes = 2 * 16384;            // epilogue, one buffer per group
 constexpr uint32_t kBarOff = kStages * kStageBytes + kStagingBytes;
 constexpr int kRing = 4;                                 // tiles announced ahead
 constexpr uint32_t kRingOff = kBarOff + 256;
@@ -61,11 +63,11 @@ constexpr uint32_t kPairSmem = kRingOff + kRing * 64 + 1024;   // + alignment sl
 static_assert(kPairSmem <= 232448, "shared memory of one CTA");
 constexpr int kTileCols = 256;
 constexpr uint32_t kTmemCols = 512;                      // two accumulators of 256 columns
-// A contraction is cut into at most kMaxSplit parts, when the launch has at
-// most kMaxTickets tiles and the parts' sums at most kPartCols columns of 256.
+// The tiles past the last whole round of all pairs are cut into at most
+// kMaxSplit parts of their contraction: never more parts than pairs, so their
+// sums take at most kMaxPairs tiles of 256 x 256.
 constexpr int kMaxSplit = 8;
-constexpr int kMaxTickets = 1024;
-constexpr int kPartCols = 16384;
+constexpr int kMaxPairs = 128;
 
 struct Job {
   CUtensorMap a;
@@ -97,12 +99,12 @@ __device__ __forceinline__ int rows_of(const P &p, int e) {
 
 // Columns per tile of `rows` tokens: equal tiles, a multiple of 32.
 __device__ __forceinline__ int tile_cols(int rows) {
+  if (rows <= kTileCols) return (rows + 31) & ~31;
   const int n = (rows + kTileCols - 1) / kTileCols;
-  const int c = (rows + n - 1) / n;
-  return (c + 31) & ~31;
+  return ((rows + n - 1) / n + 31) & ~31;
 }
 __device__ __forceinline__ int token_tiles(int rows) {
-  if (rows == 0) return 0;
+  if (rows <= kTileCols) return rows > 0 ? 1 : 0;
   const int c = tile_cols(rows);
   return (rows + c - 1) / c;
 }
@@ -115,7 +117,7 @@ struct alignas(16) Tile {
   int cols;                // row products: tokens in the tile
   int k0, nk;              // blocks of 64 of the contraction: [k0, k0 + nk); nk = 0: the result is 0
   int split, part;         // parts of the tile's contraction, and which this is
-  int slot;                // split > 1: tile of the launch
+  int slot;                // split > 1: tile among those that are cut
   int part_cols;           // and columns that each part's sums have room for
   int reserved[2];
 };
@@ -128,95 +130,95 @@ static_assert(sizeof(Tile) == 64, "a tile's record is 64 bytes");
 template <int KIND>
 struct Schedule {
   const PairParams<KIND> &p;
-  int64_t base, incl;
-  int e0, rows;
-  int split, part_cols;    // parts of a contraction, columns of a part's sums
+  int64_t base;            // tiles before this batch of 32 experts
+  int incl, e0, rows;      // tiles of the batch up to this lane's expert; its tokens
+  int64_t whole;           // tiles that are not cut
+  int split, part_cols;    // parts of the others, columns of a part's sums
   __device__ __forceinline__ explicit Schedule(const PairParams<KIND> &p_)
-      : p(p_), base(0), incl(0), e0(0), rows(0), split(1), part_cols(0) {
+      : p(p_), base(0), incl(0), e0(0), rows(0), whole(INT64_MAX), split(1), part_cols(0) {
     count();
-    if constexpr (KIND != kRest) choose_split();
+    if (KIND != kRest && p.job[0].K >= 16 * kBlockK) choose_split();
   }
+  // At most 2^46 elements of h: the batch's tiles fit an int.
   __device__ __forceinline__ void count() {
     const int lane = threadIdx.x & 31, e = e0 + lane;
     rows = e < p.E ? rows_of(p, e) : 0;
-    int64_t v = (int64_t)token_tiles(rows) * p.job[0].mt;
+    incl = token_tiles(rows) * p.job[0].mt;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t o = __shfl_up_sync(0xFFFFFFFFu, v, d);
-      if (lane >= d) v += o;
+      const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl += o;
     }
-    incl = base + v;
   }
-  // Few tiles for the SMs and a long contraction: cut it into parts.  The
-  // estimate is in blocks of 64: a unit costs its blocks and about kUnitCost
-  // more (filling the ring, the epilogue), a split tile the joining too.
+  // The tiles that would leave pairs idle in the last round are cut, if their
+  // contraction is long.  The estimate is in blocks of 64: a unit costs its
+  // blocks and about kUnitCost more (filling the ring, the epilogue), a tile
+  // that is cut kJoinCost and one per part for adding the sums.
   __device__ __forceinline__ void choose_split() {
     constexpr int kUnitCost = 6, kJoinCost = 8;
-    const int nk = (p.job[0].K + kBlockK - 1) / kBlockK;
-    const int pairs = gridDim.x >> 1;
-    if (nk < 16) return;
     const int lane = threadIdx.x & 31;
-    int64_t tiles = 0;
-    int cols = 0;
-    for (int e = lane; e < p.E; e += 32) {
+    int64_t tiles = incl;
+    int cols = tile_cols(rows);
+    for (int e = e0 + 32 + lane; e < p.E; e += 32) {
       const int r = rows_of(p, e);
-      if (r == 0) continue;
       tiles += (int64_t)token_tiles(r) * p.job[0].mt;
       cols = max(cols, tile_cols(r));
     }
+    if (lane < 31) tiles -= incl;            // the first batch's sum is the last lane's
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, d);
-      cols = max(cols, __shfl_xor_sync(0xFFFFFFFFu, cols, d));
-    }
-    if (tiles == 0 || tiles >= 4 * pairs || tiles > kMaxTickets) return;
+    for (int d = 16; d > 0; d >>= 1) tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, d);
+    cols = __reduce_max_sync(0xFFFFFFFFu, cols);
+    const int pairs = gridDim.x >> 1, nk = (p.job[0].K + kBlockK - 1) / kBlockK;
+    const int left = (int)(tiles % pairs);
+    if (left == 0) return;
+    // lane s - 1 prices s parts
+    const int s = lane + 1;
+    const bool can = s == 1 || (s <= kMaxSplit && s * left <= kMaxPairs && 4 * s <= nk);
+    const int cost = can ? ((left * s + pairs - 1) / pairs) * ((nk + s - 1) / s + kUnitCost) +
+                               (s > 1 ? kJoinCost + s : 0)
+                         : INT_MAX >> 6;
+    split = (__reduce_min_sync(0xFFFFFFFFu, cost * 32 + lane) & 31) + 1;
+    whole = tiles - left;
     part_cols = cols;
-    const int t = (int)tiles;
-    int best = (t + pairs - 1) / pairs * (nk + kUnitCost);
-    for (int s = 2; s <= kMaxSplit && s * 4 <= nk; ++s) {
-      if (t * s * cols > kPartCols) break;
-      const int cost = (t * s + pairs - 1) / pairs * ((nk + s - 1) / s + kUnitCost) + kJoinCost;
-      if (cost < best) {
-        best = cost;
-        split = s;
-      }
-    }
   }
   __device__ __forceinline__ bool find(int64_t unit, Tile &o) {
-    const int64_t t = split > 1 ? unit / split : unit;
+    const bool cut = unit >= whole && split > 1;
+    const int in = cut ? (int)(unit - whole) : 0;
+    const int64_t t = cut ? whole + in / split : unit;
     while (true) {
-      const int64_t end = __shfl_sync(0xFFFFFFFFu, incl, 31);
+      const int64_t end = base + __shfl_sync(0xFFFFFFFFu, incl, 31);
       if (t < end) break;
       base = end;
       if (e0 + 32 >= p.E) {
+        incl = 0;                            // base now counts every row tile, for good
         if constexpr (KIND == kRest) return find_weight(t - base, o);
         else return false;
       }
       e0 += 32;
       count();
     }
-    const unsigned after = __ballot_sync(0xFFFFFFFFu, incl > t);
-    const int l = __ffs(after) - 1;
-    const int64_t before = __shfl_sync(0xFFFFFFFFu, incl, l > 0 ? l - 1 : 0);
-    const int r = (int)(t - (l > 0 ? before : base));
+    const int tb = (int)(t - base);
+    const int l = __ffs(__ballot_sync(0xFFFFFFFFu, incl > tb)) - 1;
+    const int before = __shfl_sync(0xFFFFFFFFu, incl, l > 0 ? l - 1 : 0);
+    const int r = tb - (l > 0 ? before : 0);
     o.job = 0;
     o.e = e0 + l;
     o.rows = __shfl_sync(0xFFFFFFFFu, rows, l);
-    const int c = tile_cols(o.rows), nt = (o.rows + c - 1) / c;
-    o.m = r / nt;
+    const int c = tile_cols(o.rows), nt = token_tiles(o.rows);
+    o.m = nt == 1 ? r : r / nt;
     o.n0 = (r - o.m * nt) * c;
     o.cols = min(c, o.rows - o.n0);
     o.n = (o.cols + 31) & ~31;
     const int nk = (p.job[0].K + kBlockK - 1) / kBlockK;
     o.k0 = 0;
     o.nk = nk;
-    o.split = split;
+    o.split = cut ? split : 1;
     o.part = 0;
     o.slot = 0;
     o.part_cols = part_cols;
-    if (split > 1) {
-      o.slot = (int)t;
-      o.part = (int)(unit - t * split);
+    if (cut) {
+      o.slot = in / split;
+      o.part = in - o.slot * split;
       o.k0 = nk * o.part / split;
       o.nk = nk * (o.part + 1) / split - o.k0;
     }
@@ -334,12 +336,12 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init_at(tm_full + 8 * b, 1);
-      tc::mbar_init_at(tm_empty + 8 * b, 8);   // four epilogue warps in each CTA
+      tc::mbar_init_at(tm_empty + 8 * b, 2 * kEpiWarps);   // the epilogue warps of both CTAs
     }
     for (int r = 0; r < kRing; ++r) {
       tc::mbar_init_at(rec_full + 8 * r, 1);
       // TMA, epilogue, and where they run the MMA and the zeroing warp
-      tc::mbar_init_at(rec_empty + 8 * r, 5 + (rank == 0 ? 1 : 0) + (KIND == kRest ? 1 : 0));
+      tc::mbar_init_at(rec_empty + 8 * r, kEpiWarps + 1 + (rank == 0 ? 1 : 0) + (KIND == kRest ? 1 : 0));
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   } else if (threadIdx.x == 32 && p.job[0].mt > 0) {
@@ -523,26 +525,91 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     }
   } else if (live && warp >= 4) {
     // ---- epilogue: tensor memory -> registers -> shared memory -> results
-    uint32_t it = 0, chunk = 0;
-    const int wq = warp - 4, tid = threadIdx.x - 128;
+    uint32_t it = 0;
+    const int wq = warp & 3, grp = (warp - 4) >> 2, tid = (threadIdx.x - 128) & 127;
     const uint32_t empty0 = tc::map_rank(tm_empty, 0);
+    uint8_t *const stage_p = smem_p + kStages * kStageBytes + grp * 16384;
+    const uint32_t stage_u = staging + grp * 16384;
     while (true) {
       const bool more = feed.next(t, ok);
       const uint32_t buf = it & 1u;
+      const Job &j = p.job[KIND == kRest ? t.job : 0];
+      // a thread's place in the staged chunk: 4 features of rows r8, r8 + 8, ...
+      const int i4 = tid & 15, r8 = tid >> 4;
+      const int f0 = KIND == kGateUp ? t.m * 128 + (int)rank * 64 + 4 * i4
+                                     : t.m * 256 + (int)rank * 128 + 4 * i4;
+      const int64_t row0 = (int64_t)t.e * p.cap + t.n0;
+      uint2 g[4][2], u[4][2];                // kActGrad: kept gate and up of a chunk
+      const auto load_h = [&](int c) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+            if (c + r * 8 + r8 < t.cols && f0 + 64 * hf < j.M) {
+              const uint16_t *q = j.h + (row0 + c + r * 8 + r8) * 2 * j.M + f0 + 64 * hf;
+              g[r][hf] = *reinterpret_cast<const uint2 *>(q);
+              u[r][hf] = *reinterpret_cast<const uint2 *>(q + j.M);
+            }
+      };
+      // one token's 4 + 4 features: sums lo, hi -> results
+      const auto emit = [&](int tok, int r, const float4 &lo4, const float4 &hi4) {
+        const float lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
+        const int64_t row = row0 + tok;
+        if (KIND == kGateUp) {               // lo: gate, hi: up of the same features
+          if (f0 < j.M) {
+            float a[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) a[k] = lo[k] * sigmoid(lo[k]) * hi[k];
+            *reinterpret_cast<uint2 *>(j.o0 + row * j.M + f0) = pack4(a);
+            if (j.o1) {
+              *reinterpret_cast<uint2 *>(j.o1 + row * 2 * j.M + f0) = pack4(lo);
+              *reinterpret_cast<uint2 *>(j.o1 + row * 2 * j.M + j.M + f0) = pack4(hi);
+            }
+          }
+        } else if (KIND == kActGrad) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+            if (f0 + 64 * hf < j.M) {
+              float gv[4], uv[4], a[4], dg[4], du[4];
+              unpack4(g[r][hf], gv);
+              unpack4(u[r][hf], uv);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float da = hf ? hi[k] : lo[k];
+                const float sg = sigmoid(gv[k]), silu = gv[k] * sg;
+                a[k] = silu * uv[k];
+                du[k] = da * silu;
+                dg[k] = da * uv[k] * (sg + silu * (1.0f - sg));
+              }
+              *reinterpret_cast<uint2 *>(j.o0 + row * j.M + f0 + 64 * hf) = pack4(a);
+              uint16_t *q = j.o1 + row * 2 * j.M + f0 + 64 * hf;
+              *reinterpret_cast<uint2 *>(q) = pack4(dg);
+              *reinterpret_cast<uint2 *>(q + j.M) = pack4(du);
+            }
+        } else {
+          if (f0 < j.M) *reinterpret_cast<uint2 *>(j.o0 + row * j.M + f0) = pack4(lo);
+          if (f0 + 64 < j.M) *reinterpret_cast<uint2 *>(j.o0 + row * j.M + f0 + 64) = pack4(hi);
+        }
+      };
       if (more && t.nk > 0) {
+        if (KIND == kActGrad) load_h(grp * 32);          // while the tile is multiplied
         ok = wait_bar(tm_full + 8 * buf, (it >> 1) & 1u, limit);
         tc::fence_after();
       }
-      // all four warps agree to go on, and are done with the staging buffers
-      ok = named_sync_and(1, 128, ok);
+      // all the warps agree to go on, and are done with the staging buffers
+      ok = named_sync_and(3, 32 * kEpiWarps, ok);
       if (!ok || !more) break;
-      const Job &j = p.job[KIND == kRest ? t.job : 0];
       const uint32_t src = tmem + ((uint32_t)(wq * 32) << 16) + buf * kTileCols;
+      const auto release = [&] {             // this warp has read its part of the accumulator
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_remote(empty0 + 8 * buf);
+      };
       if (KIND == kRest && t.job > 0) {
         // each warp on its own: 32 rows x 64 columns of bf16, swizzled, stored by TMA
         const int m0 = t.m * 256 + (int)rank * 128 + wq * 32;
-        for (int c = 0; c < t.n; c += 64, ++chunk) {
-          const uint32_t dst = wq * 8192u + (chunk & 1u) * 4096u;
+        if (t.nk > 0 && grp * 64 >= t.n) release();
+        for (int c = grp * 64; c < t.n; c += 128) {
           uint32_t v[32], w[32];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
@@ -557,15 +624,11 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
             for (int q = 0; q < 16; ++q)
               w[hf * 16 + q] = pack2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
           }
-          if (t.nk > 0 && c + 64 >= t.n) {
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_remote(empty0 + 8 * buf);
-          }
-          // the store of two chunks ago has read its buffer
-          if (lane == 0) tc::store_wait_read<1>();
+          if (t.nk > 0 && c + 128 >= t.n) release();
+          // this warp's last store has read the buffer
+          if (lane == 0) tc::store_wait_read<0>();
           __syncwarp();
-          uint8_t *q = smem_p + kStages * kStageBytes + dst + lane * 128;
+          uint8_t *q = stage_p + wq * 4096 + lane * 128;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             *reinterpret_cast<uint4 *>(q + ((k ^ (lane & 7)) * 16)) =
@@ -573,131 +636,77 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
           tc::fence_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (m0 < j.M && t.n0 + c < j.N) tc::tma_store(&j.out, staging + dst, t.n0 + c, m0, 0, t.e);
+            if (m0 < j.M && t.n0 + c < j.N)
+              tc::tma_store(&j.out, stage_u + wq * 4096, t.n0 + c, m0, 0, t.e);
             tc::store_commit();
           }
         }
-      } else {
-        const int i4 = tid & 15, r8 = tid >> 4;
-        const int f0 = KIND == kGateUp ? t.m * 128 + (int)rank * 64 + 4 * i4
-                                       : t.m * 256 + (int)rank * 128 + 4 * i4;
-        const int64_t row0 = (int64_t)t.e * p.cap + t.n0;
+      } else if (KIND != kRest && t.split > 1) {
         // A part of a split contraction leaves its sums in the workspace
         // ([tile][part][CTA][column][128 features]); the last part to finish
         // adds all of them, in the order of the parts.
-        const bool split = KIND != kRest && t.split > 1;
-        float *part = nullptr;
-        if (split) {
-          part = p.part + (t.slot * t.split * 2 + (int)rank) * ((int64_t)t.part_cols * 128);
-          float *own = part + (int64_t)t.part * 2 * t.part_cols * 128;
-          for (int c = 0; c < t.n; c += 32) {
-            uint32_t v[32];
-            tc::tmem_ld32(v, src + c);
-            tc::tmem_ld_wait();
+        const int64_t size = (int64_t)t.part_cols * 128;
+        const float *part = p.part + (t.slot * t.split * 2 + (int)rank) * size;
+        float *own = p.part + ((t.slot * t.split + t.part) * 2 + (int)rank) * size;
+        for (int c = grp * 32; c < t.n; c += 64) {
+          uint32_t v[32];
+          tc::tmem_ld32(v, src + c);
+          tc::tmem_ld_wait();
 #pragma unroll
-            for (int q = 0; q < 32; ++q)
-              __stcg(own + (int64_t)(c + q) * 128 + wq * 32 + lane, __uint_as_float(v[q]));
-          }
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive_remote(empty0 + 8 * buf);
-          ++it;
-          __threadfence();
-          named_sync(1, 128);
-          if (tid == 0) {
-            uint32_t *ticket = p.tickets + t.slot * 2 + rank;
-            const bool last = atomicAdd(ticket, 1u) == (uint32_t)t.split - 1;
-            if (last) *ticket = 0;
-            *last_in = last;
-            __threadfence();
-          }
-          named_sync(1, 128);
-          const bool last = *last_in != 0;
-          named_sync(1, 128);
-          if (!last) continue;
+          for (int q = 0; q < 32; ++q)
+            __stcg(own + (c + q) * 128 + wq * 32 + lane, __uint_as_float(v[q]));
+        }
+        release();
+        __threadfence();
+        named_sync(3, 32 * kEpiWarps);
+        if (threadIdx.x == 128) {
+          uint32_t *ticket = p.tickets + t.slot * 2 + rank;
+          const bool last = atomicAdd(ticket, 1u) == (uint32_t)t.split - 1;
+          if (last) *ticket = 0;
+          *last_in = last;
           __threadfence();
         }
-        for (int c = 0; c < t.n; c += 32, ++chunk) {
-          uint2 g[4][2], u[4][2];
-          if (KIND == kActGrad) {
+        named_sync(3, 32 * kEpiWarps);
+        if (*last_in != 0)
+          for (int c = grp * 32; c < t.n; c += 64) {
+            float4 lo[4], hi[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) lo[r] = hi[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int s = 0; s < t.split; ++s)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float *q = part + s * 2 * size + (c + r * 8 + r8) * 128 + 4 * i4;
+                const float4 a = __ldcg(reinterpret_cast<const float4 *>(q));
+                const float4 b = __ldcg(reinterpret_cast<const float4 *>(q + 64));
+                lo[r] = make_float4(lo[r].x + a.x, lo[r].y + a.y, lo[r].z + a.z, lo[r].w + a.w);
+                hi[r] = make_float4(hi[r].x + b.x, hi[r].y + b.y, hi[r].z + b.z, hi[r].w + b.w);
+              }
+            if (KIND == kActGrad && c > grp * 32) load_h(c);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
-                if (c + r * 8 + r8 < t.cols && f0 + 64 * hf < j.M) {
-                  const uint16_t *q = j.h + (row0 + c + r * 8 + r8) * 2 * j.M + f0 + 64 * hf;
-                  g[r][hf] = *reinterpret_cast<const uint2 *>(q);
-                  u[r][hf] = *reinterpret_cast<const uint2 *>(q + j.M);
-                }
+              if (c + r * 8 + r8 < t.cols) emit(c + r * 8 + r8, r, lo[r], hi[r]);
           }
+      } else {
+        if (grp * 32 >= t.n) release();
+        float *st = reinterpret_cast<float *>(stage_p);
+        for (int c = grp * 32; c < t.n; c += 64) {
           uint32_t v[32];
-          if (!split) {
-            tc::tmem_ld32(v, src + c);
-            tc::tmem_ld_wait();
-            if (c + 32 >= t.n) {
-              tc::fence_before();
-              __syncwarp();
-              if (lane == 0) tc::mbar_arrive_remote(empty0 + 8 * buf);
-            }
-          } else {
-            const float *q0 = part + (int64_t)c * 128 + wq * 32 + lane;
-#pragma unroll
-            for (int q = 0; q < 32; ++q) v[q] = 0u;
-            for (int s = 0; s < t.split; ++s, q0 += (int64_t)2 * t.part_cols * 128)
-#pragma unroll
-              for (int q = 0; q < 32; ++q)
-                v[q] = __float_as_uint(__uint_as_float(v[q]) + __ldcg(q0 + q * 128));
-          }
-          float *st = reinterpret_cast<float *>(smem_p + kStages * kStageBytes + (chunk & 1u) * 16384u);
+          tc::tmem_ld32(v, src + c);
+          tc::tmem_ld_wait();
+          if (c + 64 >= t.n) release();
+          if (c > grp * 32) named_sync(1 + grp, 128);      // the last chunk has been read
 #pragma unroll
           for (int q = 0; q < 32; ++q) st[q * 128 + wq * 32 + lane] = __uint_as_float(v[q]);
-          named_sync(1, 128);
+          named_sync(1 + grp, 128);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int tok = r * 8 + r8;
-            if (c + tok >= t.cols) continue;
-            const float4 lo4 = *reinterpret_cast<const float4 *>(st + tok * 128 + 4 * i4);
-            const float4 hi4 = *reinterpret_cast<const float4 *>(st + tok * 128 + 64 + 4 * i4);
-            const float lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
-            const int64_t row = row0 + c + tok;
-            if (KIND == kGateUp) {
-              if (f0 < j.M) {
-                float a[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) a[k] = lo[k] * sigmoid(lo[k]) * hi[k];
-                *reinterpret_cast<uint2 *>(j.o0 + row * j.M + f0) = pack4(a);
-                if (j.o1) {
-                  *reinterpret_cast<uint2 *>(j.o1 + row * 2 * j.M + f0) = pack4(lo);
-                  *reinterpret_cast<uint2 *>(j.o1 + row * 2 * j.M + j.M + f0) = pack4(hi);
-                }
-              }
-            } else if (KIND == kActGrad) {
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
-                if (f0 + 64 * hf < j.M) {
-                  float gv[4], uv[4], a[4], dg[4], du[4];
-                  unpack4(g[r][hf], gv);
-                  unpack4(u[r][hf], uv);
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const float da = hf ? hi[k] : lo[k];
-                    const float sg = sigmoid(gv[k]), silu = gv[k] * sg;
-                    a[k] = silu * uv[k];
-                    du[k] = da * silu;
-                    dg[k] = da * uv[k] * (sg + silu * (1.0f - sg));
-                  }
-                  *reinterpret_cast<uint2 *>(j.o0 + row * j.M + f0 + 64 * hf) = pack4(a);
-                  uint16_t *q = j.o1 + row * 2 * j.M + f0 + 64 * hf;
-                  *reinterpret_cast<uint2 *>(q) = pack4(dg);
-                  *reinterpret_cast<uint2 *>(q + j.M) = pack4(du);
-                }
-            } else {
-              if (f0 < j.M) *reinterpret_cast<uint2 *>(j.o0 + row * j.M + f0) = pack4(lo);
-              if (f0 + 64 < j.M) *reinterpret_cast<uint2 *>(j.o0 + row * j.M + f0 + 64) = pack4(hi);
-            }
+            if (c + tok < t.cols)
+              emit(c + tok, r, *reinterpret_cast<const float4 *>(st + tok * 128 + 4 * i4),
+                   *reinterpret_cast<const float4 *>(st + tok * 128 + 64 + 4 * i4));
           }
+          if (KIND == kActGrad && c + 64 < t.n) load_h(c + 64);
         }
-        if (split) continue;        // counted above
       }
       if (t.nk > 0) ++it;
     }
@@ -764,7 +773,8 @@ cudaError_t launch_pair(const PairParams<KIND> &p, int64_t tiles, cudaStream_t s
                                 (int)kPairSmem);
   });
   if (attr != cudaSuccess) return attr;
-  const int64_t most = device_sm_count() / 2;
+  int64_t most = device_sm_count() / 2;
+  if (most > kMaxPairs) most = kMaxPairs;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -814,8 +824,7 @@ size_t ffn_scratch_bytes(int64_t E, int64_t cap, int64_t H, int64_t I) {
   const int64_t mt = cdiv(I, 128) > cdiv(H, 256) ? cdiv(I, 128) : cdiv(H, 256);
   const int64_t most = mt * E * cdiv(cap, kTileCols) * kMaxSplit;
   const int64_t cols = cap < kTileCols ? (cap + 31) / 32 * 32 : kTileCols;
-  const int64_t part_cols = most < kPartCols / cols ? most * cols : kPartCols;
-  return kTicketBytes + (size_t)part_cols * 256 * sizeof(float);
+  return kTicketBytes + (size_t)((most < kMaxPairs ? most : kMaxPairs) * cols) * 256 * sizeof(float);
 }
 
 cudaError_t launch_ffn(const FfnParams &f, cudaStream_t stream) {

@@ -29,7 +29,7 @@ struct FfnParams {
 
 // Scratch past the plan's workspace: kTicketBytes of tickets, zero between
 // calls, then the partial sums of split contractions.
-constexpr size_t kTicketBytes = 8192;
+constexpr size_t kTicketBytes = 1024;
 size_t ffn_scratch_bytes(int64_t E, int64_t cap, int64_t H, int64_t I);
 
 cudaError_t launch_ffn(const FfnParams &p, cudaStream_t stream);

@@ -27,7 +27,8 @@ D = torch.float64
 # just over it, and a multiple of 64; sizes that are multiples of 8 alone;
 # more experts than a warp has lanes, most of them empty; counts below zero
 # and above cap are clamped; few tiles and contractions over 1024 and more,
-# which are cut into parts.
+# which are cut into parts; several tiles of every
+# product for each pair of SMs.
 SHAPES = [
     (1, 1, 8, 8, [1]),
     (3, 5, 264, 136, [0, 5, 1]),
@@ -40,6 +41,8 @@ SHAPES = [
     (2, 130, 2056, 520, [130, 65]),
     (3, 33, 1040, 2056, [33, 0, 7]),
     (1, 300, 2048, 1096, [290]),
+    (8, 64, 1032, 520, [64, 1, 0, 63, 33, 64, 5, 64]),
+    (33, 20, 520, 264, [20, 1, 0] * 11),
 ]
 IDS = [f"E{s[0]}-cap{s[1]}-H{s[2]}-I{s[3]}" for s in SHAPES]
 
