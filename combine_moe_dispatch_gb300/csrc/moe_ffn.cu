@@ -77,6 +77,7 @@ struct Job {
   const uint16_t *h;       // kActGrad: kept gate | up
   int M, N, K;             // features; weight gradients: output columns; row products: contraction
   int mt;                  // tiles of 256 accumulator rows (kGateUp: of 128 features); 0: no job
+  int a_wide, b_wide;      // MN-major operands: a copy brings 128 rows (else 64) x 64 k
 };
 
 template <int KIND>
@@ -288,6 +289,18 @@ struct Feed {
     }
     return t.valid != 0;
   }
+  // The same, called by one thread of the warp alone.
+  __device__ __forceinline__ bool next_alone(Tile &t, bool &ok) {
+    ok = wait_bar(full + 8 * s, ph, limit);
+    if (!ok) return false;
+    t = ring[s];
+    tc::mbar_arrive_local(empty + 8 * s);
+    if (++s == kRing) {
+      s = 0;
+      ph ^= 1u;
+    }
+    return t.valid != 0;
+  }
 };
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -386,17 +399,34 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     }
   } else if (live && warp == 0) {
     // ---- TMA: both CTAs load their halves; bytes complete on the leader's barrier
-    int s = 0;
-    uint32_t ph = 0;
-    const uint32_t full0 = tc::map_rank(full, 0);
-    while (ok && feed.next(t, ok)) {
-      if (lane == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      const uint32_t full0 = tc::map_rank(full, 0);
+      while (ok && feed.next_alone(t, ok)) {
         const Job &j = p.job[KIND == kRest ? t.job : 0];
         const bool weight = KIND == kRest && t.job > 0;
         const uint32_t half_n = t.n >> 1;
         const int bsel = half_n <= 16 ? 0 : half_n <= 32 ? 1 : half_n <= 64 ? 2 : 3;
         const uint32_t bytes = kHalfBytes + (weight ? kHalfBytes : (16u << bsel) * 128u);
         const int tail_rows = weight ? (t.rows & (kBlockK - 1)) : 0;
+        // 128 rows of an MN-major operand from row r on: 64 rows a copy, or all
+        const auto load_mn = [&](uint32_t dst, const CUtensorMap *map, int wide, bool own, uint32_t bar,
+                                 int r, int k0) {
+          if (own) {
+            if (wide) {
+              tc::tma_load_own(dst, map, bar, 0, k0, r >> 6, t.e);
+            } else {
+              tc::tma_load_own(dst, map, bar, r, k0, 0, t.e);
+              tc::tma_load_own(dst + 8192, map, bar, r + 64, k0, 0, t.e);
+            }
+          } else if (wide) {
+            tc::tma_load_pair(dst, map, bar, 0, k0, r >> 6, t.e);
+          } else {
+            tc::tma_load_pair(dst, map, bar, r, k0, 0, t.e);
+            tc::tma_load_pair(dst + 8192, map, bar, r + 64, k0, 0, t.e);
+          }
+        };
         for (int kb = 0; kb < t.nk; ++kb) {
           if (!wait_bar(empty + 8 * s, ph ^ 1u, limit)) {
             ok = false;
@@ -404,54 +434,33 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
           }
           const uint32_t sa = smem + s * kStageBytes, sb = sa + kHalfBytes;
           const int k0 = (t.k0 + kb) * kBlockK;
-          const uint32_t bar = full0 + 8 * s;
-          if (weight) {
-            const int m0 = t.m * 256 + rank * 128, n0 = t.n0 + rank * half_n;
-            if (tail_rows != 0 && kb == t.nk - 1) {
-              const uint32_t own = tail + 8 * s;
-              tc::mbar_expect_local(own, bytes);
-              tc::tma_load_own(sa, &j.a, own, m0, k0, 0, t.e);
-              tc::tma_load_own(sa + 8192, &j.a, own, m0 + 64, k0, 0, t.e);
-              tc::tma_load_own(sb, &j.b[0], own, n0, k0, 0, t.e);
-              tc::tma_load_own(sb + 8192, &j.b[0], own, n0 + 64, k0, 0, t.e);
-            } else {
-              if (rank == 0) {
-                tc::mbar_expect_local(full + 8 * s, 2 * bytes);
-                tc::mbar_arrive_local(full + 8 * s);
-              }
-              tc::tma_load_pair(sa, &j.a, bar, m0, k0, 0, t.e);
-              tc::tma_load_pair(sa + 8192, &j.a, bar, m0 + 64, k0, 0, t.e);
-              tc::tma_load_pair(sb, &j.b[0], bar, n0, k0, 0, t.e);
-              tc::tma_load_pair(sb + 8192, &j.b[0], bar, n0 + 64, k0, 0, t.e);
-            }
-          } else {
-            if (rank == 0) {
-              tc::mbar_expect_local(full + 8 * s, 2 * bytes);
-              if (kFullArrivals == 2) tc::mbar_arrive_local(full + 8 * s);
-            }
-            if (KIND == kGateUp) {             // 64 gate rows, then the same 64 features of up
-              const int f0 = t.m * 128 + rank * 64;
-              tc::tma_load_pair(sa, &j.a, bar, k0, f0, 0, t.e);
-              tc::tma_load_pair(sa + 8192, &j.a, bar, k0, f0, 1, t.e);
-            } else if (kAMn) {
-              const int m0 = t.m * 256 + rank * 128;
-              tc::tma_load_pair(sa, &j.a, bar, m0, k0, 0, t.e);
-              tc::tma_load_pair(sa + 8192, &j.a, bar, m0 + 64, k0, 0, t.e);
-            } else {
-              tc::tma_load_pair(sa, &j.a, bar, k0, t.m * 256 + rank * 128, 0, t.e);
-            }
-            tc::tma_load_pair(sb, &j.b[bsel], bar, k0, t.n0 + rank * half_n, 0, t.e);
+          uint32_t bar = full0 + 8 * s;
+          const bool own = tail_rows != 0 && kb == t.nk - 1;   // zeroed before it is full
+          if (own) {
+            bar = tail + 8 * s;
+            tc::mbar_expect_local(bar, bytes);
+          } else if (rank == 0) {
+            tc::mbar_expect_local(full + 8 * s, 2 * bytes);
+            if (kFullArrivals == 2) tc::mbar_arrive_local(full + 8 * s);
           }
+          const int m0 = t.m * 256 + (int)rank * 128, n0 = t.n0 + (int)(rank * half_n);
+          if (KIND == kGateUp)                 // 64 gate rows and the same 64 features of up
+            tc::tma_load_pair(sa, &j.a, bar, k0, t.m * 128 + (int)rank * 64, 0, t.e);
+          else if (kAMn)
+            load_mn(sa, &j.a, j.a_wide, own, bar, m0, k0);
+          else
+            tc::tma_load_pair(sa, &j.a, bar, k0, m0, 0, t.e);
+          if (weight)
+            load_mn(sb, &j.b[0], j.b_wide, own, bar, n0, k0);
+          else
+            tc::tma_load_pair(sb, &j.b[bsel], bar, k0, n0, 0, t.e);
           if (++s == kStages) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-    }
-    // the last commits on this CTA's barriers land before it may exit
-    if (lane == 0)
+      // the last commits on this CTA's barriers land before it may exit
       for (int i = 0; ok && i < kStages; ++i) {
         ok = wait_bar(empty + 8 * s, ph ^ 1u, limit);
         if (++s == kStages) {
@@ -459,47 +468,72 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
           ph ^= 1u;
         }
       }
+    }
     ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
   } else if (live && warp == 1 && rank == 0) {
-    // ---- matrix instructions, one thread of the leading CTA
-    int s = 0;
-    uint32_t ph = 0, it = 0;
-    while (ok && feed.next(t, ok)) {
-      if (t.nk == 0) continue;
-      if (lane == 0) {
+    // ---- matrix instructions, one thread of the leading CTA.  What it needs
+    // next (the next stage, tile and accumulator) is asked for between the
+    // instructions of a stage, so that the tensor cores have work meanwhile.
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0, it = 0;
+      bool stage_ready = false, acc_ready = false;
+      bool more = feed.next_alone(t, ok);
+      while (ok && more) {
+        if (t.nk == 0) {
+          more = feed.next_alone(t, ok);
+          continue;
+        }
         const bool bmn = KIND == kRest && t.job > 0;
         const uint32_t buf = it & 1u;
         const uint32_t d = tmem + buf * kTileCols;
         const uint32_t idesc = tc::instr_desc(256, t.n, kAMn, bmn);
         const uint32_t blead = bmn ? 8192u : 16u, bstep = bmn ? 128u : 2u;
-        ok = wait_bar(tm_empty + 8 * buf, ((it >> 1) & 1u) ^ 1u, limit);
+        // the last block of a weight gradient: no more than its tokens need
+        const int tail_rows = bmn ? (t.rows & (kBlockK - 1)) : 0;
+        if (!acc_ready) ok = wait_bar(tm_empty + 8 * buf, ((it >> 1) & 1u) ^ 1u, limit);
+        acc_ready = false;
         tc::fence_after();
+        Tile nx;
+        bool nx_ok = true;
         for (int kb = 0; ok && kb < t.nk; ++kb) {
-          if (!wait_bar(full + 8 * s, ph, limit)) {
+          if (!stage_ready && !wait_bar(full + 8 * s, ph, limit)) {
             ok = false;
             break;
           }
+          const bool last = kb == t.nk - 1;
+          const int steps = last && tail_rows != 0 ? (tail_rows + 15) >> 4 : kBlockK / 16;
           // zeroed by ordinary stores in either CTA: acquire those too
-          if (KIND == kRest && bmn && kb == t.nk - 1) tc::mbar_try_cluster(full + 8 * s, ph);
+          if (last && tail_rows != 0) tc::mbar_try_cluster(full + 8 * s, ph);
           tc::fence_after();
           const uint32_t sa = smem + s * kStageBytes, sb = sa + kHalfBytes;
           const uint64_t da = tc::smem_desc(sa, kAMn ? 8192u : 16u);
           const uint64_t db = tc::smem_desc(sb, blead);
-#pragma unroll
-          for (int k = 0; k < kBlockK / 16; ++k)
-            // 16 k on: 32 bytes of a K-major line, 16 lines (2048 bytes) MN-major
-            tc::mma_pair(d, da + (kAMn ? k * 128 : k * 2), db + k * bstep, idesc, kb > 0 || k > 0);
-          tc::mma_commit_pair(empty + 8 * s);
+          // 16 k on: 32 bytes of a K-major line, 16 lines (2048 bytes) MN-major
+          constexpr int astep = kAMn ? 128 : 2;
+          tc::mma_pair(d, da, db, idesc, kb > 0);
+          if (steps > 1) tc::mma_pair(d, da + astep, db + bstep, idesc, 1);
+          const uint32_t stage = empty + 8 * s;
           if (++s == kStages) {
             s = 0;
             ph ^= 1u;
           }
+          // one tile ahead only: the epilogue waits for this one
+          if (kb == 0) more = feed.next_alone(nx, nx_ok);
+          const bool go_on = more && nx.nk > 0;
+          stage_ready = (!last || go_on) && tc::mbar_test(full + 8 * s, ph);
+          if (last && go_on) acc_ready = tc::mbar_test(tm_empty + 8 * (buf ^ 1u), (((it + 1) >> 1) & 1u) ^ 1u);
+          if (steps > 2) tc::mma_pair(d, da + 2 * astep, db + 2 * bstep, idesc, 1);
+          if (steps > 3) tc::mma_pair(d, da + 3 * astep, db + 3 * bstep, idesc, 1);
+          tc::mma_commit_pair(stage);
         }
         if (ok) tc::mma_commit_pair(tm_full + 8 * buf);
+        ok = ok && nx_ok;
+        t = nx;
+        ++it;
       }
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-      ++it;
     }
+    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
   } else if (live && warp == 2 && KIND == kRest) {
     // ---- zero the rows past the expert's count in its last block
     int s = 0;
@@ -516,8 +550,9 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
       phases ^= 1u << last;
       if (!ok) break;
       uint8_t *base = smem_p + last * kStageBytes;
+      // up to the next multiple of 16, the k of one matrix instruction
       for (int c = 0; c < 4; ++c)
-        for (int j = valid * 8 + lane; j < kBlockK * 8; j += 32)
+        for (int j = valid * 8 + lane; j < ((valid + 15) & ~15) * 8; j += 32)
           *reinterpret_cast<uint4 *>(base + c * 8192 + j * 16) = make_uint4(0, 0, 0, 0);
       tc::fence_async_smem();
       __syncwarp();
@@ -747,19 +782,34 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// [d3][d2][d1][d0] bf16, dense; boxes of 64 x rows elements, 128-byte swizzle.
-bool make_map(CUtensorMap *m, const void *base, int64_t d0, int64_t d1, int64_t d2, int64_t d3,
-              int rows) {
+// bf16 elements [d3][d2][d1][d0], `s1`, `s2` and `s3` elements apart; boxes of
+// deep x rows x 64 elements, 128-byte swizzle.
+bool encode(CUtensorMap *m, const void *base, int64_t d0, int64_t d1, int64_t d2, int64_t d3,
+            int64_t s1, int64_t s2, int64_t s3, int rows, int deep) {
   const EncodeFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2, (cuuint64_t)d3};
-  const cuuint64_t strides[3] = {(cuuint64_t)d0 * 2, (cuuint64_t)(d0 * d1) * 2,
-                                 (cuuint64_t)(d0 * d1 * d2) * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+  const cuuint64_t strides[3] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2, (cuuint64_t)s3 * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)deep, 1};
   const cuuint32_t step[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, step,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A dense array [d3][d2][d1][d0].
+bool make_map(CUtensorMap *m, const void *base, int64_t d0, int64_t d1, int64_t d2, int64_t d3,
+              int rows, int deep = 1) {
+  return encode(m, base, d0, d1, d2, d3, d0, d0 * d1, d0 * d1 * d2, rows, deep);
+}
+
+// An operand stored [E][k][width], its contraction dimension k outside: one
+// copy brings 64 k of 128 rows, as two blocks of 64 rows, where the width
+// allows (*wide), else of 64.
+bool make_map_mn(CUtensorMap *m, int *wide, const void *base, int64_t width, int64_t k, int64_t E) {
+  *wide = width % 128 == 0;
+  if (*wide) return encode(m, base, 64, k, width / 64, E, width, 64, k * width, 64, 2);
+  return make_map(m, base, width, k, 1, E, 64);
 }
 
 template <int KIND>
@@ -831,7 +881,7 @@ cudaError_t launch_ffn(const FfnParams &f, cudaStream_t stream) {
   {
     PairParams<kGateUp> p = base_params<kGateUp>(f);
     Job &j = p.job[0];
-    if (!make_map(&j.a, f.w_gate_up, f.H, f.I, 2, f.E, 64) || !token_maps(j, f.x, f.H, f.cap, f.E))
+    if (!make_map(&j.a, f.w_gate_up, f.H, f.I, 2, f.E, 64, 2) || !token_maps(j, f.x, f.H, f.cap, f.E))
       return cudaErrorInvalidValue;
     j.o0 = f.act;
     j.o1 = f.h;
@@ -857,7 +907,7 @@ cudaError_t launch_ffn_backward(const FfnParams &f, cudaStream_t stream) {
   {
     PairParams<kActGrad> p = base_params<kActGrad>(f);       // dh and a
     Job &j = p.job[0];
-    if (!make_map(&j.a, f.w_down, f.I, f.H, 1, f.E, 64) || !token_maps(j, f.dy, f.H, f.cap, f.E))
+    if (!make_map_mn(&j.a, &j.a_wide, f.w_down, f.I, f.H, f.E) || !token_maps(j, f.dy, f.H, f.cap, f.E))
       return cudaErrorInvalidValue;
     j.o0 = f.act;
     j.o1 = f.dh;
@@ -873,7 +923,7 @@ cudaError_t launch_ffn_backward(const FfnParams &f, cudaStream_t stream) {
   int64_t tiles = 0;
   if (f.dx) {
     Job &j = p.job[0];
-    if (!make_map(&j.a, f.w_gate_up, f.H, I2, 1, f.E, 64) || !token_maps(j, f.dh, I2, f.cap, f.E))
+    if (!make_map_mn(&j.a, &j.a_wide, f.w_gate_up, f.H, I2, f.E) || !token_maps(j, f.dh, I2, f.cap, f.E))
       return cudaErrorInvalidValue;
     j.o0 = f.dx;
     j.M = f.H;
@@ -886,8 +936,8 @@ cudaError_t launch_ffn_backward(const FfnParams &f, cudaStream_t stream) {
     if (!out) continue;
     Job &j = p.job[1 + w];
     const int64_t M = w ? f.H : I2, N = w ? f.I : f.H;
-    if (!make_map(&j.a, w ? (const void *)f.dy : f.dh, M, f.cap, 1, f.E, 64) ||
-        !make_map(&j.b[0], w ? (const void *)f.act : f.x, N, f.cap, 1, f.E, 64) ||
+    if (!make_map_mn(&j.a, &j.a_wide, w ? (const void *)f.dy : f.dh, M, f.cap, f.E) ||
+        !make_map_mn(&j.b[0], &j.b_wide, w ? (const void *)f.act : f.x, N, f.cap, f.E) ||
         !make_map(&j.out, out, N, M, 1, f.E, 32))
       return cudaErrorInvalidValue;
     j.M = (int)M;
