@@ -123,6 +123,7 @@ struct alignas(16) Tile {
   int reserved[2];
 };
 static_assert(sizeof(Tile) == 64, "a tile's record is 64 bytes");
+constexpr int kTileWords = 14;
 
 // The launch's units of work in order: tiles of the row product by expert
 // (each `split` times, once per part of the contraction), then the weight
@@ -276,25 +277,29 @@ struct Feed {
   uint32_t ph;
   __device__ __forceinline__ Feed(const Tile *ring_, uint32_t full_, uint32_t empty_, uint64_t limit_)
       : ring(ring_), full(full_), empty(empty_), limit(limit_), s(0), ph(0) {}
-  // The next tile; false when there is none, or (ok false) when the wait ran out.
+  // The next tile; false when there is none, or (ok false) when the wait ran
+  // out.  Called by the whole warp; every lane gets the same values.
   __device__ __forceinline__ bool next(Tile &t, bool &ok) {
     ok = __all_sync(0xFFFFFFFFu, wait_bar(full + 8 * s, ph, limit));
     if (!ok) return false;
-    t = ring[s];
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) tc::mbar_arrive_local(empty + 8 * s);
-    if (++s == kRing) {
-      s = 0;
-      ph ^= 1u;
-    }
-    return t.valid != 0;
+    const Raw r = read();
+    return spread(r, t);
   }
-  // The same, called by one thread of the warp alone.
-  __device__ __forceinline__ bool next_alone(Tile &t, bool &ok) {
-    ok = wait_bar(full + 8 * s, ph, limit);
-    if (!ok) return false;
-    t = ring[s];
-    tc::mbar_arrive_local(empty + 8 * s);
+  // In two steps, for a warp that should not wait for the record: lane i < 16
+  // reads word i, later spread() gives every lane all of it.
+  struct Raw {
+    int word;
+  };
+  __device__ __forceinline__ Raw read() {
+    Raw r;
+    r.word = reinterpret_cast<const int *>(ring + s)[threadIdx.x & 15];
+    return r;
+  }
+  __device__ __forceinline__ bool spread(const Raw &r, Tile &t) {
+    int *w = reinterpret_cast<int *>(&t);
+#pragma unroll
+    for (int i = 0; i < kTileWords; ++i) w[i] = __shfl_sync(0xFFFFFFFFu, r.word, i);
+    tc::mbar_arrive_warp(empty + 8 * s);     // after every lane has its word
     if (++s == kRing) {
       s = 0;
       ph ^= 1u;
@@ -328,7 +333,8 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t *smem_p = smem_raw + (smem - smem_u32(smem_raw));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the same value in every lane, and known to be
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_cta_rank();
 
   const uint32_t staging = smem + kStages * kStageBytes;
@@ -399,141 +405,137 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     }
   } else if (live && warp == 0) {
     // ---- TMA: both CTAs load their halves; bytes complete on the leader's barrier
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      const uint32_t full0 = tc::map_rank(full, 0);
-      while (ok && feed.next_alone(t, ok)) {
-        const Job &j = p.job[KIND == kRest ? t.job : 0];
-        const bool weight = KIND == kRest && t.job > 0;
-        const uint32_t half_n = t.n >> 1;
-        const int bsel = half_n <= 16 ? 0 : half_n <= 32 ? 1 : half_n <= 64 ? 2 : 3;
-        const uint32_t bytes = kHalfBytes + (weight ? kHalfBytes : (16u << bsel) * 128u);
-        const int tail_rows = weight ? (t.rows & (kBlockK - 1)) : 0;
-        // 128 rows of an MN-major operand from row r on: 64 rows a copy, or all
-        const auto load_mn = [&](uint32_t dst, const CUtensorMap *map, int wide, bool own, uint32_t bar,
-                                 int r, int k0) {
-          if (own) {
-            if (wide) {
-              tc::tma_load_own(dst, map, bar, 0, k0, r >> 6, t.e);
-            } else {
-              tc::tma_load_own(dst, map, bar, r, k0, 0, t.e);
-              tc::tma_load_own(dst + 8192, map, bar, r + 64, k0, 0, t.e);
-            }
-          } else if (wide) {
-            tc::tma_load_pair(dst, map, bar, 0, k0, r >> 6, t.e);
+    int s = 0;
+    uint32_t ph = 0;
+    const uint32_t full0 = tc::map_rank(full, 0);
+    while (ok && feed.next(t, ok)) {
+      const Job &j = p.job[KIND == kRest ? t.job : 0];
+      const bool weight = KIND == kRest && t.job > 0;
+      const uint32_t half_n = t.n >> 1;
+      const int bsel = half_n <= 16 ? 0 : half_n <= 32 ? 1 : half_n <= 64 ? 2 : 3;
+      const uint32_t bytes = kHalfBytes + (weight ? kHalfBytes : (16u << bsel) * 128u);
+      const int tail_rows = weight ? (t.rows & (kBlockK - 1)) : 0;
+      const int m0 = t.m * 256 + (int)rank * 128, n0 = t.n0 + (int)(rank * half_n);
+      // 128 rows of an MN-major operand from row r on: 64 rows a copy, or all
+      const auto load_mn = [&](uint32_t dst, const CUtensorMap *map, int wide, bool own, uint32_t bar,
+                               int r, int k0) {
+        if (own) {
+          if (wide) {
+            tc::tma_load_own(dst, map, bar, 0, k0, r >> 6, t.e);
           } else {
-            tc::tma_load_pair(dst, map, bar, r, k0, 0, t.e);
-            tc::tma_load_pair(dst + 8192, map, bar, r + 64, k0, 0, t.e);
+            tc::tma_load_own(dst, map, bar, r, k0, 0, t.e);
+            tc::tma_load_own(dst + 8192, map, bar, r + 64, k0, 0, t.e);
           }
-        };
-        for (int kb = 0; kb < t.nk; ++kb) {
-          if (!wait_bar(empty + 8 * s, ph ^ 1u, limit)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sa = smem + s * kStageBytes, sb = sa + kHalfBytes;
-          const int k0 = (t.k0 + kb) * kBlockK;
-          uint32_t bar = full0 + 8 * s;
-          const bool own = tail_rows != 0 && kb == t.nk - 1;   // zeroed before it is full
-          if (own) {
-            bar = tail + 8 * s;
-            tc::mbar_expect_local(bar, bytes);
-          } else if (rank == 0) {
-            tc::mbar_expect_local(full + 8 * s, 2 * bytes);
-            if (kFullArrivals == 2) tc::mbar_arrive_local(full + 8 * s);
-          }
-          const int m0 = t.m * 256 + (int)rank * 128, n0 = t.n0 + (int)(rank * half_n);
-          if (KIND == kGateUp)                 // 64 gate rows and the same 64 features of up
-            tc::tma_load_pair(sa, &j.a, bar, k0, t.m * 128 + (int)rank * 64, 0, t.e);
-          else if (kAMn)
-            load_mn(sa, &j.a, j.a_wide, own, bar, m0, k0);
-          else
-            tc::tma_load_pair(sa, &j.a, bar, k0, m0, 0, t.e);
-          if (weight)
-            load_mn(sb, &j.b[0], j.b_wide, own, bar, n0, k0);
-          else
-            tc::tma_load_pair(sb, &j.b[bsel], bar, k0, n0, 0, t.e);
-          if (++s == kStages) {
-            s = 0;
-            ph ^= 1u;
-          }
+        } else if (wide) {
+          tc::tma_load_pair(dst, map, bar, 0, k0, r >> 6, t.e);
+        } else {
+          tc::tma_load_pair(dst, map, bar, r, k0, 0, t.e);
+          tc::tma_load_pair(dst + 8192, map, bar, r + 64, k0, 0, t.e);
         }
-      }
-      // the last commits on this CTA's barriers land before it may exit
-      for (int i = 0; ok && i < kStages; ++i) {
-        ok = wait_bar(empty + 8 * s, ph ^ 1u, limit);
+      };
+      for (int kb = 0; kb < t.nk; ++kb) {
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(empty + 8 * s, ph ^ 1u, limit));
+        if (!ok) break;
+        const uint32_t sa = smem + s * kStageBytes, sb = sa + kHalfBytes;
+        const int k0 = (t.k0 + kb) * kBlockK;
+        uint32_t bar = full0 + 8 * s;
+        const bool own = tail_rows != 0 && kb == t.nk - 1;   // zeroed before it is full
+        if (own) {
+          bar = tail + 8 * s;
+          tc::mbar_expect_warp(bar, bytes);
+        } else if (rank == 0) {
+          tc::mbar_expect_warp(full + 8 * s, 2 * bytes);
+          if (kFullArrivals == 2) tc::mbar_arrive_warp(full + 8 * s);
+        }
+        if (KIND == kGateUp)                 // 64 gate rows and the same 64 features of up
+          tc::tma_load_pair(sa, &j.a, bar, k0, t.m * 128 + (int)rank * 64, 0, t.e);
+        else if (kAMn)
+          load_mn(sa, &j.a, j.a_wide, own, bar, m0, k0);
+        else
+          tc::tma_load_pair(sa, &j.a, bar, k0, m0, 0, t.e);
+        if (weight)
+          load_mn(sb, &j.b[0], j.b_wide, own, bar, n0, k0);
+        else
+          tc::tma_load_pair(sb, &j.b[bsel], bar, k0, n0, 0, t.e);
         if (++s == kStages) {
           s = 0;
           ph ^= 1u;
         }
       }
     }
-    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-  } else if (live && warp == 1 && rank == 0) {
-    // ---- matrix instructions, one thread of the leading CTA.  What it needs
-    // next (the next stage, tile and accumulator) is asked for between the
-    // instructions of a stage, so that the tensor cores have work meanwhile.
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0, it = 0;
-      bool stage_ready = false, acc_ready = false;
-      bool more = feed.next_alone(t, ok);
-      while (ok && more) {
-        if (t.nk == 0) {
-          more = feed.next_alone(t, ok);
-          continue;
-        }
-        const bool bmn = KIND == kRest && t.job > 0;
-        const uint32_t buf = it & 1u;
-        const uint32_t d = tmem + buf * kTileCols;
-        const uint32_t idesc = tc::instr_desc(256, t.n, kAMn, bmn);
-        const uint32_t blead = bmn ? 8192u : 16u, bstep = bmn ? 128u : 2u;
-        // the last block of a weight gradient: no more than its tokens need
-        const int tail_rows = bmn ? (t.rows & (kBlockK - 1)) : 0;
-        if (!acc_ready) ok = wait_bar(tm_empty + 8 * buf, ((it >> 1) & 1u) ^ 1u, limit);
-        acc_ready = false;
-        tc::fence_after();
-        Tile nx;
-        bool nx_ok = true;
-        for (int kb = 0; ok && kb < t.nk; ++kb) {
-          if (!stage_ready && !wait_bar(full + 8 * s, ph, limit)) {
-            ok = false;
-            break;
-          }
-          const bool last = kb == t.nk - 1;
-          const int steps = last && tail_rows != 0 ? (tail_rows + 15) >> 4 : kBlockK / 16;
-          // zeroed by ordinary stores in either CTA: acquire those too
-          if (last && tail_rows != 0) tc::mbar_try_cluster(full + 8 * s, ph);
-          tc::fence_after();
-          const uint32_t sa = smem + s * kStageBytes, sb = sa + kHalfBytes;
-          const uint64_t da = tc::smem_desc(sa, kAMn ? 8192u : 16u);
-          const uint64_t db = tc::smem_desc(sb, blead);
-          // 16 k on: 32 bytes of a K-major line, 16 lines (2048 bytes) MN-major
-          constexpr int astep = kAMn ? 128 : 2;
-          tc::mma_pair(d, da, db, idesc, kb > 0);
-          if (steps > 1) tc::mma_pair(d, da + astep, db + bstep, idesc, 1);
-          const uint32_t stage = empty + 8 * s;
-          if (++s == kStages) {
-            s = 0;
-            ph ^= 1u;
-          }
-          // one tile ahead only: the epilogue waits for this one
-          if (kb == 0) more = feed.next_alone(nx, nx_ok);
-          const bool go_on = more && nx.nk > 0;
-          stage_ready = (!last || go_on) && tc::mbar_test(full + 8 * s, ph);
-          if (last && go_on) acc_ready = tc::mbar_test(tm_empty + 8 * (buf ^ 1u), (((it + 1) >> 1) & 1u) ^ 1u);
-          if (steps > 2) tc::mma_pair(d, da + 2 * astep, db + 2 * bstep, idesc, 1);
-          if (steps > 3) tc::mma_pair(d, da + 3 * astep, db + 3 * bstep, idesc, 1);
-          tc::mma_commit_pair(stage);
-        }
-        if (ok) tc::mma_commit_pair(tm_full + 8 * buf);
-        ok = ok && nx_ok;
-        t = nx;
-        ++it;
+    // the last commits on this CTA's barriers land before it may exit
+    for (int i = 0; ok && i < kStages; ++i) {
+      ok = __all_sync(0xFFFFFFFFu, wait_bar(empty + 8 * s, ph ^ 1u, limit));
+      if (++s == kStages) {
+        s = 0;
+        ph ^= 1u;
       }
     }
-    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+  } else if (live && warp == 1 && rank == 0) {
+    // ---- matrix instructions, one warp of the leading CTA.  What it needs
+    // next (the next stage, tile and accumulator) is asked for while the
+    // instructions of a stage run, so that the tensor cores have work meanwhile.
+    int s = 0;
+    uint32_t ph = 0, it = 0;
+    bool stage_ready = false, acc_ready = false;
+    const uint64_t desc_a0 = tc::smem_desc(smem, kAMn ? 8192u : 16u);
+    const uint64_t desc_b0 = tc::smem_desc(smem + kHalfBytes, 16u);
+    bool more = feed.next(t, ok);
+    while (ok && more) {
+      if (t.nk == 0) {
+        more = feed.next(t, ok);
+        continue;
+      }
+      const bool bmn = KIND == kRest && t.job > 0;
+      const uint32_t buf = it & 1u;
+      const uint32_t d = tmem + buf * kTileCols;
+      const uint32_t idesc = tc::instr_desc(256, t.n, kAMn, bmn);
+      // 16 k on: 32 bytes of a K-major line, 16 lines (2048 bytes) MN-major
+      constexpr uint64_t astep = kAMn ? 128 : 2;
+      const uint64_t bstep = bmn ? 128 : 2;
+      const uint64_t desc_b = desc_b0 + (bmn ? (uint64_t)((8192u - 16u) >> 4) << 16 : 0);
+      // the last block of a weight gradient: no more than its tokens need
+      const int tail_rows = bmn ? (t.rows & (kBlockK - 1)) : 0;
+      if (!acc_ready)
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(tm_empty + 8 * buf, ((it >> 1) & 1u) ^ 1u, limit));
+      acc_ready = false;
+      tc::fence_after();
+      Feed::Raw next_raw;
+      bool have = false;                     // the next tile's record is being read
+      for (int kb = 0; ok && kb < t.nk; ++kb) {
+        if (!stage_ready) {
+          ok = __all_sync(0xFFFFFFFFu, wait_bar(full + 8 * s, ph, limit));
+          if (!ok) break;
+        }
+        const bool last = kb == t.nk - 1;
+        const uint32_t steps = last && tail_rows != 0 ? (tail_rows + 15) >> 4 : kBlockK / 16;
+        // zeroed by ordinary stores in either CTA: acquire those too
+        if (last && tail_rows != 0) tc::mbar_try_cluster(full + 8 * s, ph);
+        tc::fence_after();
+        const uint64_t at = (uint64_t)(s * (kStageBytes >> 4));
+        const uint32_t stage = empty + 8 * s;
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+        // the last block asks for the next accumulator, the others for the next record
+        const uint32_t bar1 = last || have ? tm_empty + 8 * (buf ^ 1u) : feed.full + 8 * feed.s;
+        const uint32_t p1 = last || have ? (((it + 1) >> 1) & 1u) ^ 1u : feed.ph;
+        const tc::Asked r = tc::mma_stage(d, desc_a0 + at, desc_b + at, idesc, kb > 0, steps, astep, bstep,
+                                          stage, full + 8 * s, ph, bar1, p1);
+        stage_ready = __all_sync(0xFFFFFFFFu, r.first);
+        const bool second = __all_sync(0xFFFFFFFFu, r.second);
+        if (last) {
+          acc_ready = second;
+        } else if (!have && second) {
+          have = true;
+          next_raw = feed.read();
+        }
+      }
+      if (ok) tc::mma_commit_pair(tm_full + 8 * buf);
+      if (ok) more = have ? feed.spread(next_raw, t) : feed.next(t, ok);
+      ++it;
+    }
   } else if (live && warp == 2 && KIND == kRest) {
     // ---- zero the rows past the expert's count in its last block
     int s = 0;

@@ -19,9 +19,16 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t local, uint32_t rank) {
 __device__ __forceinline__ void mbar_init_at(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
-__device__ __forceinline__ void mbar_expect_local(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+// Arrive once for the whole warp, announcing `bytes`.
+__device__ __forceinline__ void mbar_expect_warp(uint32_t bar, uint32_t bytes) {
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+               "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
                : "memory");
+}
+// Arrive once for the whole warp.
+__device__ __forceinline__ void mbar_arrive_warp(uint32_t bar) {
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+               "@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_local(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -45,15 +52,6 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
                : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
-// Whether the phase is over, without waiting for it.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\t"
-               "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-               "selp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
 // The counterpart of mbar_release_cluster.
 __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -68,19 +66,27 @@ __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) 
 __device__ __forceinline__ void prefetch_map(const void *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
+// Copies and matrix instructions take their operands from the warp's uniform
+// registers.  In a branch that one lane takes alone the compiler moves each
+// operand there anew, about 70 cycles more per instruction (four matrix
+// instructions of 256 x 256 x 16: 595 cycles instead of the 512 they take).  So
+// whole warps run the loops that issue them, and these helpers pick the lane.
+
 // A tile into this CTA's shared memory; its bytes complete on `bar`, which
-// may lie in either CTA of the pair.
+// may lie in either CTA of the pair.  Called by a whole warp.
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const void *map, uint32_t bar, int c0,
                                               int c1, int c2, int c3) {
-  asm volatile("cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-               "[%0], [%1, {%3, %4, %5, %6}], [%2];"
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+               "@e cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+               "[%0], [%1, {%3, %4, %5, %6}], [%2];\n\t}"
                ::"r"(dst), "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3) : "memory");
 }
 // The same with the barrier in this CTA.
 __device__ __forceinline__ void tma_load_own(uint32_t dst, const void *map, uint32_t bar, int c0,
                                              int c1, int c2, int c3) {
-  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
-               "[%0], [%1, {%3, %4, %5, %6}], [%2];"
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+               "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+               "[%0], [%1, {%3, %4, %5, %6}], [%2];\n\t}"
                ::"r"(dst), "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3) : "memory");
 }
 __device__ __forceinline__ void tma_store(const void *map, uint32_t src, int c0, int c1, int c2,
@@ -149,25 +155,53 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading) {
   return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(leading >> 4) << 16) |
          ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-// D (+)= A B^T over 16 k, both CTAs of the pair; issued by one thread.
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile("{\n\t.reg .pred p;\n\t"
-               "setp.ne.u32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+// A stage's products on both CTAs of the pair, by a whole warp: D (+)= A B^T
+// over `steps` (1 to 4) times 16 k, `astep` and `bstep` apart in the
+// descriptors; then arrive on `done`, at that offset in both CTAs, when they
+// and everything before them are finished.  Between the instructions it asks
+// whether phases `p0` of barrier `bar0` and `p1` of `bar1` are over; reading a
+// barrier takes about 200 cycles beside the tensor cores' own reads, which
+// pass while the instructions run.
+struct Asked {
+  uint32_t first, second;
+};
+__device__ __forceinline__ Asked mma_stage(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate, uint32_t steps, uint64_t astep,
+                                           uint64_t bstep, uint32_t done, uint32_t bar0, uint32_t p0,
+                                           uint32_t bar1, uint32_t p1) {
+  Asked r;
+  asm volatile("{\n\t.reg .pred e, e1, e2, e3, c, q0, q1;\n\t"
+               ".reg .b64 a1, b1, a2, b2, a3, b3;\n\t"
+               "elect.sync _|e, 0xFFFFFFFF;\n\t"
+               "setp.ne.u32 c, %6, 0;\n\t"
+               "setp.gt.and.u32 e1, %7, 1, e;\n\t"
+               "setp.gt.and.u32 e2, %7, 2, e;\n\t"
+               "setp.gt.and.u32 e3, %7, 3, e;\n\t"
+               "add.s64 a1, %3, %8;\n\tadd.s64 b1, %4, %9;\n\t"
+               "add.s64 a2, a1, %8;\n\tadd.s64 b2, b1, %9;\n\t"
+               "add.s64 a3, a2, %8;\n\tadd.s64 b3, b2, %9;\n\t"
+               "@e tcgen05.mma.cta_group::2.kind::f16 [%2], %3, %4, %5, c;\n\t"
+               "mbarrier.test_wait.parity.shared::cta.b64 q0, [%11], %12;\n\t"
+               "mbarrier.test_wait.parity.shared::cta.b64 q1, [%13], %14;\n\t"
+               "@e1 tcgen05.mma.cta_group::2.kind::f16 [%2], a1, b1, %5, 1;\n\t"
+               "@e2 tcgen05.mma.cta_group::2.kind::f16 [%2], a2, b2, %5, 1;\n\t"
+               "@e3 tcgen05.mma.cta_group::2.kind::f16 [%2], a3, b3, %5, 1;\n\t"
+               "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+               "[%10], %15;\n\t"
+               "selp.u32 %0, 1, 0, q0;\n\t"
+               "selp.u32 %1, 1, 0, q1;\n\t}"
+               : "=r"(r.first), "=r"(r.second)
+               : "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(steps), "l"(astep), "l"(bstep),
+                 "r"(done), "r"(bar0), "r"(p0), "r"(bar1), "r"(p1), "h"((uint16_t)3)
+               : "memory");
+  return r;
 }
-// Arrive on the barrier at this offset in both CTAs once every earlier
-// matrix instruction of this thread is done.
+// Arrive on the barrier at this offset in both CTAs once every earlier matrix
+// instruction of this warp is done.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-               "[%0], %1;" ::"r"(bar), "h"((uint16_t)3) : "memory");
-}
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(p));
-  return p != 0;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+               "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+               "[%0], %1;\n\t}" ::"r"(bar), "h"((uint16_t)3) : "memory");
 }
 
 }  // namespace tc
