@@ -123,7 +123,6 @@ struct alignas(16) Tile {
   int reserved[2];
 };
 static_assert(sizeof(Tile) == 64, "a tile's record is 64 bytes");
-constexpr int kTileWords = 14;
 
 // The launch's units of work in order: tiles of the row product by expert
 // (each `split` times, once per part of the contraction), then the weight
@@ -278,15 +277,19 @@ struct Feed {
   __device__ __forceinline__ Feed(const Tile *ring_, uint32_t full_, uint32_t empty_, uint64_t limit_)
       : ring(ring_), full(full_), empty(empty_), limit(limit_), s(0), ph(0) {}
   // The next tile; false when there is none, or (ok false) when the wait ran
-  // out.  Called by the whole warp; every lane gets the same values.
+  // out.  Called by the whole warp.
   __device__ __forceinline__ bool next(Tile &t, bool &ok) {
     ok = __all_sync(0xFFFFFFFFu, wait_bar(full + 8 * s, ph, limit));
     if (!ok) return false;
-    const Raw r = read();
-    return spread(r, t);
+    t = ring[s];
+    __syncwarp();
+    done();
+    return t.valid != 0;
   }
-  // In two steps, for a warp that should not wait for the record: lane i < 16
-  // reads word i, later spread() gives every lane all of it.
+  // The same for the words of WORDS (a bit each) alone, through shuffles, so
+  // that the compiler knows the values to be the same in every lane.  In two
+  // steps, for a warp that should not wait for the record: lane i < 16 reads
+  // word i, spread() gives every lane all of them later.
   struct Raw {
     int word;
   };
@@ -295,18 +298,36 @@ struct Feed {
     r.word = reinterpret_cast<const int *>(ring + s)[threadIdx.x & 15];
     return r;
   }
+  template <uint32_t WORDS>
   __device__ __forceinline__ bool spread(const Raw &r, Tile &t) {
     int *w = reinterpret_cast<int *>(&t);
 #pragma unroll
-    for (int i = 0; i < kTileWords; ++i) w[i] = __shfl_sync(0xFFFFFFFFu, r.word, i);
-    tc::mbar_arrive_warp(empty + 8 * s);     // after every lane has its word
+    for (int i = 0; i < 16; ++i)
+      if ((WORDS >> i) & 1u) w[i] = __shfl_sync(0xFFFFFFFFu, r.word, i);
+    done();
+    return t.valid != 0;
+  }
+  template <uint32_t WORDS>
+  __device__ __forceinline__ bool next_uniform(Tile &t, bool &ok) {
+    ok = __all_sync(0xFFFFFFFFu, wait_bar(full + 8 * s, ph, limit));
+    if (!ok) return false;
+    return spread<WORDS>(read(), t);
+  }
+
+ private:
+  __device__ __forceinline__ void done() {     // every lane has read the record
+    tc::mbar_arrive_warp(empty + 8 * s);
     if (++s == kRing) {
       s = 0;
       ph ^= 1u;
     }
-    return t.valid != 0;
   }
 };
+// Words of a record: what the copies and what the matrix instructions need.
+constexpr uint32_t kValid = 1u << 0, kJob = 1u << 1, kExpert = 1u << 2, kRows = 1u << 3, kM = 1u << 4,
+                   kN0 = 1u << 5, kN = 1u << 6, kK0 = 1u << 8, kNk = 1u << 9;
+constexpr uint32_t kCopyWords = kValid | kJob | kExpert | kRows | kM | kN0 | kN | kK0 | kNk;
+constexpr uint32_t kMathWords = kValid | kJob | kRows | kN | kNk;
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -408,7 +429,7 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     int s = 0;
     uint32_t ph = 0;
     const uint32_t full0 = tc::map_rank(full, 0);
-    while (ok && feed.next(t, ok)) {
+    while (ok && feed.next_uniform<kCopyWords>(t, ok)) {
       const Job &j = p.job[KIND == kRest ? t.job : 0];
       const bool weight = KIND == kRest && t.job > 0;
       const uint32_t half_n = t.n >> 1;
@@ -480,10 +501,10 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     bool stage_ready = false, acc_ready = false;
     const uint64_t desc_a0 = tc::smem_desc(smem, kAMn ? 8192u : 16u);
     const uint64_t desc_b0 = tc::smem_desc(smem + kHalfBytes, 16u);
-    bool more = feed.next(t, ok);
+    bool more = feed.next_uniform<kMathWords>(t, ok);
     while (ok && more) {
       if (t.nk == 0) {
-        more = feed.next(t, ok);
+        more = feed.next_uniform<kMathWords>(t, ok);
         continue;
       }
       const bool bmn = KIND == kRest && t.job > 0;
@@ -533,7 +554,7 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
         }
       }
       if (ok) tc::mma_commit_pair(tm_full + 8 * buf);
-      if (ok) more = have ? feed.spread(next_raw, t) : feed.next(t, ok);
+      if (ok) more = have ? feed.spread<kMathWords>(next_raw, t) : feed.next_uniform<kMathWords>(t, ok);
       ++it;
     }
   } else if (live && warp == 2 && KIND == kRest) {
