@@ -391,7 +391,8 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
   if (warp == 2) tc::tmem_alloc_pair(tm_slot, kTmemCols);
   tc::fence_before();
   __syncthreads();
-  cluster_barrier();
+  cluster_arrive_relaxed();              // the barriers' initial values are released above
+  cluster_wait();
   tc::fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem_p + kBarOff + 24 * kStages + 32);
 
@@ -406,12 +407,13 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
   Tile t;
   Feed feed(ring, rec_full, rec_empty, limit);
 
-  if (live && warp == 3) {
-    // ---- scheduling: one warp finds the pair's tiles, up to kRing ahead
+  if (warp == 3) {
+    // ---- scheduling: one warp finds the pair's tiles, up to kRing ahead (the
+    // first counts are read together with the status)
     Schedule<KIND> sched(p);
     int s = 0;
     uint32_t ph = 0;
-    for (int64_t i = blockIdx.x >> 1; ok; i += gridDim.x >> 1) {
+    for (int64_t i = blockIdx.x >> 1; live && ok; i += gridDim.x >> 1) {
       t.valid = sched.find(i, t);
       ok = __all_sync(0xFFFFFFFFu, wait_bar(rec_empty + 8 * s, ph ^ 1u, limit));
       if (ok && lane == 0) {
@@ -779,10 +781,14 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
       for (int i = 0; i < 1000; ++i) __nanosleep(10000);
     }
   }
+  // Neither CTA leaves while the other may still use its shared or tensor
+  // memory or its barriers; nothing is handed over, so nothing is released.
   __syncwarp();
   tc::fence_before();
   __syncthreads();
-  cluster_barrier();
+  cluster_arrive_relaxed();
+  cluster_wait();
+  tc::fence_after();
   if (warp == 2) tc::tmem_free_pair(tmem, kTmemCols);
 }
 
