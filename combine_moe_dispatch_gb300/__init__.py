@@ -339,12 +339,12 @@ def clip_grad_norm(grads, outs, max_norm: float, total_norm, workspace, stream=N
                                                  sizes != list(map(numel, outs)))):
         return _check(Status.INVALID_ARG, "moe_clip_grad_norm", check)
     codes = {torch.bfloat16: 0, torch.float32: 1}
-    table = array.array("q", bytes(32 * n))               # moe_grad_tensor, 32 bytes each
-    at = list(map(ptr, grads))
-    table[0::4] = array.array("q", at)
-    table[1::4] = array.array("q", at if outs is grads else list(map(ptr, outs)))
-    table[2::4] = array.array("q", sizes)
-    table[3::4] = array.array("q", [codes.get(t, 0x7FFFFFFF) for t in types])
+    words = [0] * (4 * n)                                 # moe_grad_tensor, 32 bytes each
+    words[0::4] = list(map(ptr, grads))
+    words[1::4] = words[0::4] if outs is grads else list(map(ptr, outs))
+    words[2::4] = sizes
+    words[3::4] = [codes.get(t, 0x7FFFFFFF) for t in types]
+    table = array.array("q", words)
     st = load_library().moe_clip_grad_norm(table.buffer_info()[0], n, max_norm, _ptr(total_norm),
                                            _ptr(workspace),
                                            workspace.numel() * workspace.element_size(),
