@@ -413,8 +413,15 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     Schedule<KIND> sched(p);
     int s = 0;
     uint32_t ph = 0;
-    for (int64_t i = blockIdx.x >> 1; live && ok; i += gridDim.x >> 1) {
-      t.valid = sched.find(i, t);
+    // In round r, pair q takes unit (q + r) mod pairs of the round: an expert's
+    // tiles are not all of one size, and without the turn a pair would get the
+    // same place among them in every round (4 tiles per feature tile, 76 pairs:
+    // 960 rows per expert took as long as 1024).
+    const int pairs = gridDim.x >> 1;
+    int turn = blockIdx.x >> 1;
+    for (int64_t round = 0; live && ok; round += pairs) {
+      t.valid = sched.find(round + turn, t);
+      if (++turn == pairs) turn = 0;
       ok = __all_sync(0xFFFFFFFFu, wait_bar(rec_empty + 8 * s, ph ^ 1u, limit));
       if (ok && lane == 0) {
         ring[s] = t;
