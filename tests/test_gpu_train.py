@@ -211,3 +211,59 @@ def test_clip_many_tensors_repeats_and_special_values():
     g[1][77] = float("inf")
     assert bool(torch.isinf(_clip(g, outs, 1.0, ws)).all())
     assert bool((outs[0] == 0).all()) and bool(torch.isnan(outs[1][77]))
+
+
+def _example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "train_moe_layer.py")
+    spec = importlib.util.spec_from_file_location("train_moe_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+def test_layer_gradients_against_autograd():
+    """The example's layer against automatic differentiation in 64 bits with
+    the same routing.  At most eight roundings to bf16, 2^-8 relative each at
+    most, lie between an input and a gradient (h, a, expert_y, y; d_expert_y,
+    dh, d_expert_x, d_x); to first order, and in norm, a gradient is off by no
+    more than eight of them: 2^-5."""
+    import combine_moe_dispatch_gb300 as moe
+    N, H, I, E, K = 96, 128, 192, 8, 2
+    layer = _example().MoELayer(N, H, I, E, K, seed=3)
+    x = _normal((N, H), 1.0, 21)
+    d_y = _normal((N, H), 0.1, 22)
+    y = layer.forward(x).clone()
+    d_x = layer.backward(d_y)
+    assert moe.read_status(layer.b.workspace) == moe.Status.OK
+    x64 = x.to(D).requires_grad_()
+    ps = [p.to(D).requires_grad_() for p in layer.params]
+    idx = layer.topk_idx.long()
+    w = torch.softmax((x64 @ ps[0].t()).gather(1, idx), 1)
+    want = torch.zeros((N, H), dtype=D, device="cuda")
+    for k in range(K):
+        gu = torch.einsum("nh,nfh->nf", x64, ps[1][idx[:, k]])
+        a = torch.nn.functional.silu(gu[:, :I]) * gu[:, I:]
+        want = want + w[:, k:k + 1] * torch.einsum("ni,nhi->nh", a, ps[2][idx[:, k]])
+    want.backward(d_y.to(D))
+    for got, ref, what in [(y, want.detach(), "y"), (d_x, x64.grad, "d_x"),
+                           *[(g, p.grad, f"gradient {i}") for i, (g, p) in enumerate(zip(layer.grads, ps))]]:
+        assert float((got.to(D) - ref).norm()) <= 2.0 ** -5 * float(ref.norm()), what
+
+
+def test_example_learns():
+    """A few clipped gradient steps of the example lower its loss, and every
+    norm that it reports is the norm of its gradients."""
+    layer = _example().MoELayer(128, 256, 256, 8, 2, seed=5)
+    x, target = _normal((128, 256), 1.0, 31), _normal((128, 256), 1.0, 32, torch.float32)
+    losses = []
+    for _ in range(12):
+        diff = layer.forward(x).float() - target
+        losses.append(float(diff.square().mean()))
+        layer.backward((diff / 128).bfloat16())
+        norm = sum(float(g.to(D).square().sum()) for g in layer.grads) ** 0.5
+        layer.step(lr=0.5, max_norm=1.0)
+        assert abs(float(layer.grad_norm) - norm) <= 2.0 ** -16 * norm
+    assert losses[-1] < losses[0]
