@@ -384,14 +384,16 @@ static moe_status ffn_check(const moe_shape *shape, int32_t intermediate, const 
 size_t moe_ffn_workspace_size(const moe_shape *shape, int32_t intermediate) {
   const size_t plan = moe_workspace_size(shape);
   if (plan == 0 || intermediate <= 0) return 0;
-  return plan + ffn_scratch_bytes(shape->num_experts, shape->capacity, shape->hidden, intermediate);
+  return plan + ffn_scratch(shape->num_experts, shape->capacity, shape->hidden, intermediate).total;
 }
 
 // The scratch lies past the plan's part of the workspace (a multiple of 256 bytes).
-static void ffn_scratch(FfnParams &f, const moe_shape *shape, void *workspace) {
+static void set_scratch(FfnParams &f, const moe_shape *shape, int32_t intermediate, void *workspace) {
+  const FfnScratch s = ffn_scratch(shape->num_experts, shape->capacity, shape->hidden, intermediate);
   char *base = static_cast<char *>(workspace) + ws_layout(*shape).total;
   f.tickets = reinterpret_cast<uint32_t *>(base);
-  f.part = reinterpret_cast<float *>(base + kTicketBytes);
+  f.part = reinterpret_cast<float *>(base + s.part_off);
+  f.row_maps = reinterpret_cast<void *>(align_up((uintptr_t)(base + s.maps_off), 128));
 }
 
 moe_status moe_ffn(const moe_shape *shape, int32_t intermediate, const void *expert_x,
@@ -407,7 +409,7 @@ moe_status moe_ffn(const moe_shape *shape, int32_t intermediate, const void *exp
       !aligned(expert_num_tokens, 4))
     return MOE_ERR_ALIGNMENT;
   FfnParams f = {};
-  ffn_scratch(f, shape, workspace);
+  set_scratch(f, shape, intermediate, workspace);
   f.counts = expert_num_tokens;
   f.hdr = header(workspace);
   f.E = shape->num_experts;
@@ -439,7 +441,7 @@ moe_status moe_ffn_backward(const moe_shape *shape, int32_t intermediate, const 
       !aligned(d_w_down, 16) || !aligned(expert_num_tokens, 4))
     return MOE_ERR_ALIGNMENT;
   FfnParams f = {};
-  ffn_scratch(f, shape, workspace);
+  set_scratch(f, shape, intermediate, workspace);
   f.counts = expert_num_tokens;
   f.hdr = header(workspace);
   f.E = shape->num_experts;

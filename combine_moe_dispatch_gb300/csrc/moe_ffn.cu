@@ -24,8 +24,9 @@
 //  - Weight gradients ("weight" modes) contract over the expert's tokens;
 //    both operands are then read with the contraction as the outer dimension
 //    (MN-major shared-memory tiles).  Rows past count[e] are not the
-//    expert's and may hold anything, NaN included, so the last block of 64
-//    tokens is zeroed in shared memory past the count before it is used.
+//    expert's and may hold anything, NaN included: the kernel before writes,
+//    for every expert, tensor maps that end at its count, and the copies fill
+//    the rest of the last block of 64 tokens with zeros.
 // Counts are read on the device: nothing waits for the host, and the call can
 // be captured in a CUDA graph.  Tiles go to the pairs round robin.
 //
@@ -49,7 +50,7 @@ namespace {
 // one another, as one list of tiles.
 enum Kind { kGateUp = 0, kDown = 1, kActGrad = 2, kRest = 3 };
 
-constexpr int kPairThreads = 384;      // warps: 0 TMA, 1 MMA, 2 zeroes tails, 3 scheduling, 4-11 epilogue
+constexpr int kPairThreads = 384;      // warps: 0 TMA, 1 MMA, 2 maps, 3 scheduling, 4-11 epilogue
 constexpr int kEpiWarps = 8;           // two groups of four; each takes every other chunk of columns
 constexpr int kStages = 6;
 constexpr int kBlockK = 64;            // one 128-byte swizzled line of bf16
@@ -59,7 +60,8 @@ constexpr uint32_t kStagingBytes = 2 * 16384;            // epilogue, one buffer
 constexpr uint32_t kBarOff = kStages * kStageBytes + kStagingBytes;
 constexpr int kRing = 4;                                 // tiles announced ahead
 constexpr uint32_t kRingOff = kBarOff + 256;
-constexpr uint32_t kPairSmem = kRingOff + kRing * 64 + 1024;   // + alignment slack
+constexpr uint32_t kMapOff = kRingOff + kRing * 64;      // kActGrad: a tensor map being written
+constexpr uint32_t kPairSmem = kMapOff + 128 + 1024;     // + alignment slack
 static_assert(kPairSmem <= 232448, "shared memory of one CTA");
 constexpr int kTileCols = 256;
 constexpr uint32_t kTmemCols = 512;                      // two accumulators of 256 columns
@@ -80,6 +82,17 @@ struct Job {
   int a_wide, b_wide;      // MN-major operands: a copy brings 128 rows (else 64) x 64 k
 };
 
+// The operands of the weight gradients, dh and x of dWgu, dy and a of dWd: their
+// tensor maps, and those that end at each expert's count, [4][E] in the
+// workspace.  Written by kActGrad, read by kRest.
+constexpr int kRowMaps = 4;
+template <int KIND>
+struct RowMaps {};
+template <>
+struct RowMaps<kActGrad> {
+  CUtensorMap whole[kRowMaps];
+};
+
 template <int KIND>
 struct PairParams {
   static constexpr int kJobs = KIND == kRest ? 3 : 1;
@@ -88,6 +101,8 @@ struct PairParams {
   WsHeader *hdr;
   float *part;             // partial sums of split contractions
   uint32_t *tickets;       // one per tile and CTA of the pair; zero between calls
+  CUtensorMap *row_maps;   // [4][E], or null
+  RowMaps<KIND> maps;
   int E, cap;
 };
 
@@ -348,9 +363,6 @@ template <int KIND>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
 pair_kernel(const __grid_constant__ PairParams<KIND> p) {
   constexpr bool kAMn = KIND == kActGrad || KIND == kRest;
-  // A stage is full after one arrival, the leader's, and the bytes of both
-  // CTAs; a stage whose tail is zeroed, after each CTA's zeroing warp.
-  constexpr uint32_t kFullArrivals = KIND == kRest ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t *smem_p = smem_raw + (smem - smem_u32(smem_raw));
@@ -360,19 +372,18 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
 
   const uint32_t staging = smem + kStages * kStageBytes;
   const uint32_t bars = smem + kBarOff;
-  const uint32_t full = bars, empty = bars + 8 * kStages, tail = bars + 16 * kStages;
-  const uint32_t tm_full = bars + 24 * kStages, tm_empty = tm_full + 16;
+  const uint32_t full = bars, empty = bars + 8 * kStages;
+  const uint32_t tm_full = bars + 16 * kStages, tm_empty = tm_full + 16;
   const uint32_t tm_slot = tm_empty + 16;
   // barriers of the ring of tiles
   const uint32_t rec_full = bars + 192, rec_empty = bars + 224;
   Tile *ring = reinterpret_cast<Tile *>(smem_p + kRingOff);
-  volatile uint32_t *last_in = reinterpret_cast<uint32_t *>(smem_p + kBarOff + 24 * kStages + 40);
+  volatile uint32_t *last_in = reinterpret_cast<uint32_t *>(smem_p + kBarOff + 16 * kStages + 40);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      tc::mbar_init_at(full + 8 * s, kFullArrivals);
+      tc::mbar_init_at(full + 8 * s, 1);     // the leader's arrival, and the bytes of both CTAs
       tc::mbar_init_at(empty + 8 * s, 1);    // the commit of the stage's instructions
-      tc::mbar_init_at(tail + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init_at(tm_full + 8 * b, 1);
@@ -380,8 +391,8 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     }
     for (int r = 0; r < kRing; ++r) {
       tc::mbar_init_at(rec_full + 8 * r, 1);
-      // TMA, epilogue, and where they run the MMA and the zeroing warp
-      tc::mbar_init_at(rec_empty + 8 * r, kEpiWarps + 1 + (rank == 0 ? 1 : 0) + (KIND == kRest ? 1 : 0));
+      // TMA, epilogue, and in the leader the MMA warp
+      tc::mbar_init_at(rec_empty + 8 * r, kEpiWarps + 1 + (rank == 0 ? 1 : 0));
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   } else if (threadIdx.x == 32 && p.job[0].mt > 0) {
@@ -394,7 +405,7 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
   cluster_arrive_relaxed();              // the barriers' initial values are released above
   cluster_wait();
   tc::fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem_p + kBarOff + 24 * kStages + 32);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem_p + kBarOff + 16 * kStages + 32);
 
   pdl_allow_dependents();
   pdl_wait_for_previous();
@@ -438,25 +449,27 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     int s = 0;
     uint32_t ph = 0;
     const uint32_t full0 = tc::map_rank(full, 0);
+    const CUtensorMap *held = nullptr;       // kRest: the maps acquired last
     while (ok && feed.next_uniform<kCopyWords>(t, ok)) {
       const Job &j = p.job[KIND == kRest ? t.job : 0];
       const bool weight = KIND == kRest && t.job > 0;
       const uint32_t half_n = t.n >> 1;
       const int bsel = half_n <= 16 ? 0 : half_n <= 32 ? 1 : half_n <= 64 ? 2 : 3;
       const uint32_t bytes = kHalfBytes + (weight ? kHalfBytes : (16u << bsel) * 128u);
-      const int tail_rows = weight ? (t.rows & (kBlockK - 1)) : 0;
       const int m0 = t.m * 256 + (int)rank * 128, n0 = t.n0 + (int)(rank * half_n);
+      const CUtensorMap *map_a = &j.a, *map_b = &j.b[bsel];
+      if (weight) {                          // the expert's own maps, which end at its count
+        map_a = p.row_maps + (int64_t)(2 * (t.job - 1)) * p.E + t.e;
+        map_b = map_a + p.E;
+        if (map_a != held && t.nk > 0) {
+          tc::map_acquire(map_a);
+          tc::map_acquire(map_b);
+          held = map_a;
+        }
+      }
       // 128 rows of an MN-major operand from row r on: 64 rows a copy, or all
-      const auto load_mn = [&](uint32_t dst, const CUtensorMap *map, int wide, bool own, uint32_t bar,
-                               int r, int k0) {
-        if (own) {
-          if (wide) {
-            tc::tma_load_own(dst, map, bar, 0, k0, r >> 6, t.e);
-          } else {
-            tc::tma_load_own(dst, map, bar, r, k0, 0, t.e);
-            tc::tma_load_own(dst + 8192, map, bar, r + 64, k0, 0, t.e);
-          }
-        } else if (wide) {
+      const auto load_mn = [&](uint32_t dst, const CUtensorMap *map, int wide, uint32_t bar, int r, int k0) {
+        if (wide) {
           tc::tma_load_pair(dst, map, bar, 0, k0, r >> 6, t.e);
         } else {
           tc::tma_load_pair(dst, map, bar, r, k0, 0, t.e);
@@ -468,25 +481,18 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
         if (!ok) break;
         const uint32_t sa = smem + s * kStageBytes, sb = sa + kHalfBytes;
         const int k0 = (t.k0 + kb) * kBlockK;
-        uint32_t bar = full0 + 8 * s;
-        const bool own = tail_rows != 0 && kb == t.nk - 1;   // zeroed before it is full
-        if (own) {
-          bar = tail + 8 * s;
-          tc::mbar_expect_warp(bar, bytes);
-        } else if (rank == 0) {
-          tc::mbar_expect_warp(full + 8 * s, 2 * bytes);
-          if (kFullArrivals == 2) tc::mbar_arrive_warp(full + 8 * s);
-        }
+        const uint32_t bar = full0 + 8 * s;
+        if (rank == 0) tc::mbar_expect_warp(full + 8 * s, 2 * bytes);
         if (KIND == kGateUp)                 // 64 gate rows and the same 64 features of up
-          tc::tma_load_pair(sa, &j.a, bar, k0, t.m * 128 + (int)rank * 64, 0, t.e);
+          tc::tma_load_pair(sa, map_a, bar, k0, t.m * 128 + (int)rank * 64, 0, t.e);
         else if (kAMn)
-          load_mn(sa, &j.a, j.a_wide, own, bar, m0, k0);
+          load_mn(sa, map_a, j.a_wide, bar, m0, k0);
         else
-          tc::tma_load_pair(sa, &j.a, bar, k0, m0, 0, t.e);
+          tc::tma_load_pair(sa, map_a, bar, k0, m0, 0, t.e);
         if (weight)
-          load_mn(sb, &j.b[0], j.b_wide, own, bar, n0, k0);
+          load_mn(sb, map_b, j.b_wide, bar, n0, k0);
         else
-          tc::tma_load_pair(sb, &j.b[bsel], bar, k0, n0, 0, t.e);
+          tc::tma_load_pair(sb, map_b, bar, k0, n0, 0, t.e);
         if (++s == kStages) {
           s = 0;
           ph ^= 1u;
@@ -539,8 +545,6 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
         }
         const bool last = kb == t.nk - 1;
         const uint32_t steps = last && tail_rows != 0 ? (tail_rows + 15) >> 4 : kBlockK / 16;
-        // zeroed by ordinary stores in either CTA: acquire those too
-        if (last && tail_rows != 0) tc::mbar_try_cluster(full + 8 * s, ph);
         tc::fence_after();
         const uint64_t at = (uint64_t)(s * (kStageBytes >> 4));
         const uint32_t stage = empty + 8 * s;
@@ -566,29 +570,15 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
       if (ok) more = have ? feed.spread<kMathWords>(next_raw, t) : feed.next_uniform<kMathWords>(t, ok);
       ++it;
     }
-  } else if (live && warp == 2 && KIND == kRest) {
-    // ---- zero the rows past the expert's count in its last block
-    int s = 0;
-    uint32_t phases = 0;
-    const uint32_t full0 = tc::map_rank(full, 0);
-    while (ok && feed.next(t, ok)) {
-      if (t.nk == 0) continue;
-      const int last = (s + t.nk - 1) % kStages;
-      s = (s + t.nk) % kStages;
-      const int valid = t.job > 0 ? (t.rows & (kBlockK - 1)) : 0;
-      if (valid == 0) continue;
-      ok = wait_bar(tail + 8 * last, (phases >> last) & 1u, limit);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      phases ^= 1u << last;
-      if (!ok) break;
-      uint8_t *base = smem_p + last * kStageBytes;
-      // up to the next multiple of 16, the k of one matrix instruction
-      for (int c = 0; c < 4; ++c)
-        for (int j = valid * 8 + lane; j < ((valid + 15) & ~15) * 8; j += 32)
-          *reinterpret_cast<uint4 *>(base + c * 8192 + j * 16) = make_uint4(0, 0, 0, 0);
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_release_cluster(full0 + 8 * last);
+  } else if (live && warp == 2 && KIND == kActGrad) {
+    // ---- the weight gradients' tensor maps: each block writes some experts'
+    if constexpr (KIND == kActGrad) {
+      if (p.row_maps)
+        for (int i = blockIdx.x; i < kRowMaps * p.E; i += gridDim.x) {
+          const int e = i % p.E, rows = rows_of(p, e);
+          if (rows > 0)                      // an expert without rows has nothing to copy
+            tc::map_with_rows(p.row_maps + i, &p.maps.whole[i / p.E], smem_p + kMapOff, (uint32_t)rows);
+        }
     }
   } else if (live && warp >= 4) {
     // ---- epilogue: tensor memory -> registers -> shared memory -> results
@@ -884,6 +874,7 @@ PairParams<KIND> base_params(const FfnParams &f) {
   p.hdr = f.hdr;
   p.part = f.part;
   p.tickets = f.tickets;
+  p.row_maps = f.dw_gate_up || f.dw_down ? static_cast<CUtensorMap *>(f.row_maps) : nullptr;
   p.E = f.E;
   p.cap = f.cap;
   return p;
@@ -906,11 +897,16 @@ int64_t units(const Job &j, const FfnParams &f) {
 
 }  // namespace
 
-size_t ffn_scratch_bytes(int64_t E, int64_t cap, int64_t H, int64_t I) {
+FfnScratch ffn_scratch(int64_t E, int64_t cap, int64_t H, int64_t I) {
   const int64_t mt = cdiv(I, 128) > cdiv(H, 256) ? cdiv(I, 128) : cdiv(H, 256);
   const int64_t most = mt * E * cdiv(cap, kTileCols) * kMaxSplit;
   const int64_t cols = cap < kTileCols ? (cap + 31) / 32 * 32 : kTileCols;
-  return kTicketBytes + (size_t)((most < kMaxPairs ? most : kMaxPairs) * cols) * 256 * sizeof(float);
+  FfnScratch s;
+  s.part_off = kMaxPairs * 2 * sizeof(uint32_t);
+  s.maps_off = s.part_off + (size_t)((most < kMaxPairs ? most : kMaxPairs) * cols) * 256 * sizeof(float);
+  // the caller's workspace is aligned to 16 bytes, a tensor map to 128
+  s.total = s.maps_off + 128 + (size_t)(kRowMaps * E) * sizeof(CUtensorMap);
+  return s;
 }
 
 cudaError_t launch_ffn(const FfnParams &f, cudaStream_t stream) {
@@ -940,11 +936,18 @@ cudaError_t launch_ffn(const FfnParams &f, cudaStream_t stream) {
 
 cudaError_t launch_ffn_backward(const FfnParams &f, cudaStream_t stream) {
   const int64_t I2 = 2 * (int64_t)f.I;
+  // what the weight gradients contract: dh and x, dy and a
+  const void *operand[kRowMaps] = {f.dh, f.x, f.dy, f.act};
+  const int64_t width[kRowMaps] = {I2, f.H, f.H, f.I};
+  int wide[kRowMaps];
   {
     PairParams<kActGrad> p = base_params<kActGrad>(f);       // dh and a
     Job &j = p.job[0];
     if (!make_map_mn(&j.a, &j.a_wide, f.w_down, f.I, f.H, f.E) || !token_maps(j, f.dy, f.H, f.cap, f.E))
       return cudaErrorInvalidValue;
+    for (int i = 0; i < kRowMaps; ++i)
+      if (!make_map_mn(&p.maps.whole[i], &wide[i], operand[i], width[i], f.cap, f.E))
+        return cudaErrorInvalidValue;
     j.o0 = f.act;
     j.o1 = f.dh;
     j.h = f.h;
@@ -971,11 +974,10 @@ cudaError_t launch_ffn_backward(const FfnParams &f, cudaStream_t stream) {
     uint16_t *out = w ? f.dw_down : f.dw_gate_up;
     if (!out) continue;
     Job &j = p.job[1 + w];
-    const int64_t M = w ? f.H : I2, N = w ? f.I : f.H;
-    if (!make_map_mn(&j.a, &j.a_wide, w ? (const void *)f.dy : f.dh, M, f.cap, f.E) ||
-        !make_map_mn(&j.b[0], &j.b_wide, w ? (const void *)f.act : f.x, N, f.cap, f.E) ||
-        !make_map(&j.out, out, N, M, 1, f.E, 32))
-      return cudaErrorInvalidValue;
+    const int64_t M = width[2 * w], N = width[2 * w + 1];
+    if (!make_map(&j.out, out, N, M, 1, f.E, 32)) return cudaErrorInvalidValue;
+    j.a_wide = wide[2 * w];
+    j.b_wide = wide[2 * w + 1];
     j.M = (int)M;
     j.N = (int)N;
     j.mt = (int)cdiv(M, 256);

@@ -11,8 +11,9 @@ namespace moe {
 struct FfnParams {
   const int32_t *counts;         // [E] rows per expert, or null (cap each)
   WsHeader *hdr;
-  float *part;                   // scratch of ffn_scratch_bytes(): tickets, then partial sums
-  uint32_t *tickets;
+  uint32_t *tickets;             // scratch, see FfnScratch
+  float *part;
+  void *row_maps;
   int E, cap, H, I;
   const uint16_t *x;             // [E, cap, H]
   const uint16_t *w_gate_up;     // [E, 2I, H]
@@ -27,10 +28,12 @@ struct FfnParams {
   uint16_t *dw_down;             // [E, H, I]
 };
 
-// Scratch past the plan's workspace: kTicketBytes of tickets, zero between
-// calls, then the partial sums of split contractions.
-constexpr size_t kTicketBytes = 1024;
-size_t ffn_scratch_bytes(int64_t E, int64_t cap, int64_t H, int64_t I);
+// Scratch past the plan's part of the workspace: tickets, zero between calls;
+// the partial sums of split contractions; the backward pass's tensor maps.
+struct FfnScratch {
+  size_t part_off, maps_off, total;
+};
+FfnScratch ffn_scratch(int64_t E, int64_t cap, int64_t H, int64_t I);
 
 cudaError_t launch_ffn(const FfnParams &p, cudaStream_t stream);
 cudaError_t launch_ffn_backward(const FfnParams &p, cudaStream_t stream);

@@ -38,12 +38,6 @@ __device__ __forceinline__ void mbar_arrive_local(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The same, releasing this thread's earlier writes to the whole cluster.  A
-// release at cluster scope waits for the thread's outstanding memory
-// operations: for rare arrivals only.
-__device__ __forceinline__ void mbar_release_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile("{\n\t.reg .pred p;\n\t"
@@ -52,16 +46,6 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
                : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
-// The counterpart of mbar_release_cluster.
-__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\t"
-               "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-               "selp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
-
 // --- TMA ---
 __device__ __forceinline__ void prefetch_map(const void *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -81,13 +65,24 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const void *map, uin
                "[%0], [%1, {%3, %4, %5, %6}], [%2];\n\t}"
                ::"r"(dst), "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3) : "memory");
 }
-// The same with the barrier in this CTA.
-__device__ __forceinline__ void tma_load_own(uint32_t dst, const void *map, uint32_t bar, int c0,
-                                             int c1, int c2, int c3) {
-  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
-               "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
-               "[%0], [%1, {%3, %4, %5, %6}], [%2];\n\t}"
-               ::"r"(dst), "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3) : "memory");
+// A copy of the tensor map `map` in global memory at `out` whose dimension 1
+// has `rows` elements; `tmp` is 128 bytes of this CTA's shared memory.  Called
+// by a whole warp.  A reader in a later kernel calls map_acquire first.
+__device__ __forceinline__ void map_with_rows(void *out, const void *map, uint8_t *tmp, uint32_t rows) {
+  const int lane = threadIdx.x & 31;
+  reinterpret_cast<uint32_t *>(tmp)[lane] = static_cast<const uint32_t *>(map)[lane];
+  __syncwarp();
+  const uint32_t t = smem_u32(tmp);
+  if (lane == 0)
+    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(t), "r"(rows)
+                 : "memory");
+  __syncwarp();
+  asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned "
+               "[%0], [%1], 128;" ::"l"(out), "r"(t) : "memory");
+  __syncwarp();
+}
+__device__ __forceinline__ void map_acquire(const void *map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
 }
 __device__ __forceinline__ void tma_store(const void *map, uint32_t src, int c0, int c1, int c2,
                                           int c3) {
