@@ -8,6 +8,7 @@
 
 #include "moe_common.cuh"
 #include "moe_ffn.cuh"
+#include "moe_train.cuh"
 
 namespace moe {
 

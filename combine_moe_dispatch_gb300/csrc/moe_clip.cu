@@ -23,7 +23,7 @@
 // (eight SMs read too slowly), and was not kept.
 #include <cuda_bf16.h>
 
-#include "moe_common.cuh"
+#include "moe_train.cuh"
 
 namespace moe {
 

@@ -18,7 +18,7 @@
 // memory, always in the same order.
 #include <cuda_bf16.h>
 
-#include "moe_common.cuh"
+#include "moe_train.cuh"
 
 namespace moe {
 

@@ -181,29 +181,6 @@ struct ActParams {
   int scale_t;
 };
 
-struct CombineBackwardParams {
-  const uint16_t *d_y;         // [N, H]
-  const uint16_t *expert_y;    // [E, cap, H]
-  const int32_t *topk_idx;
-  const int32_t *slot_of;
-  const float *topk_weights;
-  uint16_t *d_expert_y;        // [E, cap, H]
-  float *d_weights;            // [N, K]
-  float *d_logits;             // [N, E], or null
-  WsHeader *hdr;
-  int N, H, E, K, cap;
-};
-
-// Workspace of the gradient norm: this header, then one partial sum per block.
-struct ClipHeader {
-  double total;                // sum of squares so far
-  float coef;
-  uint32_t done;               // blocks that have left their sum (reset by the last)
-  uint32_t reserved[60];
-};
-static_assert(sizeof(ClipHeader) == 256, "clip header is 256 bytes");
-constexpr int kClipMaxBlocks = 1024;
-
 struct RouterParams {
   const float *logits;     // [N, E]
   int32_t *topk_idx;       // [N, K]
@@ -230,10 +207,6 @@ cudaError_t launch_combine(const CombineParams &p, cudaStream_t stream);
 // is outside the fused path's limits (then run moe_plan and moe_dispatch).
 bool plan_dispatch_geometry(const moe_shape &s, FusedParams &p);
 cudaError_t launch_plan_dispatch(const FusedParams &p, bool fp8, cudaStream_t stream);
-cudaError_t launch_combine_backward(const CombineBackwardParams &p, cudaStream_t stream);
-size_t clip_workspace_bytes();
-cudaError_t launch_clip(const moe_grad_tensor *tensors, int num, float max_norm, float *norm,
-                        void *workspace, cudaStream_t stream);
 cudaError_t launch_router(const RouterParams &p, cudaStream_t stream);
 cudaError_t launch_silu_quant(const ActParams &p, cudaStream_t stream);
 cudaError_t launch_set_debug(WsHeader *hdr, uint32_t flags, uint64_t timeout_ns,
