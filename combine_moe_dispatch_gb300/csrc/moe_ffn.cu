@@ -28,7 +28,10 @@
 //    for every expert, tensor maps that end at its count, and the copies fill
 //    the rest of the last block of 64 tokens with zeros.
 // Counts are read on the device: nothing waits for the host, and the call can
-// be captured in a CUDA graph.  Tiles go to the pairs round robin.
+// be captured in a CUDA graph.  Tiles go to the pairs in order, as they get
+// free: what runs at one time is then a stretch of the list, whose operands
+// the L2 holds.  Dealt out round robin instead, pairs whose tiles were
+// narrower ran ahead.
 //
 // Rounding: the operands are bf16, every product and sum is accumulated in
 // binary32; a, dh and the results are rounded to bf16 once each (the matrix
@@ -58,7 +61,8 @@ constexpr uint32_t kHalfBytes = 128 * kBlockK * 2;       // a CTA's half of one 
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
 constexpr uint32_t kStagingBytes = 2 * 16384;            // epilogue, one buffer per group
 constexpr uint32_t kBarOff = kStages * kStageBytes + kStagingBytes;
-constexpr int kRing = 4;                                 // tiles announced ahead
+constexpr int kRing = 4;                                 // tiles announced ahead, at most
+constexpr int kLongTile = 64;                            // blocks of 64: announced only 2 ahead
 constexpr uint32_t kRingOff = kBarOff + 256;
 constexpr uint32_t kMapOff = kRingOff + kRing * 64;      // kActGrad: a tensor map being written
 constexpr uint32_t kPairSmem = kMapOff + 128 + 1024;     // + alignment slack
@@ -93,6 +97,14 @@ struct RowMaps<kActGrad> {
   CUtensorMap whole[kRowMaps];
 };
 
+// The launch's next unit of work, past the first of every pair.  Zero between
+// launches: the last pair to finish resets it.
+struct UnitCounter {
+  unsigned long long next;
+  uint32_t done;           // pairs that have finished
+  uint32_t reserved;
+};
+
 template <int KIND>
 struct PairParams {
   static constexpr int kJobs = KIND == kRest ? 3 : 1;
@@ -101,9 +113,11 @@ struct PairParams {
   WsHeader *hdr;
   float *part;             // partial sums of split contractions
   uint32_t *tickets;       // one per tile and CTA of the pair; zero between calls
+  UnitCounter *units;
   CUtensorMap *row_maps;   // [4][E], or null
   RowMaps<KIND> maps;
   int E, cap;
+  int single;              // no more units than pairs
 };
 
 template <class P>
@@ -282,10 +296,10 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t
   return false;
 }
 
-// A warp's view of the tiles that the scheduling warp announces.
+// A warp's view of the tiles that the leader's scheduling warp announces.
 struct Feed {
   const Tile *ring;
-  uint32_t full, empty;
+  uint32_t full, empty;    // this CTA's barriers, the leader's
   uint64_t limit;
   int s;
   uint32_t ph;
@@ -331,7 +345,7 @@ struct Feed {
 
  private:
   __device__ __forceinline__ void done() {     // every lane has read the record
-    tc::mbar_arrive_warp(empty + 8 * s);
+    tc::mbar_arrive_warp_at(empty + 8 * s);
     if (++s == kRing) {
       s = 0;
       ph ^= 1u;
@@ -391,8 +405,8 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     }
     for (int r = 0; r < kRing; ++r) {
       tc::mbar_init_at(rec_full + 8 * r, 1);
-      // TMA, epilogue, and in the leader the MMA warp
-      tc::mbar_init_at(rec_empty + 8 * r, kEpiWarps + 1 + (rank == 0 ? 1 : 0));
+      // in the leader: TMA and epilogue of both CTAs, and the MMA warp
+      tc::mbar_init_at(rec_empty + 8 * r, 2 * (kEpiWarps + 1) + 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   } else if (threadIdx.x == 32 && p.job[0].mt > 0) {
@@ -416,33 +430,52 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
   const uint64_t limit = tmo ? tmo : kDefaultTimeoutNs;
   bool ok = true;
   Tile t;
-  Feed feed(ring, rec_full, rec_empty, limit);
+  Feed feed(ring, rec_full, tc::map_rank(rec_empty, 0), limit);
 
   if (warp == 3) {
-    // ---- scheduling: one warp finds the pair's tiles, up to kRing ahead (the
-    // first counts are read together with the status)
+    // ---- scheduling: each CTA finds the pair's first tile (the first counts
+    // are read together with the status); then one warp of the leader takes
+    // units and announces their tiles to both CTAs
     Schedule<KIND> sched(p);
-    int s = 0;
-    uint32_t ph = 0;
-    // In round r, pair q takes unit (q + r) mod pairs of the round: an expert's
-    // tiles are not all of one size, and without the turn a pair would get the
-    // same place among them in every round (4 tiles per feature tile, 76 pairs:
-    // 960 rows per expert took as long as 1024).
-    const int pairs = gridDim.x >> 1;
-    int turn = blockIdx.x >> 1;
-    for (int64_t round = 0; live && ok; round += pairs) {
-      t.valid = sched.find(round + turn, t);
-      if (++turn == pairs) turn = 0;
-      ok = __all_sync(0xFFFFFFFFu, wait_bar(rec_empty + 8 * s, ph ^ 1u, limit));
-      if (ok && lane == 0) {
+    const uint32_t peer_full = tc::map_rank(rec_full, 1), peer_ring = tc::map_rank(smem + kRingOff, 1);
+    int64_t unit = blockIdx.x >> 1;
+    for (uint32_t c = 0; live; ++c) {
+      const uint32_t s = c % kRing;
+      if (c > 0 && p.single) {
+        t.valid = 0;                         // and that was all
+      } else {
+        if (c > 0) {
+          // A unit is taken as late as its tile allows: once the record 2 or
+          // kRing before it has been read by every warp of both CTAs.
+          const uint32_t ahead = t.nk >= kLongTile ? 2 : kRing;
+          if (c >= ahead) {
+            const uint32_t r = c - ahead;
+            ok = __all_sync(0xFFFFFFFFu, wait_bar(rec_empty + 8 * (r % kRing), (r / kRing) & 1u, limit));
+            if (!ok) break;
+          }
+          unsigned long long n = 0;
+          if (lane == 0) n = atomicAdd(&p.units->next, 1ull);
+          unit = (gridDim.x >> 1) + (int64_t)__shfl_sync(0xFFFFFFFFu, n, 0);
+        }
+        t.valid = sched.find(unit, t);
+      }
+      if (lane == 0) {
         ring[s] = t;
         tc::mbar_arrive_local(rec_full + 8 * s);
       }
-      if (!t.valid) break;
-      if (++s == kRing) {
-        s = 0;
-        ph ^= 1u;
+      if (c > 0 && !p.single) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_expect_at(peer_full + 8 * s, sizeof(Tile));
+        if (lane < 4)
+          tc::store_async(peer_ring + s * (uint32_t)sizeof(Tile) + lane * 16,
+                          reinterpret_cast<const uint4 *>(ring + s)[lane], peer_full + 8 * s);
       }
+      if (!t.valid || (rank != 0 && !p.single)) break;
+    }
+    if (rank == 0 && !p.single && lane == 0 &&
+        atomicAdd(&p.units->done, 1u) == (gridDim.x >> 1) - 1) {
+      p.units->next = 0;
+      p.units->done = 0;
     }
   } else if (live && warp == 0) {
     // ---- TMA: both CTAs load their halves; bytes complete on the leader's barrier
@@ -839,7 +872,7 @@ bool make_map_mn(CUtensorMap *m, int *wide, const void *base, int64_t width, int
 }
 
 template <int KIND>
-cudaError_t launch_pair(const PairParams<KIND> &p, int64_t tiles, cudaStream_t stream) {
+cudaError_t launch_pair(PairParams<KIND> &p, int64_t tiles, cudaStream_t stream) {
   static std::once_flag once[64];
   int dev = 0;
   cudaGetDevice(&dev);
@@ -861,6 +894,7 @@ cudaError_t launch_pair(const PairParams<KIND> &p, int64_t tiles, cudaStream_t s
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  p.single = tiles <= most;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, pair_kernel<KIND>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -874,6 +908,7 @@ PairParams<KIND> base_params(const FfnParams &f) {
   p.hdr = f.hdr;
   p.part = f.part;
   p.tickets = f.tickets;
+  p.units = reinterpret_cast<UnitCounter *>(f.tickets + 2 * kMaxPairs);
   p.row_maps = f.dw_gate_up || f.dw_down ? static_cast<CUtensorMap *>(f.row_maps) : nullptr;
   p.E = f.E;
   p.cap = f.cap;
@@ -902,7 +937,7 @@ FfnScratch ffn_scratch(int64_t E, int64_t cap, int64_t H, int64_t I) {
   const int64_t most = mt * E * cdiv(cap, kTileCols) * kMaxSplit;
   const int64_t cols = cap < kTileCols ? (cap + 31) / 32 * 32 : kTileCols;
   FfnScratch s;
-  s.part_off = kMaxPairs * 2 * sizeof(uint32_t);
+  s.part_off = align_up(kMaxPairs * 2 * sizeof(uint32_t) + sizeof(UnitCounter), 256);
   s.maps_off = s.part_off + (size_t)((most < kMaxPairs ? most : kMaxPairs) * cols) * 256 * sizeof(float);
   // the caller's workspace is aligned to 16 bytes, a tensor map to 128
   s.total = s.maps_off + 128 + (size_t)(kRowMaps * E) * sizeof(CUtensorMap);

@@ -28,8 +28,9 @@ struct FfnParams {
   uint16_t *dw_down;             // [E, H, I]
 };
 
-// Scratch past the plan's part of the workspace: tickets, zero between calls;
-// the partial sums of split contractions; the backward pass's tensor maps.
+// Scratch past the plan's part of the workspace: tickets and the unit counter, both
+// zero between calls; the partial sums of split contractions; the backward
+// pass's tensor maps.
 struct FfnScratch {
   size_t part_off, maps_off, total;
 };

@@ -25,13 +25,26 @@ __device__ __forceinline__ void mbar_expect_warp(uint32_t bar, uint32_t bytes) {
                "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
                : "memory");
 }
-// Arrive once for the whole warp.
-__device__ __forceinline__ void mbar_arrive_warp(uint32_t bar) {
-  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
-               "@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ void mbar_arrive_local(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Arrive once for the whole warp on a barrier of any CTA of the cluster; what
+// the lanes have read stays read, their stores are not released.
+__device__ __forceinline__ void mbar_arrive_warp_at(uint32_t bar) {
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+               "@e mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar) : "memory");
+}
+// Arrive on a barrier of any CTA of the cluster, announcing `bytes`; nothing
+// else is released.
+__device__ __forceinline__ void mbar_expect_at(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
+               "r"(bytes) : "memory");
+}
+// 16 bytes into the shared memory of any CTA of the cluster; they complete on
+// `bar` of the same CTA.
+__device__ __forceinline__ void store_async(uint32_t dst, const uint4 &v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+               ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar) : "memory");
 }
 // Arrive on a barrier of any CTA of the cluster.  Orders tcgen05 reads (after
 // fence_before), not ordinary stores to memory that another CTA reads.
