@@ -117,7 +117,6 @@ struct PairParams {
   CUtensorMap *row_maps;   // [4][E], or null
   RowMaps<KIND> maps;
   int E, cap;
-  int single;              // no more units than pairs
 };
 
 template <class P>
@@ -127,17 +126,12 @@ __device__ __forceinline__ int rows_of(const P &p, int e) {
   return c < 0 ? 0 : (c > p.cap ? p.cap : c);
 }
 
-// Columns per tile of `rows` tokens: equal tiles, a multiple of 32.
-__device__ __forceinline__ int tile_cols(int rows) {
-  if (rows <= kTileCols) return (rows + 31) & ~31;
-  const int n = (rows + kTileCols - 1) / kTileCols;
-  return ((rows + n - 1) / n + 31) & ~31;
-}
-__device__ __forceinline__ int token_tiles(int rows) {
-  if (rows <= kTileCols) return rows > 0 ? 1 : 0;
-  const int c = tile_cols(rows);
-  return (rows + c - 1) / c;
-}
+// Tiles of `rows` tokens, and the columns of each but the last: as few tiles as
+// 256 columns allow, equal, a multiple of 32 (the granularity of a matrix
+// instruction's columns).  With n tiles rows > 256 (n - 1) and the columns are
+// at most 256, so that the last tile is never empty.
+__device__ __forceinline__ int token_tiles(int rows) { return (int)(((unsigned)rows + 255u) >> 8); }
+__device__ __forceinline__ int tile_cols(int rows, int tiles) { return ((rows + tiles - 1) / tiles + 31) & ~31; }
 
 struct alignas(16) Tile {
   int valid;               // 0: no more work
@@ -183,33 +177,31 @@ struct Schedule {
   // The tiles that would leave pairs idle in the last round are cut, if their
   // contraction is long.  The estimate is in blocks of 64: a unit costs its
   // blocks and about kUnitCost more (filling the ring, the epilogue), a tile
-  // that is cut kJoinCost and one per part for adding the sums.
+  // that is cut kJoinCost and a block per part and 64 columns for the sums.
   __device__ __forceinline__ void choose_split() {
-    constexpr int kUnitCost = 6, kJoinCost = 8;
+    constexpr int kUnitCost = 6, kJoinCost = 14;
     const int lane = threadIdx.x & 31;
-    int64_t tiles = incl;
-    int cols = tile_cols(rows);
-    for (int e = e0 + 32 + lane; e < p.E; e += 32) {
+    int64_t tiles = lane == 31 ? incl : 0;   // the first batch's sum
+    int most = rows;
+    for (int e = 32 + lane; e < p.E; e += 32) {
       const int r = rows_of(p, e);
-      tiles += (int64_t)token_tiles(r) * p.job[0].mt;
-      cols = max(cols, tile_cols(r));
+      tiles += token_tiles(r) * p.job[0].mt;
+      most = max(most, r);
     }
-    if (lane < 31) tiles -= incl;            // the first batch's sum is the last lane's
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, d);
-    cols = __reduce_max_sync(0xFFFFFFFFu, cols);
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
     const int pairs = gridDim.x >> 1, nk = (p.job[0].K + kBlockK - 1) / kBlockK;
     const int left = (int)(tiles % pairs);
-    if (left == 0) return;
+    part_cols = min((most + 31) & ~31, kTileCols);
     // lane s - 1 prices s parts
     const int s = lane + 1;
     const bool can = s == 1 || (s <= kMaxSplit && s * left <= kMaxPairs && 4 * s <= nk);
-    const int cost = can ? ((left * s + pairs - 1) / pairs) * ((nk + s - 1) / s + kUnitCost) +
-                               (s > 1 ? kJoinCost + s : 0)
+    const int cost = can ? (s * left > pairs ? 2 : 1) * ((nk + s - 1) / s + kUnitCost) +
+                               (s > 1 ? kJoinCost + s * ((part_cols + 63) >> 6) : 0)
                          : INT_MAX >> 6;
-    split = (__reduce_min_sync(0xFFFFFFFFu, cost * 32 + lane) & 31) + 1;
+    split = left == 0 ? 1 : (__reduce_min_sync(0xFFFFFFFFu, cost * 32 + lane) & 31) + 1;
     whole = tiles - left;
-    part_cols = cols;
   }
   __device__ __forceinline__ bool find(int64_t unit, Tile &o) {
     const bool cut = unit >= whole && split > 1;
@@ -234,10 +226,16 @@ struct Schedule {
     o.job = 0;
     o.e = e0 + l;
     o.rows = __shfl_sync(0xFFFFFFFFu, rows, l);
-    const int c = tile_cols(o.rows), nt = token_tiles(o.rows);
-    o.m = nt == 1 ? r : r / nt;
-    o.n0 = (r - o.m * nt) * c;
-    o.cols = min(c, o.rows - o.n0);
+    const int nt = token_tiles(o.rows);
+    o.m = r;
+    o.n0 = 0;
+    o.cols = o.rows;
+    if (nt > 1) {
+      const int c = tile_cols(o.rows, nt);
+      o.m = r / nt;
+      o.n0 = (r - o.m * nt) * c;
+      o.cols = min(c, o.rows - o.n0);
+    }
     o.n = (o.cols + 31) & ~31;
     const int nk = (p.job[0].K + kBlockK - 1) / kBlockK;
     o.k0 = 0;
@@ -441,38 +439,34 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     int64_t unit = blockIdx.x >> 1;
     for (uint32_t c = 0; live; ++c) {
       const uint32_t s = c % kRing;
-      if (c > 0 && p.single) {
-        t.valid = 0;                         // and that was all
-      } else {
-        if (c > 0) {
-          // A unit is taken as late as its tile allows: once the record 2 or
-          // kRing before it has been read by every warp of both CTAs.
-          const uint32_t ahead = t.nk >= kLongTile ? 2 : kRing;
-          if (c >= ahead) {
-            const uint32_t r = c - ahead;
-            ok = __all_sync(0xFFFFFFFFu, wait_bar(rec_empty + 8 * (r % kRing), (r / kRing) & 1u, limit));
-            if (!ok) break;
-          }
-          unsigned long long n = 0;
-          if (lane == 0) n = atomicAdd(&p.units->next, 1ull);
-          unit = (gridDim.x >> 1) + (int64_t)__shfl_sync(0xFFFFFFFFu, n, 0);
+      if (c > 0) {
+        // A unit is taken as late as its tile allows: once the record 2 or
+        // kRing before it has been read by every warp of both CTAs.
+        const uint32_t ahead = t.nk >= kLongTile ? 2 : kRing;
+        if (c >= ahead) {
+          const uint32_t r = c - ahead;
+          ok = __all_sync(0xFFFFFFFFu, wait_bar(rec_empty + 8 * (r % kRing), (r / kRing) & 1u, limit));
+          if (!ok) break;
         }
-        t.valid = sched.find(unit, t);
+        unsigned long long n = 0;
+        if (lane == 0) n = atomicAdd(&p.units->next, 1ull);
+        unit = (gridDim.x >> 1) + (int64_t)__shfl_sync(0xFFFFFFFFu, n, 0);
       }
+      t.valid = sched.find(unit, t);
       if (lane == 0) {
         ring[s] = t;
         tc::mbar_arrive_local(rec_full + 8 * s);
       }
-      if (c > 0 && !p.single) {
+      if (c > 0) {
         __syncwarp();
         if (lane == 0) tc::mbar_expect_at(peer_full + 8 * s, sizeof(Tile));
         if (lane < 4)
           tc::store_async(peer_ring + s * (uint32_t)sizeof(Tile) + lane * 16,
                           reinterpret_cast<const uint4 *>(ring + s)[lane], peer_full + 8 * s);
       }
-      if (!t.valid || (rank != 0 && !p.single)) break;
+      if (!t.valid || rank != 0) break;
     }
-    if (rank == 0 && !p.single && lane == 0 &&
+    if (rank == 0 && lane == 0 &&
         atomicAdd(&p.units->done, 1u) == (gridDim.x >> 1) - 1) {
       p.units->next = 0;
       p.units->done = 0;
@@ -762,6 +756,7 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
             float4 lo[4], hi[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) lo[r] = hi[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
             for (int s = 0; s < t.split; ++s)
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
@@ -872,7 +867,7 @@ bool make_map_mn(CUtensorMap *m, int *wide, const void *base, int64_t width, int
 }
 
 template <int KIND>
-cudaError_t launch_pair(PairParams<KIND> &p, int64_t tiles, cudaStream_t stream) {
+cudaError_t launch_pair(const PairParams<KIND> &p, int64_t tiles, cudaStream_t stream) {
   static std::once_flag once[64];
   int dev = 0;
   cudaGetDevice(&dev);
@@ -894,7 +889,6 @@ cudaError_t launch_pair(PairParams<KIND> &p, int64_t tiles, cudaStream_t stream)
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  p.single = tiles <= most;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, pair_kernel<KIND>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
