@@ -371,7 +371,9 @@ static moe_status ffn_check(const moe_shape *shape, int32_t intermediate, const 
   moe_status st = check_shape(shape);
   if (st != MOE_OK) return st;
   if (intermediate <= 0) return MOE_ERR_INVALID_ARG;
-  if (shape->payload != MOE_PAYLOAD_BF16 || intermediate % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  if (shape->payload != MOE_PAYLOAD_BF16 || intermediate % 8 != 0 || intermediate >= (1 << 29) ||
+      shape->hidden >= (1 << 30))
+    return MOE_ERR_UNSUPPORTED;
   const int64_t rows = (int64_t)shape->num_experts * shape->capacity, lim = (int64_t)1 << 46;
   // rows < 2^31 and the widths < 2^32: no product here passes 2^63
   if (rows * 2 * intermediate >= lim || rows * shape->hidden >= lim ||

@@ -7,35 +7,55 @@
 //   da = dy Wd,  dgate = da up s (1 + gate (1 - s)),  dup = da gate s,
 //   dx = dh Wgu,  dWgu = dh^T x,  dWd = dy^T a.
 //
-// How: each of these six products is one launch of pair_kernel<MODE>.  A
-// cluster of two CTAs (the two SMs of a pair) computes a tile of 256 rows x
-// up to 256 columns with tcgen05.mma.cta_group::2: each CTA stages its half
-// of both operands (128 rows of A, half the columns of B, 64 k at a time) by
-// TMA in a ring of 6 stages, one thread of the leading CTA issues the matrix
-// instructions, and the accumulators stay in tensor memory, two tiles deep,
-// so that four epilogue warps per CTA write one tile while the next is
-// multiplied.
-//  - Products over the hidden or intermediate size ("row" modes) put the
+// How: four launches of pair_kernel<KIND>: kGateUp and kDown forward, kActGrad
+// (da, and from it a and dh) and kRest (dx, dWgu and dWd) backward.  A cluster
+// of two CTAs (the two SMs of a pair) computes a tile of 256 rows x up to 256
+// columns with tcgen05.mma.cta_group::2: each CTA stages its half of both
+// operands (128 rows of A, half the columns of B, 64 k at a time) by TMA in a
+// ring of 6 stages, a warp of the leading CTA issues the matrix instructions,
+// and the accumulators stay in tensor memory, two tiles deep, so that the
+// eight epilogue warps of each CTA write one tile while the next is multiplied.
+//  - Products over the hidden or intermediate size ("row products") put the
 //    weights' output features on the 256-row side and the expert's tokens on
 //    the column side: the column count of a matrix instruction can be any
 //    multiple of 32, so an expert with 40 tokens costs 64 columns and not a
 //    whole tile of 256.  An expert's tokens are cut into equal tiles of at
-//    most 256.
-//  - Weight gradients ("weight" modes) contract over the expert's tokens;
-//    both operands are then read with the contraction as the outer dimension
-//    (MN-major shared-memory tiles).  Rows past count[e] are not the
-//    expert's and may hold anything, NaN included: the kernel before writes,
-//    for every expert, tensor maps that end at its count, and the copies fill
-//    the rest of the last block of 64 tokens with zeros.
+//    most 256.  Gate and up of the same 64 features are the two halves of a
+//    CTA's 128 rows, so that a is computed from both in binary32 and h need
+//    not be written.
+//  - Weight gradients contract over the expert's tokens; both operands are
+//    then read with the contraction as the outer dimension (MN-major
+//    shared-memory tiles).  Rows past count[e] are not the expert's and may
+//    hold anything, NaN included: kActGrad writes, for every expert, tensor
+//    maps that end at its count, and the copies fill the rest of the last
+//    block of 64 tokens with zeros.  (Zeroing that block in shared memory
+//    instead took about 2000 cycles per tile: dWgu of the Mixtral-shaped batch
+//    1310 us, now 1220.)
+//  - Few tiles and a long contraction (few tokens): the tiles of the last,
+//    partial round are cut into parts whose sums are joined, see choose_split.
 // Counts are read on the device: nothing waits for the host, and the call can
 // be captured in a CUDA graph.  Tiles go to the pairs in order, as they get
 // free: what runs at one time is then a stretch of the list, whose operands
 // the L2 holds.  Dealt out round robin instead, pairs whose tiles were
-// narrower ran ahead.
+// narrower ran ahead (backward of the Mixtral-shaped batch 4.06 ms, now 3.78).
 //
 // Rounding: the operands are bf16, every product and sum is accumulated in
 // binary32; a, dh and the results are rounded to bf16 once each (the matrix
 // instructions take 16-bit operands; the kept h is never re-rounded).
+//
+// What bounds it, measured on GB300 (6.78 TB/s copy, 1.94 PFLOP/s bf16 for
+// seconds-long bursts, 1.71 sustained under the power limit):
+//  - Mixtral-shaped batch (8192 rows over 8 experts, H 4096, I 14336): forward
+//    1.78 ms (1.62 PFLOP/s), backward 3.78 ms (1.53).  The tensor pipe is
+//    active 92 to 94 % of the cycles (kActGrad 79 %, its epilogue reads h);
+//    the clock, 1.32 to 1.36 GHz at 1.37 kW, is what the power limit leaves.
+//  - DeepSeek-V3-shaped decode (256 experts, 32 rows each, 22.5 GB of weights):
+//    3.33 ms, 6.85 TB/s: the weights' reading.  One token over two experts of
+//    the Mixtral shape: 117 us for 705 MB.
+//  - Weight gradients of experts with few rows: the writing.  64 experts of 128
+//    rows, 2.1 GB of dWgu: 5.1 TB/s (a plain fill of memory reaches 4.1).
+//  - Tiny calls: latency, about 5 us a launch from the end of the one before:
+//    status and counts, the first copies, the products, the epilogue.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <limits.h>
@@ -61,8 +81,12 @@ constexpr uint32_t kHalfBytes = 128 * kBlockK * 2;       // a CTA's half of one 
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
 constexpr uint32_t kStagingBytes = 2 * 16384;            // epilogue, one buffer per group
 constexpr uint32_t kBarOff = kStages * kStageBytes + kStagingBytes;
-constexpr int kRing = 4;                                 // tiles announced ahead, at most
-constexpr int kLongTile = 64;                            // blocks of 64: announced only 2 ahead
+// Tiles announced ahead: kRing, and 2 where they are of kLongTile blocks or
+// more, since a unit taken early is a unit that cannot go to a pair that is
+// free sooner.  Measured: one token 116 us, with 4 ahead for all 122; uneven
+// experts' backward (2 to 32 blocks a tile) 213 us, with 2 ahead for all 217.
+constexpr int kRing = 4;
+constexpr int kLongTile = 64;
 constexpr uint32_t kRingOff = kBarOff + 256;
 constexpr uint32_t kMapOff = kRingOff + kRing * 64;      // kActGrad: a tensor map being written
 constexpr uint32_t kPairSmem = kMapOff + 128 + 1024;     // + alignment slack
@@ -131,7 +155,9 @@ __device__ __forceinline__ int rows_of(const P &p, int e) {
 // instruction's columns).  With n tiles rows > 256 (n - 1) and the columns are
 // at most 256, so that the last tile is never empty.
 __device__ __forceinline__ int token_tiles(int rows) { return (int)(((unsigned)rows + 255u) >> 8); }
-__device__ __forceinline__ int tile_cols(int rows, int tiles) { return ((rows + tiles - 1) / tiles + 31) & ~31; }
+__device__ __forceinline__ int tile_cols(int rows, int tiles) {
+  return (int)((((unsigned)rows + tiles - 1) / tiles + 31) & ~31u);
+}
 
 struct alignas(16) Tile {
   int valid;               // 0: no more work
@@ -175,9 +201,13 @@ struct Schedule {
     }
   }
   // The tiles that would leave pairs idle in the last round are cut, if their
-  // contraction is long.  The estimate is in blocks of 64: a unit costs its
-  // blocks and about kUnitCost more (filling the ring, the epilogue), a tile
-  // that is cut kJoinCost and a block per part and 64 columns for the sums.
+  // contraction is of 1024 or more.  The estimate is in blocks of 64: a unit
+  // costs its blocks and about kUnitCost more (filling the ring, the epilogue),
+  // a tile that is cut kJoinCost and a block per part and 64 columns for the
+  // sums.  Measured with and without: one token (two experts, H 4096, I 14336)
+  // 117 and 124 us; 128 rows of one expert, H 7168, I 2048: 36 and 41; 1109
+  // rows, H 4416, I 2168: 71 and 74; uneven experts' backward 206 and 205;
+  // ten rows over 95 experts 28 and 26 (counting the tiles takes 1 us).
   __device__ __forceinline__ void choose_split() {
     constexpr int kUnitCost = 6, kJoinCost = 14;
     const int lane = threadIdx.x & 31;
@@ -193,7 +223,7 @@ struct Schedule {
     most = __reduce_max_sync(0xFFFFFFFFu, most);
     const int pairs = gridDim.x >> 1, nk = (p.job[0].K + kBlockK - 1) / kBlockK;
     const int left = (int)(tiles % pairs);
-    part_cols = min((most + 31) & ~31, kTileCols);
+    part_cols = most >= kTileCols ? kTileCols : (most + 31) & ~31;
     // lane s - 1 prices s parts
     const int s = lane + 1;
     const bool can = s == 1 || (s <= kMaxSplit && s * left <= kMaxPairs && 4 * s <= nk);
@@ -272,7 +302,7 @@ struct Schedule {
     o.n = min(kTileCols, (j.N - o.n0 + 31) & ~31);
     o.cols = o.n;
     o.k0 = 0;
-    o.nk = (o.rows + kBlockK - 1) / kBlockK;
+    o.nk = (int)(((unsigned)o.rows + kBlockK - 1) / kBlockK);
     o.split = 1;
     o.part = o.slot = o.part_cols = 0;
     return true;
@@ -858,8 +888,9 @@ bool make_map(CUtensorMap *m, const void *base, int64_t d0, int64_t d1, int64_t 
 }
 
 // An operand stored [E][k][width], its contraction dimension k outside: one
-// copy brings 64 k of 128 rows, as two blocks of 64 rows, where the width
-// allows (*wide), else of 64.
+// copy brings 64 k of 128 rows, as two blocks of 64 rows, where the width is
+// whole blocks (*wide: a block must not run into the next row of the array),
+// else two copies bring 64 rows each.
 bool make_map_mn(CUtensorMap *m, int *wide, const void *base, int64_t width, int64_t k, int64_t E) {
   *wide = width % 128 == 0;
   if (*wide) return encode(m, base, 64, k, width / 64, E, width, 64, k * width, 64, 2);

@@ -352,9 +352,12 @@ moe_status moe_silu_mul_quant(const moe_shape *shape, int32_t intermediate, cons
  *       moe_ffn_workspace_size(shape, intermediate) bytes (which is never less
  *       than moe_workspace_size); nothing is written if its status word is
  *       set, and a wait inside a kernel that runs out sets it to TIMEOUT.
- * Limits: payload BF16; intermediate % 8 == 0; E * cap * 2 * intermediate and
- *       E * cap * H < 2^46; 4 * intermediate * H < 2^40 bytes.  All bf16 arrays
- *       16-byte aligned.  No output may overlap an input.
+ *       After TIMEOUT initialise the workspace again before its next use: its
+ *       counters may not be zero.
+ * Limits: payload BF16; intermediate % 8 == 0, intermediate < 2^29, H < 2^30;
+ *       E * cap * 2 * intermediate and E * cap * H < 2^46; 4 * intermediate * H
+ *       < 2^40.  All bf16 arrays 16-byte aligned.  No output may overlap an
+ *       input.
  * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA. */
 size_t moe_ffn_workspace_size(const moe_shape *shape, int32_t intermediate);
 moe_status moe_ffn(const moe_shape *shape, int32_t intermediate, const void *expert_x,
@@ -372,12 +375,11 @@ moe_status moe_ffn(const moe_shape *shape, int32_t intermediate, const void *exp
  * In:   d_expert_y [E, cap, H] (from moe_combine_backward), expert_x, expert_h
  *       (as moe_ffn kept it), the weights and the counts of the forward call.
  * Out:  expert_act [E, cap, intermediate] and d_expert_h [E, cap, 2*intermediate]
- *       bf16 (computed here, read by the products that follow; rows below the
- *       count); d_expert_x [E, cap, H] bf16 (rows below the count);
+ *       bf16 (computed here, read by the second launch; rows below the count); d_expert_x [E, cap, H] bf16 (rows below the count);
  *       d_w_gate_up [E, 2*intermediate, H] and d_w_down [E, H, intermediate]
  *       bf16, every element written: 0 for an expert without rows.  Each of
  *       d_expert_x, d_w_gate_up and d_w_down may be NULL: not computed.
- * Four launches at most.  Work, limits, errors: as moe_ffn. */
+ * Two launches.  Work, limits, errors: as moe_ffn. */
 moe_status moe_ffn_backward(const moe_shape *shape, int32_t intermediate, const void *d_expert_y,
                             const void *expert_x, const void *expert_h, const void *w_gate_up,
                             const void *w_down, const int32_t *expert_num_tokens, void *expert_act,

@@ -80,6 +80,11 @@ def test_ffn_size_limits(lib, call):
     assert call(lib, shape=one, inter=1 << 18, **null) == Status.UNSUPPORTED
     assert call(lib, shape=one, inter=(1 << 18) - 8, **null) == Status.INVALID_ARG
     assert call(lib, shape=(1, 4, 2147483640, 1, 1, 1, 0), inter=2147483640, **null) == Status.UNSUPPORTED
+    thin = (1, 4, 8, 1, 1, 1, 0)
+    assert call(lib, shape=thin, inter=1 << 29, **null) == Status.UNSUPPORTED
+    assert call(lib, shape=thin, inter=(1 << 29) - 8, **null) == Status.INVALID_ARG
+    assert call(lib, shape=(1, 4, 1 << 30, 1, 1, 1, 0), inter=8, **null) == Status.UNSUPPORTED
+    assert call(lib, shape=(1, 4, (1 << 30) - 8, 1, 1, 1, 0), inter=8, **null) == Status.INVALID_ARG
 
 
 def test_ffn_workspace_size(lib):
@@ -87,9 +92,10 @@ def test_ffn_workspace_size(lib):
     assert moe.ffn_workspace_size(s, I) >= moe.workspace_size(s)
     assert moe.ffn_workspace_size(s, 0) == 0
     assert moe.ffn_workspace_size(Shape(1, 16, 260, 4, 2, 16, 0), I) == 0
-    # the partial sums are bounded whatever the shape: 128 tiles of 256 x 256 floats
+    # bounded whatever the shape: sums of 128 tiles of 256 x 256 floats, four tensor
+    # maps per expert, counters
     big = Shape(8, 512, 7168, 256, 8, 8192, 0)
-    assert moe.ffn_workspace_size(big, 2048) <= moe.workspace_size(big) + (128 << 18) + 4096
+    assert moe.ffn_workspace_size(big, 2048) <= moe.workspace_size(big) + (128 << 18) + 4 * 128 * 256 + 4096
 
 
 def test_combine_backward_arguments(lib):
