@@ -149,7 +149,9 @@ combine_backward_kernel(CombineBackwardParams p) {
       else __syncthreads();
       if (sub == 0 && ok) p.d_logits[g * p.E + e_l] = s_dot[warp][lane];
     }
-    if (WPT > 1) __syncthreads();
+    // s_dot is written again in the next round
+    if (WPT == 1) __syncwarp();
+    else __syncthreads();
   }
 }
 
