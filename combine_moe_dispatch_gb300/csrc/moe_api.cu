@@ -394,8 +394,7 @@ size_t moe_ffn_workspace_size(const moe_shape *shape, int32_t intermediate) {
 static void set_scratch(FfnParams &f, const moe_shape *shape, int32_t intermediate, void *workspace) {
   const FfnScratch s = ffn_scratch(shape->num_experts, shape->capacity, shape->hidden, intermediate);
   char *base = static_cast<char *>(workspace) + ws_layout(*shape).total;
-  f.tickets = reinterpret_cast<uint32_t *>(base);
-  f.part = reinterpret_cast<float *>(base + s.part_off);
+  f.part = reinterpret_cast<float *>(base);
   f.row_maps = reinterpret_cast<void *>(align_up((uintptr_t)(base + s.maps_off), 128));
 }
 

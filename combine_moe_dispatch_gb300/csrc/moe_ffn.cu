@@ -59,6 +59,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <limits.h>
+#include <stddef.h>
 
 #include <mutex>
 
@@ -121,13 +122,18 @@ struct RowMaps<kActGrad> {
   CUtensorMap whole[kRowMaps];
 };
 
-// The launch's next unit of work, past the first of every pair.  Zero between
-// launches: the last pair to finish resets it.
+// The launch's next unit of work, past the first of every pair: the last pair
+// to finish resets it.  It and the tickets are zero between launches and stand
+// in the workspace header's reserved words, the one place that no shape's plan
+// uses for anything else.
 struct UnitCounter {
   unsigned long long next;
   uint32_t done;           // pairs that have finished
   uint32_t reserved;
 };
+constexpr int kUnitWord = 1, kTicketWord = 8;            // in WsHeader::reserved
+static_assert(offsetof(WsHeader, reserved) % 8 == 4, "the unit counter is 8-byte aligned");
+static_assert(kMaxSplit < 16 && kTicketWord + kMaxPairs * 2 * 4 / 32 <= 55, "the tickets fit");
 
 template <int KIND>
 struct PairParams {
@@ -136,7 +142,7 @@ struct PairParams {
   const int32_t *counts;   // [E], or null (cap rows each)
   WsHeader *hdr;
   float *part;             // partial sums of split contractions
-  uint32_t *tickets;       // one per tile and CTA of the pair; zero between calls
+  uint32_t *tickets;       // finished parts, 4 bits for each split tile and CTA of the pair
   UnitCounter *units;
   CUtensorMap *row_maps;   // [4][E], or null
   RowMaps<KIND> maps;
@@ -774,9 +780,10 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
         __threadfence();
         named_sync(3, 32 * kEpiWarps);
         if (threadIdx.x == 128) {
-          uint32_t *ticket = p.tickets + t.slot * 2 + rank;
-          const bool last = atomicAdd(ticket, 1u) == (uint32_t)t.split - 1;
-          if (last) *ticket = 0;
+          const uint32_t ticket = t.slot * 2 + rank, shift = 4 * (ticket & 7);
+          const uint32_t before = atomicAdd(p.tickets + (ticket >> 3), 1u << shift);
+          const bool last = ((before >> shift) & 15u) == (uint32_t)t.split - 1;
+          if (last) atomicSub(p.tickets + (ticket >> 3), (uint32_t)t.split << shift);
           *last_in = last;
           __threadfence();
         }
@@ -932,8 +939,8 @@ PairParams<KIND> base_params(const FfnParams &f) {
   p.counts = f.counts;
   p.hdr = f.hdr;
   p.part = f.part;
-  p.tickets = f.tickets;
-  p.units = reinterpret_cast<UnitCounter *>(f.tickets + 2 * kMaxPairs);
+  p.tickets = f.hdr->reserved + kTicketWord;
+  p.units = reinterpret_cast<UnitCounter *>(f.hdr->reserved + kUnitWord);
   p.row_maps = f.dw_gate_up || f.dw_down ? static_cast<CUtensorMap *>(f.row_maps) : nullptr;
   p.E = f.E;
   p.cap = f.cap;
@@ -962,8 +969,7 @@ FfnScratch ffn_scratch(int64_t E, int64_t cap, int64_t H, int64_t I) {
   const int64_t most = mt * E * cdiv(cap, kTileCols) * kMaxSplit;
   const int64_t cols = cap < kTileCols ? (cap + 31) / 32 * 32 : kTileCols;
   FfnScratch s;
-  s.part_off = align_up(kMaxPairs * 2 * sizeof(uint32_t) + sizeof(UnitCounter), 256);
-  s.maps_off = s.part_off + (size_t)((most < kMaxPairs ? most : kMaxPairs) * cols) * 256 * sizeof(float);
+  s.maps_off = (size_t)((most < kMaxPairs ? most : kMaxPairs) * cols) * 256 * sizeof(float);
   // the caller's workspace is aligned to 16 bytes, a tensor map to 128
   s.total = s.maps_off + 128 + (size_t)(kRowMaps * E) * sizeof(CUtensorMap);
   return s;

@@ -11,8 +11,7 @@ namespace moe {
 struct FfnParams {
   const int32_t *counts;         // [E] rows per expert, or null (cap each)
   WsHeader *hdr;
-  uint32_t *tickets;             // scratch, see FfnScratch
-  float *part;
+  float *part;                   // scratch, see FfnScratch
   void *row_maps;
   int E, cap, H, I;
   const uint16_t *x;             // [E, cap, H]
@@ -28,11 +27,10 @@ struct FfnParams {
   uint16_t *dw_down;             // [E, H, I]
 };
 
-// Scratch past the plan's part of the workspace: tickets and the unit counter, both
-// zero between calls; the partial sums of split contractions; the backward
-// pass's tensor maps.
+// Scratch past the plan's part of the workspace, of any content between calls:
+// the partial sums of split contractions, then the backward pass's tensor maps.
 struct FfnScratch {
-  size_t part_off, maps_off, total;
+  size_t maps_off, total;
 };
 FfnScratch ffn_scratch(int64_t E, int64_t cap, int64_t H, int64_t I);
 

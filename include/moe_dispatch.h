@@ -352,8 +352,9 @@ moe_status moe_silu_mul_quant(const moe_shape *shape, int32_t intermediate, cons
  *       moe_ffn_workspace_size(shape, intermediate) bytes (which is never less
  *       than moe_workspace_size); nothing is written if its status word is
  *       set, and a wait inside a kernel that runs out sets it to TIMEOUT.
- *       After TIMEOUT initialise the workspace again before its next use: its
- *       counters may not be zero.
+ *       Its counters stand in the workspace's first 256 bytes, so that one
+ *       workspace serves calls of different shapes in turn.  After TIMEOUT
+ *       initialise the workspace again before its next use.
  * Limits: payload BF16; intermediate % 8 == 0, intermediate < 2^29, H < 2^30;
  *       E * cap * 2 * intermediate and E * cap * H < 2^46; 4 * intermediate * H
  *       < 2^40.  All bf16 arrays 16-byte aligned.  No output may overlap an

@@ -293,3 +293,37 @@ def test_status_set_writes_nothing_and_stream_order():
     torch.cuda.synchronize()
     _untouched(y2, [0, 5, 1, 0], "y")
     assert torch.equal(y2[1, :5], want[1, :5])
+
+
+def test_one_workspace_for_many_shapes():
+    """One workspace serves shapes of every size in turn, with plans of other
+    shapes in between: past its header nothing needs to be kept or zero (the
+    plan's rows of one shape lie where another's partial sums are)."""
+    import combine_moe_dispatch_gb300 as moe
+    todo = [SHAPES[i] for i in (9, 5, 12, 10, 9)]
+    size = max(moe.ffn_workspace_size(moe.make_shape(1, max(1, E * cap), H, E, 1, cap), I)
+               for E, cap, H, I, _ in todo)
+    shared = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    plan_shape = moe.make_shape(4, 3000, 64, 200, 4, 12000)
+    assert moe.workspace_size(plan_shape) <= size
+    for k, (E, cap, H, I, counts) in enumerate(todo):
+        shared[256:] = 0xFF
+        b = moe.Buffers(plan_shape, expert_x=False, expert_y=False)
+        b.workspace = shared
+        b.plan(torch.randint(0, 200, (12000, 4), dtype=torch.int32, device="cuda"))
+        assert moe.read_status(shared) == moe.Status.OK
+        _, shape, c, x, h, dy, wgu, wd, _, cnt = _case(E, cap, H, I, counts, 70 + k)
+        act, y = _buf(E, cap, I), _buf(E, cap, H)
+        moe.ffn(shape, I, x, wgu, wd, cnt, None, act, y, shared)
+        dh, dx, dwgu, dwd = _buf(E, cap, 2 * I), _buf(E, cap, H), _buf(E, 2 * I, H), _buf(E, H, I)
+        moe.ffn_backward(shape, I, dy, x, h, wgu, wd, cnt, act, dh, dx, dwgu, dwd, shared)
+        for e, n in enumerate(c):
+            if n == 0:
+                continue
+            y64, ytol, *_ = _forward64(x[e, :n], wgu[e], wd[e], I)
+            _near(y[e, :n], y64, ytol, f"y, shape {k}, expert {e}")
+            (rx, ex), (rgu, egu), (rd, ed) = _backward64(dy[e, :n], x[e, :n], h[e, :n], wgu[e], wd[e], I)
+            _near(dx[e, :n], rx, ex, f"dx, shape {k}, expert {e}")
+            _near(dwgu[e], rgu, egu, f"d_w_gate_up, shape {k}, expert {e}")
+            _near(dwd[e], rd, ed, f"d_w_down, shape {k}, expert {e}")
+        assert moe.read_status(shared) == moe.Status.OK
