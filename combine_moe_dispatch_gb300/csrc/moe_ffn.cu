@@ -405,6 +405,7 @@ __device__ __forceinline__ void unpack4(const uint2 &w, float (&v)[4]) {
   v[2] = bf16_lo(w.y);
   v[3] = bf16_hi(w.y);
 }
+// Good to 2^-20 relative for |g| < 20; 0 where it is below 2^-126.
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
 template <int KIND>
@@ -457,10 +458,11 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
 
   pdl_allow_dependents();
   pdl_wait_for_previous();
-  // The status is read once, by every thread alike: after a plan error no
-  // tile is computed and nothing is written.
+  // After a plan error no tile is computed and nothing is written.  The block's
+  // threads decide together: the status may change under them when another
+  // pair's wait runs out.
   const uint64_t tmo = p.hdr->timeout_ns;
-  const bool live = read_status(p.hdr) == MOE_OK;
+  const bool live = __syncthreads_and(read_status(p.hdr) == MOE_OK);
   const uint64_t limit = tmo ? tmo : kDefaultTimeoutNs;
   bool ok = true;
   Tile t;
