@@ -327,3 +327,21 @@ def test_one_workspace_for_many_shapes():
             _near(dwgu[e], rgu, egu, f"d_w_gate_up, shape {k}, expert {e}")
             _near(dwd[e], rd, ed, f"d_w_down, shape {k}, expert {e}")
         assert moe.read_status(shared) == moe.Status.OK
+
+
+@pytest.mark.parametrize("i", [4, 9, 10, 11])
+def test_same_bits_every_time(i):
+    """Which pair of SMs takes a tile, and which part of a split contraction
+    finishes last, differ from run to run; the results do not."""
+    E, cap, H, I, counts = SHAPES[i]
+    moe, shape, c, x, h, dy, wgu, wd, ws, cnt = _case(E, cap, H, I, counts, 90)
+    first = None
+    for _ in range(4):
+        act, y, dx = _buf(E, cap, I), _buf(E, cap, H), _buf(E, cap, H)
+        dh, dwgu, dwd = _buf(E, cap, 2 * I), _buf(E, 2 * I, H), _buf(E, H, I)
+        moe.ffn(shape, I, x, wgu, wd, cnt, None, act, y, ws)
+        moe.ffn_backward(shape, I, dy, x, h, wgu, wd, cnt, act, dh, dx, dwgu, dwd, ws)
+        out = [t.view(torch.int16) for t in (y, act, dh, dx, dwgu, dwd)]
+        if first is None:
+            first = out
+        assert all(torch.equal(a, b) for a, b in zip(out, first))

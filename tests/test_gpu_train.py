@@ -267,3 +267,70 @@ def test_example_learns():
         layer.step(lr=0.5, max_norm=1.0)
         assert abs(float(layer.grad_norm) - norm) <= 2.0 ** -16 * norm
     assert losses[-1] < losses[0]
+
+
+def test_combine_backward_against_differences():
+    """The loss sum(y * d_y), with y the weighted sum of the experts' rows and
+    the weights the softmax of the chosen logits, moved by a small step along a
+    random direction of the rows and of the logits, in 64 bits: the central
+    differences agree with the gradients' inner products.  d_expert_y is off by
+    one bf16 rounding (2^-8 relative) per element, d_logits by binary32
+    roundings: 2^-8 and 2^-12 of the gradients' norms, times the direction's
+    spread of a few, stay below the 2 % and 0.2 % asked."""
+    import combine_moe_dispatch_gb300 as moe
+    N, H, E, K = 24, 200, 10, 3
+    shape = moe.make_shape(1, N, H, E, K, N)
+    logits = _normal((N, E), 1.0, 41, torch.float32)
+    idx = torch.empty((N, K), dtype=torch.int32, device="cuda")
+    w = torch.empty((N, K), device="cuda")
+    moe.router_topk(shape, logits, idx, w)
+    b = moe.Buffers(shape, expert_x=False, expert_y=False)
+    b.plan(idx)
+    dy, ey = _normal((N, H), 1.0, 42), _normal((E, N, H), 1.0, 43)
+    dey = torch.zeros((E, N, H), dtype=torch.bfloat16, device="cuda")
+    dw, dl = torch.empty((N, K), device="cuda"), torch.empty((N, E), device="cuda")
+    moe.combine_backward(shape, dy, ey, idx, b.slot_of, w, dey, dw, dl, b.workspace)
+    e, s = idx.long(), b.slot_of.long()
+
+    def loss(rows, logits):
+        weights = torch.softmax(logits.gather(1, e), 1)
+        return float(((weights[:, :, None] * rows[e, s]).sum(1) * dy.to(D)).sum())
+
+    at, step = [ey.to(D), logits.to(D)], 1e-5
+    for i, (grad, part) in enumerate(((dey, 0.02), (dl, 0.002))):
+        v = torch.randn(at[i].shape, dtype=D, device="cuda", generator=_gen(50 + i))
+        up = [t + step * v if j == i else t for j, t in enumerate(at)]
+        down = [t - step * v if j == i else t for j, t in enumerate(at)]
+        slope = (loss(*up) - loss(*down)) / (2 * step)
+        assert abs(float((grad.to(D) * v).sum()) - slope) <= part * float(grad.to(D).norm()), i
+
+
+def test_offsets_past_32_bits():
+    """Rows of the experts' buffers past 2^31 elements, and a gradient of more
+    than 2^31 elements."""
+    import combine_moe_dispatch_gb300 as moe
+    N, H, E, cap = 4, 8192, 5, 65536
+    shape = moe.make_shape(1, N, H, E, 1, cap)
+    ws = torch.zeros(moe.workspace_size(shape), dtype=torch.uint8, device="cuda")
+    idx = torch.full((N, 1), E - 1, dtype=torch.int32, device="cuda")
+    slot = torch.arange(cap - N, cap, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    w = torch.full((N, 1), 0.5, device="cuda")
+    dy = _normal((N, H), 1.0, 61)
+    ey = torch.empty((E, cap, H), dtype=torch.bfloat16, device="cuda")
+    ey[-1, -N:] = _normal((N, H), 1.0, 62)
+    dey = torch.empty_like(ey)
+    dey[-1, -2 * N:] = SENTINEL
+    dw = torch.empty((N, 1), device="cuda")
+    moe.combine_backward(shape, dy, ey, idx, slot, w, dey, dw, None, ws)
+    assert torch.equal(dey[-1, -N:], (0.5 * dy.float()).bfloat16())
+    assert bool((dey[-1, -2 * N:-N] == SENTINEL).all())
+    terms = dy.to(D) * ey[-1, -N:].to(D)
+    _near(dw[:, 0], terms.sum(1), H * U24 * terms.abs().sum(1), "d_weights")
+    del ey, dey
+    n = 2 ** 31 + 1001
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g[0], g[2 ** 31 + 7], g[-1] = 3.0, 4.0, 12.0
+    assert abs(float(_clip([g], [g], 6.5)) - 13.0) <= 2.0 ** -16 * 13.0
+    for i, want in ((0, 1.5), (2 ** 31 + 7, 2.0), (n - 1, 6.0)):
+        assert abs(float(g[i]) - want) <= (U8 + 2.0 ** -15) * want
+    assert int((g != 0).sum()) == 3
