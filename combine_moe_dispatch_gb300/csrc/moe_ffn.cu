@@ -70,9 +70,10 @@ namespace moe {
 
 namespace {
 
-// What one launch computes.  kRest: dx, dWgu and dWd, which need nothing of
-// one another, as one list of tiles.
-enum Kind { kGateUp = 0, kDown = 1, kActGrad = 2, kRest = 3 };
+// What one launch computes.  kForward: a (and h), then y, whose tiles wait until
+// every tile of a is written.  kRest: dx, dWgu and dWd, which need nothing of one
+// another, as one list of tiles.
+enum Kind { kForward = 0, kActGrad = 1, kRest = 2 };
 
 constexpr int kPairThreads = 384;      // warps: 0 TMA, 1 MMA, 2 maps, 3 scheduling, 4-11 epilogue
 constexpr int kEpiWarps = 8;           // two groups of four; each takes every other chunk of columns
@@ -104,10 +105,10 @@ struct Job {
   CUtensorMap a;
   CUtensorMap b[4];        // row products: boxes of 16, 32, 64 and 128 tokens
   CUtensorMap out;         // weight gradients: stored by TMA
-  uint16_t *o0, *o1;       // row products: outputs (kGateUp: a, h or null; kActGrad: a, dh)
+  uint16_t *o0, *o1;       // row products: outputs (gate and up: a, h or null; kActGrad: a, dh)
   const uint16_t *h;       // kActGrad: kept gate | up
   int M, N, K;             // features; weight gradients: output columns; row products: contraction
-  int mt;                  // tiles of 256 accumulator rows (kGateUp: of 128 features); 0: no job
+  int mt;                  // tiles of 256 accumulator rows (gate and up: of 128 features); 0: no job
   int a_wide, b_wide;      // MN-major operands: a copy brings 128 rows (else 64) x 64 k
 };
 
@@ -128,17 +129,19 @@ struct RowMaps<kActGrad> {
 // uses for anything else.
 struct UnitCounter {
   unsigned long long next;
-  uint32_t done;           // pairs that have finished
-  uint32_t reserved;
+  uint32_t done;           // pairs that have taken all they will
+  uint32_t epoch;          // kForward: which of `ready` counts this launch's
+  uint32_t ready[2];       // CTAs' halves of tiles of a that are written; the other one is 0
 };
 constexpr int kUnitWord = 1, kTicketWord = 8;            // in WsHeader::reserved
+static_assert(kUnitWord * 4 + sizeof(UnitCounter) <= kTicketWord * 4, "the counters fit");
 static_assert(offsetof(WsHeader, reserved) % 8 == 4, "the unit counter is 8-byte aligned");
 static_assert(kMaxSplit < 16 && kTicketWord + kMaxPairs * 2 * 4 / 32 <= 55, "the tickets fit");
 
 template <int KIND>
 struct PairParams {
-  static constexpr int kJobs = KIND == kRest ? 3 : 1;
-  Job job[kJobs];          // kRest: dx, dWgu, dWd
+  static constexpr int kJobs = KIND == kRest ? 3 : KIND == kForward ? 2 : 1;
+  Job job[kJobs];          // kForward: a, y; kRest: dx, dWgu, dWd
   const int32_t *counts;   // [E], or null (cap rows each)
   WsHeader *hdr;
   float *part;             // partial sums of split contractions
@@ -175,7 +178,8 @@ struct alignas(16) Tile {
   int split, part;         // parts of the tile's contraction, and which this is
   int slot;                // split > 1: tile among those that are cut
   int part_cols;           // and columns that each part's sums have room for
-  int reserved[2];
+  int need;                // halves of tiles of a that have to be written before the tokens are read
+  int epoch;               // where they are counted
 };
 static_assert(sizeof(Tile) == 64, "a tile's record is 64 bytes");
 
@@ -190,16 +194,26 @@ struct Schedule {
   int incl, e0, rows;      // tiles of the batch up to this lane's expert; its tokens
   int64_t whole;           // tiles that are not cut
   int split, part_cols;    // parts of the others, columns of a part's sums
-  __device__ __forceinline__ explicit Schedule(const PairParams<KIND> &p_)
-      : p(p_), base(0), incl(0), e0(0), rows(0), whole(INT64_MAX), split(1), part_cols(0) {
+  int row;                 // the row product that is being dealt out,
+  int64_t first;           // its first unit,
+  int need;                // and what its tiles wait for
+  __device__ __forceinline__ explicit Schedule(const PairParams<KIND> &p_) : p(p_), row(0), first(0), need(0) {
+    start();
+  }
+  __device__ __forceinline__ void start() {
+    base = 0;
+    e0 = 0;
+    whole = INT64_MAX;
+    split = 1;
+    part_cols = 0;
     count();
-    if (KIND != kRest && p.job[0].K >= 16 * kBlockK) choose_split();
+    if (KIND != kRest && p.job[KIND == kForward ? row : 0].K >= 16 * kBlockK) choose_split();
   }
   // At most 2^46 elements of h: the batch's tiles fit an int.
   __device__ __forceinline__ void count() {
     const int lane = threadIdx.x & 31, e = e0 + lane;
     rows = e < p.E ? rows_of(p, e) : 0;
-    incl = token_tiles(rows) * p.job[0].mt;
+    incl = token_tiles(rows) * p.job[KIND == kForward ? row : 0].mt;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
@@ -221,13 +235,13 @@ struct Schedule {
     int most = rows;
     for (int e = 32 + lane; e < p.E; e += 32) {
       const int r = rows_of(p, e);
-      tiles += token_tiles(r) * p.job[0].mt;
+      tiles += token_tiles(r) * p.job[KIND == kForward ? row : 0].mt;
       most = max(most, r);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, d);
     most = __reduce_max_sync(0xFFFFFFFFu, most);
-    const int pairs = gridDim.x >> 1, nk = (p.job[0].K + kBlockK - 1) / kBlockK;
+    const int pairs = gridDim.x >> 1, nk = (p.job[KIND == kForward ? row : 0].K + kBlockK - 1) / kBlockK;
     const int left = (int)(tiles % pairs);
     part_cols = most >= kTileCols ? kTileCols : (most + 31) & ~31;
     // lane s - 1 prices s parts
@@ -240,26 +254,34 @@ struct Schedule {
     whole = tiles - left;
   }
   __device__ __forceinline__ bool find(int64_t unit, Tile &o) {
-    const bool cut = unit >= whole && split > 1;
-    const int in = cut ? (int)(unit - whole) : 0;
-    const int64_t t = cut ? whole + in / split : unit;
+    bool cut;
+    int in;
+    int64_t t;
     while (true) {
+      cut = unit - first >= whole && split > 1;
+      in = cut ? (int)(unit - first - whole) : 0;
+      t = cut ? whole + in / split : unit - first;
       const int64_t end = base + __shfl_sync(0xFFFFFFFFu, incl, 31);
       if (t < end) break;
       base = end;
-      if (e0 + 32 >= p.E) {
-        incl = 0;                            // base now counts every row tile, for good
-        if constexpr (KIND == kRest) return find_weight(t - base, o);
-        else return false;
+      if (e0 + 32 < p.E) {
+        e0 += 32;
+        count();
+        continue;
       }
-      e0 += 32;
-      count();
+      incl = 0;                              // base now counts every row tile, for good
+      if constexpr (KIND == kRest) return find_weight(t - base, o);
+      if (KIND != kForward || row == 1) return false;
+      need = (int)(uint32_t)(2 * base);      // fewer than 2^31 tiles
+      first += split > 1 ? whole + (base - whole) * split : base;
+      row = 1;
+      start();
     }
     const int tb = (int)(t - base);
     const int l = __ffs(__ballot_sync(0xFFFFFFFFu, incl > tb)) - 1;
     const int before = __shfl_sync(0xFFFFFFFFu, incl, l > 0 ? l - 1 : 0);
     const int r = tb - (l > 0 ? before : 0);
-    o.job = 0;
+    o.job = KIND == kForward ? row : 0;
     o.e = e0 + l;
     o.rows = __shfl_sync(0xFFFFFFFFu, rows, l);
     const int nt = token_tiles(o.rows);
@@ -273,7 +295,8 @@ struct Schedule {
       o.cols = min(c, o.rows - o.n0);
     }
     o.n = (o.cols + 31) & ~31;
-    const int nk = (p.job[0].K + kBlockK - 1) / kBlockK;
+    const int nk = (p.job[KIND == kForward ? row : 0].K + kBlockK - 1) / kBlockK;
+    o.need = need;
     o.k0 = 0;
     o.nk = nk;
     o.split = cut ? split : 1;
@@ -310,7 +333,7 @@ struct Schedule {
     o.k0 = 0;
     o.nk = (int)(((unsigned)o.rows + kBlockK - 1) / kBlockK);
     o.split = 1;
-    o.part = o.slot = o.part_cols = 0;
+    o.part = o.slot = o.part_cols = o.need = 0;
     return true;
   }
 };
@@ -322,6 +345,24 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t
   for (uint32_t it = 0; it < (1u << 26); ++it) {
     if (tc::mbar_try(bar, parity)) return true;
     if ((it & 63u) == 63u) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > limit) return false;
+    }
+  }
+  return false;
+}
+
+// Wait until the counter has reached `want` and what was stored before it was
+// raised can be read by asynchronous copies; bounded as wait_bar.
+__device__ __forceinline__ bool wait_count(const uint32_t *counter, uint32_t want, uint64_t limit) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 0; it < (1u << 26); ++it) {
+    if (ld_acquire_gpu(counter) >= want) {
+      tc::fence_async_global();
+      return true;
+    }
+    if ((it & 15u) == 15u) {
       const uint64_t now = global_timer_ns();
       if (t0 == 0) t0 = now;
       else if (now - t0 > limit) return false;
@@ -388,8 +429,9 @@ struct Feed {
 };
 // Words of a record: what the copies and what the matrix instructions need.
 constexpr uint32_t kValid = 1u << 0, kJob = 1u << 1, kExpert = 1u << 2, kRows = 1u << 3, kM = 1u << 4,
-                   kN0 = 1u << 5, kN = 1u << 6, kK0 = 1u << 8, kNk = 1u << 9;
-constexpr uint32_t kCopyWords = kValid | kJob | kExpert | kRows | kM | kN0 | kN | kK0 | kNk;
+                   kN0 = 1u << 5, kN = 1u << 6, kK0 = 1u << 8, kNk = 1u << 9, kNeed = 1u << 14, kEpoch = 1u << 15;
+constexpr uint32_t kCopyWords = kValid | kJob | kExpert | kRows | kM | kN0 | kN | kK0 | kNk |
+                                kNeed | kEpoch;
 constexpr uint32_t kMathWords = kValid | kJob | kRows | kN | kNk;
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -447,6 +489,7 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
   } else if (threadIdx.x == 32 && p.job[0].mt > 0) {
     tc::prefetch_map(&p.job[0].a);
     tc::prefetch_map(&p.job[0].b[0]);
+    if (KIND == kForward) tc::prefetch_map(&p.job[PairParams<KIND>::kJobs - 1].a);
   }
   if (warp == 2) tc::tmem_alloc_pair(tm_slot, kTmemCols);
   tc::fence_before();
@@ -469,33 +512,46 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
   Feed feed(ring, rec_full, tc::map_rank(rec_empty, 0), limit);
 
   if (warp == 3) {
-    // ---- scheduling: each CTA finds the pair's first tile (the first counts
-    // are read together with the status); then one warp of the leader takes
-    // units and announces their tiles to both CTAs
+    // ---- scheduling: one warp of the leader takes units and announces their
+    // tiles to both CTAs.  (The first counts are read together with the status.)
+    // Where no tile waits for another pair's, the pair's first unit is its own
+    // number, and each CTA finds it; in kForward a unit belongs to a pair that
+    // runs, since others will wait for it.
+    constexpr bool kOwnFirst = KIND != kForward;
     Schedule<KIND> sched(p);
     const uint32_t peer_full = tc::map_rank(rec_full, 1), peer_ring = tc::map_rank(smem + kRingOff, 1);
     int64_t unit = blockIdx.x >> 1;
-    for (uint32_t c = 0; live; ++c) {
+    bool written = false;                    // kForward: all of a
+    const uint32_t epoch = KIND == kForward && rank == 0 ? p.units->epoch & 1u : 0u;
+    for (uint32_t c = 0; live && (kOwnFirst || rank == 0); ++c) {
       const uint32_t s = c % kRing;
-      if (c > 0) {
+      if (c > 0 || !kOwnFirst) {
         // A unit is taken as late as its tile allows: once the record 2 or
         // kRing before it has been read by every warp of both CTAs.
-        const uint32_t ahead = t.nk >= kLongTile ? 2 : kRing;
+        const uint32_t ahead = c > 0 && t.nk >= kLongTile ? 2 : kRing;
         if (c >= ahead) {
           const uint32_t r = c - ahead;
           ok = __all_sync(0xFFFFFFFFu, wait_bar(rec_empty + 8 * (r % kRing), (r / kRing) & 1u, limit));
           if (!ok) break;
         }
+        // one tile of y for each pair until all of a is written: a second one
+        // would be missing where a pair is still busy with a
+        if (KIND == kForward && c > 0 && t.need != 0 && !written) {
+          written = ok =
+              __all_sync(0xFFFFFFFFu, wait_count(p.units->ready + epoch, (uint32_t)t.need, limit));
+          if (!ok) break;
+        }
         unsigned long long n = 0;
         if (lane == 0) n = atomicAdd(&p.units->next, 1ull);
-        unit = (gridDim.x >> 1) + (int64_t)__shfl_sync(0xFFFFFFFFu, n, 0);
+        unit = (kOwnFirst ? gridDim.x >> 1 : 0) + (int64_t)__shfl_sync(0xFFFFFFFFu, n, 0);
       }
       t.valid = sched.find(unit, t);
+      t.epoch = epoch;
       if (lane == 0) {
         ring[s] = t;
         tc::mbar_arrive_local(rec_full + 8 * s);
       }
-      if (c > 0) {
+      if (c > 0 || !kOwnFirst) {
         __syncwarp();
         if (lane == 0) tc::mbar_expect_at(peer_full + 8 * s, sizeof(Tile));
         if (lane < 4)
@@ -506,8 +562,14 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     }
     if (rank == 0 && lane == 0 &&
         atomicAdd(&p.units->done, 1u) == (gridDim.x >> 1) - 1) {
+      // every pair knows this launch's epoch by now: the next one counts in the
+      // other counter, which nobody uses any more
       p.units->next = 0;
       p.units->done = 0;
+      if (KIND == kForward) {
+        p.units->ready[epoch ^ 1u] = 0;
+        p.units->epoch = epoch ^ 1u;
+      }
     }
   } else if (live && warp == 0) {
     // ---- TMA: both CTAs load their halves; bytes complete on the leader's barrier
@@ -515,8 +577,9 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     uint32_t ph = 0;
     const uint32_t full0 = tc::map_rank(full, 0);
     const CUtensorMap *held = nullptr;       // kRest: the maps acquired last
+    bool written = false;                    // kForward: all of a
     while (ok && feed.next_uniform<kCopyWords>(t, ok)) {
-      const Job &j = p.job[KIND == kRest ? t.job : 0];
+      const Job &j = p.job[KIND != kActGrad ? t.job : 0];
       const bool weight = KIND == kRest && t.job > 0;
       const uint32_t half_n = t.n >> 1;
       const int bsel = half_n <= 16 ? 0 : half_n <= 32 ? 1 : half_n <= 64 ? 2 : 3;
@@ -532,6 +595,12 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
           held = map_a;
         }
       }
+      if (KIND == kForward && t.need != 0 && !written) {
+        written = ok = __all_sync(0xFFFFFFFFu, wait_count(p.units->ready + t.epoch, (uint32_t)t.need, limit));
+        if (!ok) break;
+      }
+      // 64 gate rows and the same 64 features of up in one copy, or 128 features
+      const int a0 = KIND == kForward && t.job == 0 ? t.m * 128 + (int)rank * 64 : m0;
       // 128 rows of an MN-major operand from row r on: 64 rows a copy, or all
       const auto load_mn = [&](uint32_t dst, const CUtensorMap *map, int wide, uint32_t bar, int r, int k0) {
         if (wide) {
@@ -548,12 +617,10 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
         const int k0 = (t.k0 + kb) * kBlockK;
         const uint32_t bar = full0 + 8 * s;
         if (rank == 0) tc::mbar_expect_warp(full + 8 * s, 2 * bytes);
-        if (KIND == kGateUp)                 // 64 gate rows and the same 64 features of up
-          tc::tma_load_pair(sa, map_a, bar, k0, t.m * 128 + (int)rank * 64, 0, t.e);
-        else if (kAMn)
+        if (kAMn)
           load_mn(sa, map_a, j.a_wide, bar, m0, k0);
         else
-          tc::tma_load_pair(sa, map_a, bar, k0, m0, 0, t.e);
+          tc::tma_load_pair(sa, map_a, bar, k0, a0, 0, t.e);
         if (weight)
           load_mn(sb, map_b, j.b_wide, bar, n0, k0);
         else
@@ -655,10 +722,11 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     while (true) {
       const bool more = feed.next(t, ok);
       const uint32_t buf = it & 1u;
-      const Job &j = p.job[KIND == kRest ? t.job : 0];
+      const Job &j = p.job[KIND != kActGrad ? t.job : 0];
+      const bool gate = KIND == kForward && t.job == 0;
       // a thread's place in the staged chunk: 4 features of rows r8, r8 + 8, ...
       const int i4 = tid & 15, r8 = tid >> 4;
-      const int f0 = KIND == kGateUp ? t.m * 128 + (int)rank * 64 + 4 * i4
+      const int f0 = gate ? t.m * 128 + (int)rank * 64 + 4 * i4
                                      : t.m * 256 + (int)rank * 128 + 4 * i4;
       const int64_t row0 = (int64_t)t.e * p.cap + t.n0;
       uint2 g[4][2], u[4][2];                // kActGrad: kept gate and up of a chunk
@@ -677,7 +745,7 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
       const auto emit = [&](int tok, int r, const float4 &lo4, const float4 &hi4) {
         const float lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
         const int64_t row = row0 + tok;
-        if (KIND == kGateUp) {               // lo: gate, hi: up of the same features
+        if (gate) {                          // lo: gate, hi: up of the same features
           if (f0 < j.M) {
             float a[4];
 #pragma unroll
@@ -727,6 +795,7 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_remote(empty0 + 8 * buf);
       };
+      bool wrote = true;                     // this was the tile's last part
       if (KIND == kRest && t.job > 0) {
         // each warp on its own: 32 rows x 64 columns of bf16, swizzled, stored by TMA
         const int m0 = t.m * 256 + (int)rank * 128 + wq * 32;
@@ -790,7 +859,8 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
           __threadfence();
         }
         named_sync(3, 32 * kEpiWarps);
-        if (*last_in != 0)
+        wrote = *last_in != 0;
+        if (wrote)
           for (int c = grp * 32; c < t.n; c += 64) {
             float4 lo[4], hi[4];
 #pragma unroll
@@ -830,6 +900,16 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
                    *reinterpret_cast<const float4 *>(st + tok * 128 + 64 + 4 * i4));
           }
           if (KIND == kActGrad && c + 64 < t.n) load_h(c + 64);
+        }
+      }
+      if (gate && wrote) {
+        // half a tile of a is written, for copies of other CTAs to read
+        tc::fence_async_global();
+        __threadfence();
+        named_sync(3, 32 * kEpiWarps);
+        if (threadIdx.x == 128) {
+          __threadfence();
+          atomicAdd(p.units->ready + t.epoch, 1u);
         }
       }
       if (t.nk > 0) ++it;
@@ -978,28 +1058,21 @@ FfnScratch ffn_scratch(int64_t E, int64_t cap, int64_t H, int64_t I) {
 }
 
 cudaError_t launch_ffn(const FfnParams &f, cudaStream_t stream) {
-  {
-    PairParams<kGateUp> p = base_params<kGateUp>(f);
-    Job &j = p.job[0];
-    if (!make_map(&j.a, f.w_gate_up, f.H, f.I, 2, f.E, 64, 2) || !token_maps(j, f.x, f.H, f.cap, f.E))
-      return cudaErrorInvalidValue;
-    j.o0 = f.act;
-    j.o1 = f.h;
-    j.M = f.I;
-    j.K = f.H;
-    j.mt = (int)cdiv(f.I, 128);
-    const cudaError_t e = launch_pair<kGateUp>(p, units(j, f), stream);
-    if (e != cudaSuccess) return e;
-  }
-  PairParams<kDown> p = base_params<kDown>(f);
-  Job &j = p.job[0];
-  if (!make_map(&j.a, f.w_down, f.I, f.H, 1, f.E, 128) || !token_maps(j, f.act, f.I, f.cap, f.E))
+  PairParams<kForward> p = base_params<kForward>(f);
+  Job &gu = p.job[0], &d = p.job[1];
+  if (!make_map(&gu.a, f.w_gate_up, f.H, f.I, 2, f.E, 64, 2) || !token_maps(gu, f.x, f.H, f.cap, f.E) ||
+      !make_map(&d.a, f.w_down, f.I, f.H, 1, f.E, 128) || !token_maps(d, f.act, f.I, f.cap, f.E))
     return cudaErrorInvalidValue;
-  j.o0 = f.y;
-  j.M = f.H;
-  j.K = f.I;
-  j.mt = (int)cdiv(f.H, 256);
-  return launch_pair<kDown>(p, units(j, f), stream);
+  gu.o0 = f.act;
+  gu.o1 = f.h;
+  gu.M = f.I;
+  gu.K = f.H;
+  gu.mt = (int)cdiv(f.I, 128);
+  d.o0 = f.y;
+  d.M = f.H;
+  d.K = f.I;
+  d.mt = (int)cdiv(f.H, 256);
+  return launch_pair<kForward>(p, units(gu, f) + units(d, f), stream);
 }
 
 cudaError_t launch_ffn_backward(const FfnParams &f, cudaStream_t stream) {

@@ -112,6 +112,10 @@ __device__ __forceinline__ void store_wait_read() {
 __device__ __forceinline__ void store_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
+// Between ordinary accesses to global memory and asynchronous copies of it.
+__device__ __forceinline__ void fence_async_global() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+}
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
