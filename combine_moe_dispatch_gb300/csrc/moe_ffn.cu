@@ -7,8 +7,8 @@
 //   da = dy Wd,  dgate = da up s (1 + gate (1 - s)),  dup = da gate s,
 //   dx = dh Wgu,  dWgu = dh^T x,  dWd = dy^T a.
 //
-// How: four launches of pair_kernel<KIND>: kGateUp and kDown forward, kActGrad
-// (da, and from it a and dh) and kRest (dx, dWgu and dWd) backward.  A cluster
+// How: one launch of pair_kernel<KIND> forward, kForward (a, then y), and two
+// backward, kActGrad (da, and from it a and dh) and kRest (dx, dWgu and dWd).  A cluster
 // of two CTAs (the two SMs of a pair) computes a tile of 256 rows x up to 256
 // columns with tcgen05.mma.cta_group::2: each CTA stages its half of both
 // operands (128 rows of A, half the columns of B, 64 k at a time) by TMA in a
@@ -33,6 +33,17 @@
 //    1310 us, now 1220.)
 //  - Few tiles and a long contraction (few tokens): the tiles of the last,
 //    partial round are cut into parts whose sums are joined, see choose_split.
+//  - Forward, a tile of y needs all of its rows of a.  Its first copy waits, with
+//    a limit, until a counter says that every tile of a is written.  Units come
+//    from a counter in order, so that those that are waited for are with pairs
+//    that run, and wait for nothing themselves.  Two launches against one: 61 odd
+//    rows 10.3 and 8.9 us, ten rows over 95 experts 28.4 and 25.6, 128 rows of one
+//    expert 36.6 and 34.1, one token 117.7 and 114.9; batch and decode the same.
+//    The backward pass in one launch as well: 128 rows 11.7 and 10.6 us, batch
+//    sizes the same, but uneven experts 207 (two launches) and 214, few rows of
+//    many experts 271 and 288, so that it stays at two.  Bringing Wd into the L2
+//    during the wait: one token 111.9 us without, 113.2 and 115.5 with 12 and 40
+//    blocks a tile.
 // Counts are read on the device: nothing waits for the host, and the call can
 // be captured in a CUDA graph.  Tiles go to the pairs in order, as they get
 // free: what runs at one time is then a stretch of the list, whose operands
@@ -47,11 +58,12 @@
 // seconds-long bursts, 1.71 sustained under the power limit):
 //  - Mixtral-shaped batch (8192 rows over 8 experts, H 4096, I 14336): forward
 //    1.78 ms (1.62 PFLOP/s), backward 3.78 ms (1.53).  The tensor pipe is
-//    active 92 to 94 % of the cycles (kActGrad 79 %, its epilogue reads h);
+//    active 92 to 94 % of the cycles (each product by itself; kActGrad 79 %, its
+//    epilogue reads h);
 //    the clock, 1.32 to 1.36 GHz at 1.37 kW, is what the power limit leaves.
 //  - DeepSeek-V3-shaped decode (256 experts, 32 rows each, 22.5 GB of weights):
 //    3.33 ms, 6.85 TB/s: the weights' reading.  One token over two experts of
-//    the Mixtral shape: 117 us for 705 MB.
+//    the Mixtral shape: 112 to 115 us for 705 MB.
 //  - Weight gradients of experts with few rows: the writing.  64 experts of 128
 //    rows, 2.1 GB of dWgu: 5.1 TB/s (a plain fill of memory reaches 4.1).
 //  - Tiny calls: latency, about 5 us a launch from the end of the one before:
@@ -123,10 +135,10 @@ struct RowMaps<kActGrad> {
   CUtensorMap whole[kRowMaps];
 };
 
-// The launch's next unit of work, past the first of every pair: the last pair
-// to finish resets it.  It and the tickets are zero between launches and stand
-// in the workspace header's reserved words, the one place that no shape's plan
-// uses for anything else.
+// The launch's next unit of work (backward: past the first of every pair): the
+// last pair to finish resets it.  It and the tickets are zero between launches
+// and stand with the other counters in the workspace header's reserved words,
+// the one place that no shape's plan uses for anything else.
 struct UnitCounter {
   unsigned long long next;
   uint32_t done;           // pairs that have taken all they will
@@ -522,7 +534,7 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     const uint32_t peer_full = tc::map_rank(rec_full, 1), peer_ring = tc::map_rank(smem + kRingOff, 1);
     int64_t unit = blockIdx.x >> 1;
     bool written = false;                    // kForward: all of a
-    const uint32_t epoch = KIND == kForward && rank == 0 ? p.units->epoch & 1u : 0u;
+    const uint32_t epoch = KIND == kForward && rank == 0 ? __ldcg(&p.units->epoch) & 1u : 0u;
     for (uint32_t c = 0; live && (kOwnFirst || rank == 0); ++c) {
       const uint32_t s = c % kRing;
       if (c > 0 || !kOwnFirst) {
@@ -535,7 +547,8 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
           if (!ok) break;
         }
         // one tile of y for each pair until all of a is written: a second one
-        // would be missing where a pair is still busy with a
+        // would be missing where a pair is still busy with a (one token 132
+        // us, now 115; 32 rows over eight such experts 451 and 420)
         if (KIND == kForward && c > 0 && t.need != 0 && !written) {
           written = ok =
               __all_sync(0xFFFFFFFFu, wait_count(p.units->ready + epoch, (uint32_t)t.need, limit));

@@ -336,7 +336,7 @@ moe_status moe_silu_mul_quant(const moe_shape *shape, int32_t intermediate, cons
  * and higher throughput with multi-node DeepSeek deployment", GroupGEMM and
  * Quantization (grouped products over the experts' contiguous rows that read
  * the per-expert token counts, not the buffer sizes, so that they stay valid
- * in a CUDA graph).  Two launches on the tensor cores; operands bf16, sums in
+ * in a CUDA graph).  One launch on the tensor cores; operands bf16, sums in
  * binary32, one rounding to bf16 of a, of y and of the kept h.
  * In:   expert_x  [E, cap, H] bf16 (from moe_dispatch); rows from the count
  *                 on are never used, whatever they hold;
@@ -376,7 +376,8 @@ moe_status moe_ffn(const moe_shape *shape, int32_t intermediate, const void *exp
  * In:   d_expert_y [E, cap, H] (from moe_combine_backward), expert_x, expert_h
  *       (as moe_ffn kept it), the weights and the counts of the forward call.
  * Out:  expert_act [E, cap, intermediate] and d_expert_h [E, cap, 2*intermediate]
- *       bf16 (computed here, read by the second launch; rows below the count); d_expert_x [E, cap, H] bf16 (rows below the count);
+ *       bf16 (computed here, read by the second launch; rows below the
+ *       count); d_expert_x [E, cap, H] bf16 (rows below the count);
  *       d_w_gate_up [E, 2*intermediate, H] and d_w_down [E, H, intermediate]
  *       bf16, every element written: 0 for an expert without rows.  Each of
  *       d_expert_x, d_w_gate_up and d_w_down may be NULL: not computed.
