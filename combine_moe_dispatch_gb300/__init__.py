@@ -314,7 +314,9 @@ def ffn_backward(shape: Shape, intermediate: int, d_expert_y, expert_x, expert_h
 
 def combine_backward(shape: Shape, d_y, expert_y, topk_idx, slot_of, topk_weights, d_expert_y,
                      d_weights, d_logits, workspace, stream=None, check=True) -> Status:
-    """moe_combine_backward; ``d_logits`` may be None."""
+    """moe_combine_backward; ``d_logits`` may be None.  An entry that was left
+    out after the router's softmax keeps its expert in ``topk_idx`` (its
+    ``slot_of`` is -1), so that its logit gets its gradient."""
     st = load_library().moe_combine_backward(ctypes.byref(shape), _ptr(d_y), _ptr(expert_y),
                                              _ptr(topk_idx), _ptr(slot_of), _ptr(topk_weights),
                                              _ptr(d_expert_y), _ptr(d_weights), _ptr(d_logits),

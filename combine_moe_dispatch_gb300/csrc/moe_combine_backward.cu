@@ -6,8 +6,10 @@
 //   d_expert_y[e][s] = w[g,k] dy[g]
 //   d_weights[g,k]   = <dy[g], expert_y[e][s]>
 //   d_logits[g,idx]  = w[g,k] (d_weights[g,k] - sum_j w[g,j] d_weights[g,j])
-// The last line is the softmax's backward pass over the chosen logits; the
-// logits that were not chosen get 0.
+// The last line is the softmax's backward pass over the K chosen logits, with
+// d_weights = 0 for an entry that was left out afterwards (slot_of = -1): its
+// logit is in the softmax's denominator and gets -w sum_j w_j d_weights_j.
+// The logits that were not chosen get 0.
 //
 // How: WPT warps share a token.  Each lane reads 16 bytes of dy once and, for
 // a group of KG entries, the same 16 bytes of every expert row, so that KG x U
@@ -62,6 +64,8 @@ combine_backward_kernel(CombineBackwardParams p) {
     if (sub == 0 && routed && !ok)
       report_status(p.hdr, e_ok ? MOE_ERR_CAPACITY : MOE_ERR_BAD_EXPERT);
     const unsigned okmask = __ballot_sync(kFull, ok);
+    const bool left_out = on && lane < p.K && s_l == -1 && e_ok;
+    const unsigned chosen = okmask | __ballot_sync(kFull, left_out);
     for (int kb = 0; kb < p.K; kb += KG) {
       float dot[KG];
       int64_t off[KG];
@@ -130,16 +134,22 @@ combine_backward_kernel(CombineBackwardParams p) {
         for (int i = 0; i < WPT; ++i) dw += s_dot[warp + i][lane];
       if (lane < p.K) p.d_weights[g * p.K + lane] = dw;
       if (p.d_logits) {
-        const float wk = ok ? w_l : 0.0f;
+        // Entries of the softmax: the routed ones, and those left out of a token
+        // that has others.  A token with nothing routed (padding, say) has y = 0
+        // whatever its logits are: its weights may be anything, and count as 0.
+        const float wk = ok || (left_out && okmask != 0u) ? w_l : 0.0f;
         float mean = 0.0f;
-        for (int k = 0; k < p.K; ++k) mean = fmaf(__shfl_sync(kFull, wk, k), __shfl_sync(kFull, dw, k), mean);
+        for (int k = 0; k < p.K; ++k) {
+          const float term = __shfl_sync(kFull, wk, k), dk = __shfl_sync(kFull, dw, k);
+          if ((okmask >> k) & 1u) mean = fmaf(term, dk, mean);
+        }
         // an expert chosen twice gets the sum of its entries
         const float own = wk * (dw - mean);
         float sum = 0.0f;
         for (int k = 0; k < p.K; ++k) {
           const int ek = __shfl_sync(kFull, e_l, k);
           const float dk = __shfl_sync(kFull, own, k);
-          if (((okmask >> k) & 1u) && ek == e_l) sum += dk;
+          if (((chosen >> k) & 1u) && ek == e_l) sum += dk;
         }
         s_dot[warp][lane] = sum;                  // written after the row's zeros, below
       }
@@ -147,7 +157,7 @@ combine_backward_kernel(CombineBackwardParams p) {
     if (p.d_logits) {
       if (WPT == 1) __syncwarp();
       else __syncthreads();
-      if (sub == 0 && ok) p.d_logits[g * p.E + e_l] = s_dot[warp][lane];
+      if (sub == 0 && (ok || left_out)) p.d_logits[g * p.E + e_l] = s_dot[warp][lane];
     }
     // s_dot is written again in the next round
     if (WPT == 1) __syncwarp();

@@ -393,14 +393,23 @@ moe_status moe_ffn_backward(const moe_shape *shape, int32_t intermediate, const 
  *   d_expert_y[e][s] = bf16( topk_weights[g,k] * d_y[g] )
  *   d_weights[g,k]   = sum over h of d_y[g][h] * expert_y[e][s][h]
  *   d_logits[g][e]   = w_k * (d_weights[g,k] - sum over j of w_j * d_weights[g,j])
- * (moe_router_topk's softmax over the chosen logits; every other logit of the
- * token gets 0, an expert chosen twice the sum of its entries).
+ * The last line is the derivative of moe_router_topk's weights, a softmax over
+ * the token's K chosen logits.  An entry left out after the softmax (slot_of =
+ * -1 beside others that are routed) has d_weights = 0 but is still in that
+ * softmax: with its expert in topk_idx, its logit gets -w_k * (the same sum).
+ * With topk_idx = -1 its expert is not known and nothing is written for it;
+ * the other entries' values are right either way.  Weights normalised over the
+ * routed entries alone are the same formula with w_k = 0 for the rest.  A
+ * token with nothing routed gets 0, and none of its weights is used.  Every
+ * logit that was not chosen gets 0, an expert chosen twice the sum of its
+ * entries.
  *
  * The gradient of the dispatched rows goes back to the tokens by moe_combine
  * itself, with weights of 1: d_x[g] = sum over k of d_expert_x[e][s].  With
  * moe_combine_shared, the shared expert's output has the gradient d_y.
  * In:   d_y [N, H] bf16, expert_y [E, cap, H] bf16 (16-byte aligned);
- *       topk_idx, slot_of, topk_weights [N, K] as moe_combine.
+ *       topk_idx, slot_of, topk_weights [N, K] as moe_combine; the weight of
+ *       an unrouted entry is read with d_logits alone, as above.
  * Out:  d_expert_y [E, cap, H] bf16, the routed rows only; d_weights [N, K]
  *       fp32, 0 for entries that are not routed; d_logits [N, E] fp32, every
  *       element written, or NULL.
