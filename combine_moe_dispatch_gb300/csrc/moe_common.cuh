@@ -55,7 +55,7 @@ struct WsHeader {
   uint32_t epoch;       // plan launches so far; tags this launch's flags
   uint32_t err_bits;    // errors seen by the running plan (kErr*)
   int32_t status;       // moe_status of the last plan (and of later dispatch/combine)
-  uint32_t debug_flags; // kDebug* test hooks
+  uint32_t debug_flags; // kDebug* test hooks; kFfnBroken
   uint64_t timeout_ns;  // limit of every wait; 0 = kDefaultTimeoutNs
   uint32_t arrivals;    // fused plan+dispatch: blocks arrived (bits 0-7), blocks whose table
                         // copy timed out (8-15), that saw a bad expert (16-23) or an
@@ -68,6 +68,7 @@ constexpr uint32_t kErrBadExpert = 1u;
 constexpr uint32_t kErrCapacity = 2u;
 constexpr uint32_t kErrTimeout = 4u;
 constexpr uint32_t kDebugHoldTile0 = 1u;
+constexpr uint32_t kFfnBroken = 1u << 31;   // a wait of the feed-forward ran out (set for good)
 constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }

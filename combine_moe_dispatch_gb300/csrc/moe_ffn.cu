@@ -146,6 +146,23 @@ struct UnitCounter {
   uint32_t ready[2];       // CTAs' halves of tiles of a that are written; the other one is 0
 };
 constexpr int kUnitWord = 1, kTicketWord = 8;            // in WsHeader::reserved
+// A wait that runs out leaves the counters and tickets unfinished, and the
+// next plan replaces the status: a split tile would then be joined one part too
+// early.  kFfnBroken stays until moe_workspace_init clears the header.  It stands
+// beside the status, so that one load brings both: read from a word of the
+// counters' own sector it cost 0.25 us per launch.
+static_assert(offsetof(WsHeader, status) % 8 == 0 &&
+              offsetof(WsHeader, debug_flags) == offsetof(WsHeader, status) + 4, "read together");
+struct StatusWords {
+  int32_t status;
+  uint32_t flags;
+};
+__device__ __forceinline__ StatusWords read_status_words(const WsHeader *hdr) {
+  StatusWords w;
+  asm volatile("ld.volatile.global.v2.u32 {%0, %1}, [%2];"
+               : "=r"(w.status), "=r"(w.flags) : "l"(&hdr->status) : "memory");
+  return w;
+}
 static_assert(kUnitWord * 4 + sizeof(UnitCounter) <= kTicketWord * 4, "the counters fit");
 static_assert(offsetof(WsHeader, reserved) % 8 == 4, "the unit counter is 8-byte aligned");
 static_assert(kMaxSplit < 16 && kTicketWord + kMaxPairs * 2 * 4 / 32 <= 55, "the tickets fit");
@@ -513,11 +530,14 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
 
   pdl_allow_dependents();
   pdl_wait_for_previous();
-  // After a plan error no tile is computed and nothing is written.  The block's
-  // threads decide together: the status may change under them when another
-  // pair's wait runs out.
+  // After a plan error, or a wait of an earlier launch that ran out, no tile is
+  // computed and nothing is written.  The block's threads decide together: both
+  // words may change under them when another pair's wait runs out.
   const uint64_t tmo = p.hdr->timeout_ns;
-  const bool live = __syncthreads_and(read_status(p.hdr) == MOE_OK);
+  const StatusWords words = read_status_words(p.hdr);
+  const bool broken = (words.flags & kFfnBroken) != 0;
+  const bool live = __syncthreads_and(words.status == MOE_OK && !broken);
+  if (broken && threadIdx.x == 0) report_status(p.hdr, MOE_ERR_TIMEOUT);
   const uint64_t limit = tmo ? tmo : kDefaultTimeoutNs;
   bool ok = true;
   Tile t;
@@ -934,6 +954,7 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     // a wait ran out: report it, and give the copies and products that are
     // already issued (microseconds of work) time to land before the exit
     if (lane == 0) {
+      atomicOr(&p.hdr->debug_flags, kFfnBroken);
       report_status(p.hdr, MOE_ERR_TIMEOUT);
       for (int i = 0; i < 1000; ++i) __nanosleep(10000);
     }

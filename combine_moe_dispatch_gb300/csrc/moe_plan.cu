@@ -448,7 +448,7 @@ plan_cluster_kernel(PlanParams p) {
 }
 
 __global__ void set_debug_kernel(WsHeader *hdr, uint32_t flags, uint64_t timeout_ns) {
-  hdr->debug_flags = flags;
+  hdr->debug_flags = (flags & ~kFfnBroken) | (hdr->debug_flags & kFfnBroken);
   hdr->timeout_ns = timeout_ns;
 }
 

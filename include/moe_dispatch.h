@@ -90,7 +90,8 @@ size_t moe_workspace_size(const moe_shape *shape);
 /* Zero a workspace before its first use (enqueued on `stream`).  After
  * that the workspace keeps its counters consistent by itself, across shapes
  * and across calls that reported an error (the last thread block of every
- * moe_plan resets them).  A zero-filled allocation is already initialised.
+ * moe_plan resets them); a TIMEOUT of moe_ffn or moe_ffn_backward alone needs
+ * this call again.  A zero-filled allocation is already initialised.
  * Errors: INVALID_ARG (null), ALIGNMENT (not 16-byte aligned), CUDA. */
 moe_status moe_workspace_init(void *workspace, size_t workspace_bytes, void *stream);
 
@@ -353,8 +354,10 @@ moe_status moe_silu_mul_quant(const moe_shape *shape, int32_t intermediate, cons
  *       than moe_workspace_size); nothing is written if its status word is
  *       set, and a wait inside a kernel that runs out sets it to TIMEOUT.
  *       Its counters stand in the workspace's first 256 bytes, so that one
- *       workspace serves calls of different shapes in turn.  After TIMEOUT
- *       initialise the workspace again before its next use.
+ *       workspace serves calls of different shapes in turn.  A wait of
+ *       moe_ffn or moe_ffn_backward that ran out may leave them unfinished:
+ *       from then on both write nothing and report TIMEOUT, also after another
+ *       plan, until moe_workspace_init clears the workspace.
  * Limits: payload BF16; intermediate % 8 == 0, intermediate < 2^29, H < 2^30;
  *       E * cap * 2 * intermediate and E * cap * H < 2^46; 4 * intermediate * H
  *       < 2^40.  All bf16 arrays 16-byte aligned.  No output may overlap an
@@ -499,7 +502,8 @@ moe_status moe_plan_noalloc(const moe_shape *shape, const int32_t *topk_idx,
 /* Test hook (enqueued on `stream`): `flags` bit 0 makes the first tile of
  * the next moe_plan calls withhold its counts from the others, so their
  * bounded waits run out and the call reports MOE_ERR_TIMEOUT;
- * `timeout_ns` replaces the 1 s default limit of those waits (0 = default).
+ * `timeout_ns` replaces the 1 s default limit of those waits and of
+ * moe_ffn's and moe_ffn_backward's (0 = default).  Bit 31 is ignored.
  * Errors: INVALID_ARG, CUDA. */
 moe_status moe_workspace_set_debug(void *workspace, uint32_t flags,
                                    uint64_t timeout_ns, void *stream);
