@@ -416,8 +416,7 @@ struct Feed {
     if (!ok) return false;
     t = ring[s];
     __syncwarp();
-    done();
-    return t.valid != 0;
+    return done(t);
   }
   // The same for the words of WORDS (a bit each) alone, through shuffles, so
   // that the compiler knows the values to be the same in every lane.  In two
@@ -437,8 +436,7 @@ struct Feed {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if ((WORDS >> i) & 1u) w[i] = __shfl_sync(0xFFFFFFFFu, r.word, i);
-    done();
-    return t.valid != 0;
+    return done(t);
   }
   template <uint32_t WORDS>
   __device__ __forceinline__ bool next_uniform(Tile &t, bool &ok) {
@@ -448,12 +446,16 @@ struct Feed {
   }
 
  private:
-  __device__ __forceinline__ void done() {     // every lane has read the record
+  // Every lane has read the record.  The last one's place is not used again, and
+  // nobody waits for it.
+  __device__ __forceinline__ bool done(const Tile &t) {
+    if (t.valid == 0) return false;
     tc::mbar_arrive_warp_at(empty + 8 * s);
     if (++s == kRing) {
       s = 0;
       ph ^= 1u;
     }
+    return true;
   }
 };
 // Words of a record: what the copies and what the matrix instructions need.
@@ -555,7 +557,8 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     int64_t unit = blockIdx.x >> 1;
     bool written = false;                    // kForward: all of a
     const uint32_t epoch = KIND == kForward && rank == 0 ? __ldcg(&p.units->epoch) & 1u : 0u;
-    for (uint32_t c = 0; live && (kOwnFirst || rank == 0); ++c) {
+    uint32_t c = 0;
+    for (; live && (kOwnFirst || rank == 0); ++c) {
       const uint32_t s = c % kRing;
       if (c > 0 || !kOwnFirst) {
         // A unit is taken as late as its tile allows: once the record 2 or
@@ -593,6 +596,11 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
       }
       if (!t.valid || rank != 0) break;
     }
+    // the other CTA's arrivals for the records before the last (number c) land
+    // before this one may exit
+    if (live && rank == 0)
+      for (uint32_t r = c < kRing ? 0 : c - kRing + 1; ok && r < c; ++r)
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(rec_empty + 8 * (r % kRing), (r / kRing) & 1u, limit));
     if (rank == 0 && lane == 0 &&
         atomicAdd(&p.units->done, 1u) == (gridDim.x >> 1) - 1) {
       // every pair knows this launch's epoch by now: the next one counts in the
@@ -735,6 +743,9 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
       if (ok) more = have ? feed.spread<kMathWords>(next_raw, t) : feed.next_uniform<kMathWords>(t, ok);
       ++it;
     }
+    // the other CTA's arrivals for both accumulators land before this one may exit
+    for (int i = 0; ok && i < 2; ++i, ++it)
+      ok = __all_sync(0xFFFFFFFFu, wait_bar(tm_empty + 8 * (it & 1u), ((it >> 1) & 1u) ^ 1u, limit));
   } else if (live && warp == 2 && KIND == kActGrad) {
     // ---- the weight gradients' tensor maps: each block writes some experts'
     if constexpr (KIND == kActGrad) {
@@ -960,7 +971,11 @@ pair_kernel(const __grid_constant__ PairParams<KIND> p) {
     }
   }
   // Neither CTA leaves while the other may still use its shared or tensor
-  // memory or its barriers; nothing is handed over, so nothing is released.
+  // memory or its barriers.  The cluster barrier orders nothing: every arrival,
+  // copy and commit that comes from the other CTA has been waited for above, by
+  // the warp that needed it or, where nobody did (records and accumulators that
+  // are free, the last stages' commits), by their owner at its end.  A barrier
+  // that releases instead: backward of 128 rows 12.3 us, so 12.0.
   __syncwarp();
   tc::fence_before();
   __syncthreads();
