@@ -417,8 +417,10 @@ moe_status moe_ffn_backward(const moe_shape *shape, int32_t intermediate, const 
  *       fp32, 0 for entries that are not routed; d_logits [N, E] fp32, every
  *       element written, or NULL.
  * Work: the workspace moe_plan used; nothing is written if its status word
- *       is set; entries out of range are skipped and set it; entries with
- *       slot_of = -1 (not routed) are skipped silently.
+ *       is set.  An entry whose expert or slot is out of range is skipped and
+ *       sets it (BAD_EXPERT / CAPACITY); which other tokens' outputs that call
+ *       still writes is then not specified, since blocks that start later find
+ *       the status set.  Entries with slot_of = -1 (not routed) are no error.
  * Host errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA. */
 moe_status moe_combine_backward(const moe_shape *shape, const void *d_y, const void *expert_y,
                                 const int32_t *topk_idx, const int32_t *slot_of,

@@ -123,3 +123,38 @@ def test_chosen_twice_and_left_out_once():
         own = w.to(D) * (dw64 - (w.to(D) * dw64).sum(1, keepdim=True))
         dl64 = torch.zeros((N, E), dtype=D, device="cuda").scatter_add_(1, idx.long(), own)
         _near(dl, dl64, torch.full_like(dl64, 4 * H * U24 * float(mag.max())), f"d_logits, share {share}")
+
+
+@pytest.mark.parametrize("kind", ["expert", "negative expert", "slot", "negative slot"])
+def test_entries_out_of_range(kind):
+    """One entry out of range, in a batch that one block handles (so that no block
+    starts after the error): it is skipped, its logit gets nothing and its row
+    is not written, the status reports it, and every other entry is as without it."""
+    N, H, E, K = 6, 64, 4, 3
+    drop = torch.zeros((N, K), dtype=torch.bool, device="cuda")
+    moe, shape, _, idx, _, w, b, dy, _, (dey, dw, dl) = _case(N, H, E, K, drop)
+    ey = _normal((E, N, H), 1.0, 8)
+    bad_idx, bad_slot, at = idx.clone(), b.slot_of.clone(), (2, 1)
+    if kind.endswith("expert"):
+        bad_idx[at] = -7 if "negative" in kind else E
+    else:
+        bad_slot[at] = -2 if "negative" in kind else N
+    moe.combine_backward(shape, dy, ey, bad_idx, bad_slot, w, dey, dw, dl, b.workspace)
+    assert moe.read_status(b.workspace) == (moe.Status.BAD_EXPERT if kind.endswith("expert") else
+                                            moe.Status.CAPACITY)
+    ok = torch.ones((N, K), dtype=torch.bool, device="cuda")
+    ok[at] = False
+    e, s = idx.long(), b.slot_of.long()
+    assert bool((dey[e[at], s[at]] == SENTINEL).all())
+    want = w.to(D)[:, :, None] * dy.to(D)[:, None, :]
+    got = dey[e, s].to(D)
+    assert bool(((got - want).abs() <= (2.0 ** -8 + 2.0 ** -23) * want.abs())[ok].all())
+    terms = torch.where(ok[:, :, None], ey[e, s].to(D) * dy.to(D)[:, None, :], 0.0)
+    dw64, dw_tol = terms.sum(2), H * U24 * terms.abs().sum(2)
+    _near(dw, dw64, dw_tol, "d_weights")
+    w64 = torch.where(ok, w.to(D), 0.0)
+    own = w64 * (dw64 - (w64 * dw64).sum(1, keepdim=True))
+    spread = (w64 * (dw64.abs() + dw_tol)).sum(1, keepdim=True)
+    tol = w64 * (dw_tol + (w64 * dw_tol).sum(1, keepdim=True) + (K + 4) * U24 * (dw64.abs() + dw_tol + spread))
+    zero = torch.zeros((N, E), dtype=D, device="cuda")
+    _near(dl, zero.scatter(1, e, own), zero.scatter(1, e, tol), "d_logits")
