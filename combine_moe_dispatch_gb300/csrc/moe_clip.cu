@@ -8,10 +8,11 @@
 // their own addresses, and a persistent grid takes the chunks of up to
 // kClipBatch tensors in turn (the table of tensors travels in the kernel's
 // parameters, so nothing is copied or allocated).  The norm's kernel sums a
-// chunk's squares in binary32 per thread (64 or 128 elements) and everything
-// above that in binary64; each block leaves one partial sum, and the last
-// block to finish adds them in a fixed order, so that the norm does not
-// depend on the order in which blocks run.  The second kernel scales; it
+// chunk's squares in binary32 per thread (64 bf16 or 32 fp32 elements; in
+// binary64 where they leave binary32's range) and everything above that in
+// binary64; each block leaves one partial sum, and the last block to finish
+// adds them in a fixed order, so that the norm does not depend on the order
+// in which blocks run.  The second kernel scales; it
 // takes the chunks in the opposite order, so that it begins with what the
 // first one read last and the L2 (129 MB) still holds.  In place with a
 // coefficient of 1 it writes nothing.
@@ -109,8 +110,9 @@ __device__ __forceinline__ float squares(const uint4 &v, __nv_bfloat16) {
   return s;
 }
 
+// `zeros`: the thread's part holds nothing but +0 (told for whole chunks alone).
 template <typename T>
-__device__ __forceinline__ float chunk_squares(const ClipTensor &t, int64_t index) {
+__device__ __forceinline__ float chunk_squares(const ClipTensor &t, int64_t index, bool &zeros) {
   const Chunk<T> c(t, index);
   constexpr int U = kChunkGroups / kClipThreads;
   float s = 0.0f;
@@ -121,6 +123,12 @@ __device__ __forceinline__ float chunk_squares(const ClipTensor &t, int64_t inde
     for (int u = 0; u < U; ++u) v[u] = __ldg(in4 + u * kClipThreads);
 #pragma unroll
     for (int u = 0; u < U; ++u) s += squares(v[u], T());
+    if (s == 0.0f) {
+      uint32_t any = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) any |= v[u].x | v[u].y | v[u].z | v[u].w;
+      zeros = any == 0;
+    }
     return s;
   }
   for (int64_t g = c.g0 + threadIdx.x; g < c.g1; g += kClipThreads) {
@@ -134,6 +142,31 @@ __device__ __forceinline__ float chunk_squares(const ClipTensor &t, int64_t inde
     }
   }
   return s;
+}
+
+// The same in binary64, for a thread whose sum left the range in which binary32
+// squares are sums of normal numbers: values past 2^64 or so, or all below 2^-58.
+// Not the norm's usual path, so that it may read the chunk again (600 M values near
+// 1e-30: 2.2 ms, near 1 or all 0: 0.19).
+template <typename T>
+__device__ __noinline__ double chunk_squares_wide(const ClipTensor &t, int64_t index) {
+  const Chunk<T> c(t, index);
+  double s = 0.0;
+  for (int64_t g = c.g0 + threadIdx.x; g < c.g1; g += kClipThreads) {
+    for (int64_t i = max(g * c.VE, c.lead); i < min((g + 1) * c.VE, c.end); ++i) {
+      const double x = (double)to_float(c.base[i]);
+      s = fma(x, x, s);
+    }
+  }
+  return s;
+}
+
+template <typename T>
+__device__ __forceinline__ double chunk_sum(const ClipTensor &t, int64_t index) {
+  bool zeros = false;
+  const float s = chunk_squares<T>(t, index, zeros);
+  // 64 squares and sums that are subnormal lose 2^-150 each: 2^-34 of such a sum
+  return zeros || (s >= 0x1p-110f && s < INFINITY) ? (double)s : chunk_squares_wide<T>(t, index);
 }
 
 __device__ __forceinline__ double block_sum(double v, double *s_part) {
@@ -163,8 +196,7 @@ clip_norm_kernel(const __grid_constant__ ClipParams<BATCH> p) {
   for (int64_t c = blockIdx.x; c < p.chunks; c += gridDim.x) {
     const int i = tensor_of(p, c);
     const bool f32 = (p.f32[i >> 5] >> (i & 31)) & 1u;
-    sum += (double)(f32 ? chunk_squares<float>(p.t[i], c - p.first[i])
-                        : chunk_squares<__nv_bfloat16>(p.t[i], c - p.first[i]));
+    sum += f32 ? chunk_sum<float>(p.t[i], c - p.first[i]) : chunk_sum<__nv_bfloat16>(p.t[i], c - p.first[i]);
   }
   sum = block_sum(sum, s_part);
   if (threadIdx.x == 0) {

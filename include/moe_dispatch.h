@@ -447,9 +447,10 @@ typedef struct {
  *   total_norm = sqrt( sum over all tensors and elements of g^2 )
  *   out        = g * min(1, max_norm / (total_norm + 1e-6)), in g's type.
  * The pages describe serving only; this is the step between the backward pass
- * and the optimiser.  Squares are summed in binary32 over at most 128 elements
- * and in binary64 above, in an order that depends on the sizes, the addresses
- * modulo 16 and the device alone: the same inputs give the same bits.  A norm
+ * and the optimiser.  Squares are summed in binary32 over at most 64 elements
+ * (in binary64 where binary32 would overflow or lose them) and in binary64 above,
+ * in an order that depends on the sizes, the addresses modulo 16 and the
+ * device alone: the same inputs give the same bits.  A norm
  * that is NaN or infinite goes through the formula as it stands (NaN: every
  * output is NaN).  Where out is grad and nothing is clipped, nothing is
  * written.
