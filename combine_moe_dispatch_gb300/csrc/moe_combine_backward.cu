@@ -173,9 +173,16 @@ cudaError_t launch_variant(const CombineBackwardParams &p, cudaStream_t stream) 
 }
 
 // Rows of up to 2048 elements take one warp per token, longer ones the block's
-// 8 warps.  Measured: 2048 tokens, K = 2, H = 1024: one warp 4.5 us, eight 8.8;
-// 1024 tokens, K = 4, H = 2048: 8.7 and 10.7; 128 tokens, K = 8, H = 7168:
-// 31.6 and 9.1; 8192 tokens, K = 8, H = 7168: 327 and 311.
+// 8 warps.  Measured, one warp and eight, us:
+//   K  H      16 tokens   64          256         1024         8192
+//   2  256    2.5  2.5    2.5  2.5    2.7  2.7    3.0  4.8     7.3  28.4
+//   2  2048   4.2  2.5    4.3  2.6    4.4  2.8    6.6  6.6    29.3  39.2
+//   8  256    3.9  3.1    3.9  3.2    4.0  3.5    4.2  11.2   17.4  75.5
+//   8  1024   6.1  3.3    6.2  3.3    6.4  3.9    9.9  14.1   50.4  91.0
+//   8  2048   8.8  3.7    8.9  3.7    9.1  4.5   16.8  16.5   95.6  113.7
+//   8  7168   128 tokens: 31.6  9.1                          327   311
+// The rule is made for tokens that fill the SMs; up to a few hundred eight warps
+// would be faster at every H from 1024 on.
 template <int KG, int U, int MINB>
 cudaError_t launch_rows(const CombineBackwardParams &p, cudaStream_t stream) {
   if (p.H / 8 > 256) return launch_variant<KG, U, kBackWarps, MINB>(p, stream);

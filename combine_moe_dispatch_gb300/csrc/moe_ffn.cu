@@ -54,20 +54,29 @@
 // binary32; a, dh and the results are rounded to bf16 once each (the matrix
 // instructions take 16-bit operands; the kept h is never re-rounded).
 //
-// What bounds it, measured on GB300 (6.78 TB/s copy, 1.94 PFLOP/s bf16 for
-// seconds-long bursts, 1.71 sustained under the power limit):
+// What bounds it, measured on GB300 (copy 6.78 TB/s; bf16 products of the library
+// 1.94 PFLOP/s the best of ten, 1.71 for seconds, under the power limit):
 //  - Mixtral-shaped batch (8192 rows over 8 experts, H 4096, I 14336): forward
-//    1.78 ms (1.62 PFLOP/s), backward 3.78 ms (1.53).  The tensor pipe is
-//    active 92 to 94 % of the cycles (each product by itself; kActGrad 79 %, its
-//    epilogue reads h);
-//    the clock, 1.32 to 1.36 GHz at 1.37 kW, is what the power limit leaves.
+//    1.79 to 1.87 ms (1.54 to 1.61 PFLOP/s), backward 3.70 to 3.85 (1.50 to
+//    1.56).  At 2048 rows over 2 experts the tensor pipe is active 94 % of kRest's
+//    cycles, 80 % of kActGrad's (its epilogue reads h) and 85 % of the forward
+//    pass's (its ends, and the wait between a and y).  At 8192 rows the clock,
+//    1.32 to 1.36 GHz at 1.37 kW, is what the power limit leaves.
 //  - DeepSeek-V3-shaped decode (256 experts, 32 rows each, 22.5 GB of weights):
-//    3.33 ms, 6.85 TB/s: the weights' reading.  One token over two experts of
-//    the Mixtral shape: 112 to 115 us for 705 MB.
-//  - Weight gradients of experts with few rows: the writing.  64 experts of 128
-//    rows, 2.1 GB of dWgu: 5.1 TB/s (a plain fill of memory reaches 4.1).
+//    3.32 ms, 6.86 TB/s: the weights' reading.  One token over two experts of
+//    the Mixtral shape: 113 to 116 us for 705 MB.
+//  - Weight gradients of experts with few rows: not established.  64 experts of 128
+//    rows, 2.1 GB of dWgu, are written at 5 TB/s.  kRest of 31 experts with 5000
+//    rows (H 2048, I 1000) takes 147 us from cold caches, moves 0.70 GB to and from
+//    memory (4.8 TB/s) and keeps the tensor pipe active 33 % of the cycles: neither is
+//    at its limit.  Its tiles multiply for 2 to 3 blocks and then store 256 x 256
+//    values through one staging buffer per warp, which is the likely bound.
 //  - Tiny calls: latency, about 5 us a launch from the end of the one before:
 //    status and counts, the first copies, the products, the epilogue.
+//  - Few tiles: the last round.  Dense, H 7168, I 2048 (88 MB of weights, 13 us):
+//    1 row 30.1 us, 128 rows 34.1, 1024 rows 64.5 (46.6 of operations); y of 128
+//    rows is 28 tiles on 76 pairs, and no cut is priced below none.  dx alone is
+//    not cut: one token of two Mixtral-shaped experts 137 us for 705 MB.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <limits.h>
