@@ -24,6 +24,8 @@ PAYLOAD_FP8_E4M3 = 1
 PAYLOAD_FP8_E4M3_TSCALE = 2   # E4M3 bytes, scales [E, ceil(H/128), cap]
 # moe_dispatch_ex flag: x was final before the kernel preceding the dispatch began
 DISPATCH_EARLY_X = 1
+# moe_quant_mxfp4 flag: rows are a gate and an up projection (moe_ffn_mxfp4's weights)
+MXFP4_GATE_UP = 1
 
 
 class Status(enum.IntEnum):
@@ -76,6 +78,7 @@ def make_shape(R, T, H, E, K, cap, payload=PAYLOAD_BF16) -> Shape:
 LIB_PATH = _build.LIB
 # Entry points declared in include/moe_dispatch.h, with their C signatures.
 _P, _S, _U32, _U64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32, ctypes.c_uint64
+_I32 = ctypes.c_int32
 _SP = ctypes.POINTER(Shape)
 SIGNATURES = {
     "moe_workspace_size": ([_SP], _S),
@@ -99,6 +102,14 @@ SIGNATURES = {
     "moe_combine_backward": ([_SP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
     "moe_clip_workspace_size": ([], _S),
     "moe_clip_grad_norm": ([_P, ctypes.c_int32, ctypes.c_float, _P, _P, _S, _P], ctypes.c_int),
+    "moe_add_rms_norm": ([_SP, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P], ctypes.c_int),
+    "moe_norm_workspace_size": ([_SP], _S),
+    "moe_add_rms_norm_backward": ([_SP, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _S, _P],
+                                  ctypes.c_int),
+    "moe_mxfp4_scale_bytes": ([_I32, _I32, _I32], _S),
+    "moe_quant_mxfp4": ([_I32, _I32, _I32, _P, _P, _U32, _P, _P, _P, _P], ctypes.c_int),
+    "moe_dequant_mxfp4": ([_I32, _I32, _I32, _P, _P, _P, _U32, _P, _P, _P], ctypes.c_int),
+    "moe_dispatch_mxfp4": ([_SP, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
     "moe_plan_dispatch": ([_SP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P], ctypes.c_int),
 }
 
@@ -378,6 +389,61 @@ def clip_grad_norm(grads, outs, max_norm: float, total_norm, workspace, stream=N
                                            _ptr(total_norm), _ptr(workspace), workspace.nbytes,
                                            _stream(stream))
     return _check(st, "moe_clip_grad_norm", check)
+
+
+def add_rms_norm(shape: Shape, x, residual, gain, eps: float, sum_out, y, y_q=None, y_scale=None,
+                 stream=None, check=True) -> Status:
+    """moe_add_rms_norm; ``residual`` (and with it ``sum_out``) may be None,
+    ``y_q`` and ``y_scale`` belong to the fp8 payloads, for which ``y`` may be
+    None."""
+    st = load_library().moe_add_rms_norm(ctypes.byref(shape), _ptr(x), _ptr(residual), _ptr(gain), eps,
+                                         _ptr(sum_out), _ptr(y), _ptr(y_q), _ptr(y_scale),
+                                         _stream(stream))
+    return _check(st, "moe_add_rms_norm", check)
+
+
+def norm_workspace_size(shape: Shape) -> int:
+    return load_library().moe_norm_workspace_size(ctypes.byref(shape))
+
+
+def add_rms_norm_backward(shape: Shape, d_y, d_sum, sum_in, gain, eps: float, d_x, d_gain, workspace,
+                          stream=None, check=True) -> Status:
+    """moe_add_rms_norm_backward; ``d_sum`` may be None."""
+    st = load_library().moe_add_rms_norm_backward(ctypes.byref(shape), _ptr(d_y), _ptr(d_sum),
+                                                  _ptr(sum_in), _ptr(gain), eps, _ptr(d_x),
+                                                  _ptr(d_gain), _ptr(workspace),
+                                                  workspace.numel() * workspace.element_size(),
+                                                  _stream(stream))
+    return _check(st, "moe_add_rms_norm_backward", check)
+
+
+def mxfp4_scale_bytes(num_experts: int, rows: int, cols: int) -> int:
+    return load_library().moe_mxfp4_scale_bytes(num_experts, rows, cols)
+
+
+def quant_mxfp4(src, expert_num_tokens, q, scale, flags: int = 0, workspace=None, stream=None,
+                check=True) -> Status:
+    """moe_quant_mxfp4 of ``src`` [E, rows, cols]; ``expert_num_tokens`` (every
+    row exists) and ``workspace`` (no plan behind the counts) may be None."""
+    st = load_library().moe_quant_mxfp4(*src.shape, _ptr(src), _ptr(expert_num_tokens), flags, _ptr(q),
+                                        _ptr(scale), _ptr(workspace), _stream(stream))
+    return _check(st, "moe_quant_mxfp4", check)
+
+
+def dequant_mxfp4(q, scale, expert_num_tokens, out, flags: int = 0, workspace=None, stream=None,
+                  check=True) -> Status:
+    """moe_dequant_mxfp4 into ``out`` [E, rows, cols]; the rest as quant_mxfp4."""
+    st = load_library().moe_dequant_mxfp4(*out.shape, _ptr(q), _ptr(scale), _ptr(expert_num_tokens),
+                                          flags, _ptr(out), _ptr(workspace), _stream(stream))
+    return _check(st, "moe_dequant_mxfp4", check)
+
+
+def dispatch_mxfp4(shape: Shape, x, topk_idx, slot_of, expert_x, expert_x_scale, workspace,
+                   stream=None, check=True) -> Status:
+    st = load_library().moe_dispatch_mxfp4(ctypes.byref(shape), _ptr(x), _ptr(topk_idx), _ptr(slot_of),
+                                           _ptr(expert_x), _ptr(expert_x_scale), _ptr(workspace),
+                                           _stream(stream))
+    return _check(st, "moe_dispatch_mxfp4", check)
 
 
 def read_status(workspace, stream=None) -> Status:

@@ -8,6 +8,8 @@
 
 #include "moe_common.cuh"
 #include "moe_ffn.cuh"
+#include "moe_mxfp4.cuh"
+#include "moe_norm.cuh"
 #include "moe_train.cuh"
 
 namespace moe {
@@ -516,6 +518,156 @@ moe_status moe_clip_grad_norm(const moe_grad_tensor *tensors, int32_t num_tensor
   if (misaligned || !aligned(workspace, 16)) return MOE_ERR_ALIGNMENT;
   return from_cuda(launch_clip(tensors, num_tensors, max_norm, total_norm, workspace,
                                (cudaStream_t)stream));
+}
+
+moe_status moe_add_rms_norm(const moe_shape *shape, const void *x, const void *residual,
+                            const void *gain, float eps, void *sum, void *y, void *y_q,
+                            float *y_scale, void *stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if (!(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+  if (shape->tokens_per_rank == 0) return MOE_OK;   // empty batch: nothing to read or write
+  const bool fp8 = shape->payload != MOE_PAYLOAD_BF16;
+  if (!x || !gain || (fp8 ? !y_q || !y_scale : !y) || (sum && (!residual || sum == y)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gain, 16) || !aligned(sum, 16) ||
+      !aligned(y, 16) || (fp8 && (!aligned(y_q, 16) || !aligned(y_scale, 4))))
+    return MOE_ERR_ALIGNMENT;
+  NormParams p;
+  p.x = static_cast<const uint16_t *>(x);
+  p.residual = static_cast<const uint16_t *>(residual);
+  p.gain = static_cast<const uint16_t *>(gain);
+  p.sum = static_cast<uint16_t *>(sum);
+  p.y = static_cast<uint16_t *>(y);
+  p.y_q = fp8 ? static_cast<uint8_t *>(y_q) : nullptr;
+  p.y_scale = fp8 ? y_scale : nullptr;
+  p.eps = eps;
+  p.N = shape->num_ranks * shape->tokens_per_rank;
+  p.H = shape->hidden;
+  p.scale_t = shape->payload == MOE_PAYLOAD_FP8_E4M3_TSCALE;
+  return from_cuda(launch_norm(p, (cudaStream_t)stream));
+}
+
+size_t moe_norm_workspace_size(const moe_shape *shape) {
+  if (check_shape(shape) != MOE_OK) return 0;
+  const int64_t N = (int64_t)shape->num_ranks * shape->tokens_per_rank;
+  const int64_t parts = N < 1 ? 1 : N < kNormMaxBlocks ? N : kNormMaxBlocks;
+  return (size_t)parts * shape->hidden * sizeof(float);
+}
+
+moe_status moe_add_rms_norm_backward(const moe_shape *shape, const void *d_y, const void *d_sum,
+                                     const void *sum, const void *gain, float eps, void *d_x,
+                                     float *d_gain, void *workspace, size_t workspace_bytes,
+                                     void *stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if (shape->payload != MOE_PAYLOAD_BF16) return MOE_ERR_UNSUPPORTED;
+  const bool empty = shape->tokens_per_rank == 0;
+  if (!(eps >= 0.0f) || !d_gain || (!empty && (!d_y || !sum || !gain || !d_x)))
+    return MOE_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < moe_norm_workspace_size(shape)) return MOE_ERR_WORKSPACE;
+  if (!aligned(d_y, 16) || !aligned(d_sum, 16) || !aligned(sum, 16) || !aligned(gain, 16) ||
+      !aligned(d_x, 16) || !aligned(d_gain, 4) || !aligned(workspace, 16))
+    return MOE_ERR_ALIGNMENT;
+  NormBackwardParams p;
+  p.d_y = static_cast<const uint16_t *>(d_y);
+  p.d_sum = static_cast<const uint16_t *>(d_sum);
+  p.sum = static_cast<const uint16_t *>(sum);
+  p.gain = static_cast<const uint16_t *>(gain);
+  p.d_x = static_cast<uint16_t *>(d_x);
+  p.part = static_cast<float *>(workspace);
+  p.eps = eps;
+  p.N = shape->num_ranks * shape->tokens_per_rank;
+  p.H = shape->hidden;
+  return from_cuda(launch_norm_backward(p, d_gain, (cudaStream_t)stream));
+}
+
+size_t moe_mxfp4_scale_bytes(int32_t num_experts, int32_t rows, int32_t cols) {
+  if (num_experts <= 0 || rows <= 0 || cols <= 0 || cols % 32 != 0) return 0;
+  return scale_bytes(num_experts, rows, cols);
+}
+
+static Mxfp4Rows mxfp4_rows(const void *q, const void *scale, int32_t rows, int32_t cols, bool gate_up) {
+  Mxfp4Rows m;
+  m.q = static_cast<uint8_t *>(const_cast<void *>(q));
+  m.scale = static_cast<uint8_t *>(const_cast<void *>(scale));
+  m.rows = rows;
+  m.cols = cols;
+  m.row_tiles = scale_layout(rows, cols).row_tiles;
+  m.block_tiles = scale_layout(rows, cols).block_tiles;
+  m.gate = gate_up ? rows / 2 : 0;
+  return m;
+}
+
+// Checks that moe_quant_mxfp4 and moe_dequant_mxfp4 share.
+static moe_status mxfp4_check(int32_t E, int32_t rows, int32_t cols, const void *wide, const void *q,
+                              const void *scale, const int32_t *counts, uint32_t flags,
+                              const void *workspace) {
+  if (E <= 0 || rows <= 0 || cols <= 0 || (flags & ~(uint32_t)MOE_MXFP4_GATE_UP) != 0u ||
+      (flags != 0u && (counts || rows % 2 != 0)))
+    return MOE_ERR_INVALID_ARG;
+  const int64_t all = (int64_t)E * rows;
+  if (cols % 32 != 0 || all >= ((int64_t)1 << 31) || all >= ((int64_t)1 << 46) / cols)
+    return MOE_ERR_UNSUPPORTED;
+  if (!wide || !q || !scale) return MOE_ERR_INVALID_ARG;
+  if (!aligned(wide, 16) || !aligned(q, 16) || !aligned(scale, 16) || !aligned(counts, 4) ||
+      !aligned(workspace, 16))
+    return MOE_ERR_ALIGNMENT;
+  return MOE_OK;
+}
+
+moe_status moe_quant_mxfp4(int32_t num_experts, int32_t rows, int32_t cols, const void *src,
+                           const int32_t *expert_num_tokens, uint32_t flags, void *q, void *scale,
+                           void *workspace, void *stream) {
+  const moe_status st =
+      mxfp4_check(num_experts, rows, cols, src, q, scale, expert_num_tokens, flags, workspace);
+  if (st != MOE_OK) return st;
+  QuantParams p;
+  p.src = static_cast<const uint16_t *>(src);
+  p.counts = expert_num_tokens;
+  p.hdr = header(workspace);
+  p.out = mxfp4_rows(q, scale, rows, cols, flags != 0u);
+  p.E = num_experts;
+  return from_cuda(launch_quant_mxfp4(p, (cudaStream_t)stream));
+}
+
+moe_status moe_dequant_mxfp4(int32_t num_experts, int32_t rows, int32_t cols, const void *q,
+                             const void *scale, const int32_t *expert_num_tokens, uint32_t flags,
+                             void *out, void *workspace, void *stream) {
+  const moe_status st =
+      mxfp4_check(num_experts, rows, cols, out, q, scale, expert_num_tokens, flags, workspace);
+  if (st != MOE_OK) return st;
+  DequantParams p;
+  p.in = mxfp4_rows(q, scale, rows, cols, flags != 0u);
+  p.counts = expert_num_tokens;
+  p.hdr = header(workspace);
+  p.out = static_cast<uint16_t *>(out);
+  p.E = num_experts;
+  return from_cuda(launch_dequant_mxfp4(p, (cudaStream_t)stream));
+}
+
+moe_status moe_dispatch_mxfp4(const moe_shape *shape, const void *x, const int32_t *topk_idx,
+                              const int32_t *slot_of, void *expert_x, void *expert_x_scale,
+                              void *workspace, void *stream) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if (shape->payload != MOE_PAYLOAD_BF16 || shape->hidden % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  if (shape->tokens_per_rank == 0) return MOE_OK;   // empty batch: nothing to read or write
+  if (!x || !topk_idx || !slot_of || !expert_x || !expert_x_scale) return MOE_ERR_INVALID_ARG;
+  if (!workspace) return MOE_ERR_WORKSPACE;
+  if (!aligned(x, 16) || !aligned(expert_x, 16) || !aligned(expert_x_scale, 16) ||
+      !aligned(topk_idx, 4) || !aligned(slot_of, 4) || !aligned(workspace, 16))
+    return MOE_ERR_ALIGNMENT;
+  DispatchMxfp4Params p;
+  p.x = static_cast<const uint16_t *>(x);
+  p.topk_idx = topk_idx;
+  p.slot_of = slot_of;
+  p.hdr = header(workspace);
+  p.out = mxfp4_rows(expert_x, expert_x_scale, shape->capacity, shape->hidden, false);
+  p.N = shape->num_ranks * shape->tokens_per_rank;
+  p.E = shape->num_experts;
+  p.K = shape->top_k;
+  return from_cuda(launch_dispatch_mxfp4(p, (cudaStream_t)stream));
 }
 
 moe_status moe_read_status(const void *workspace, void *stream, moe_status *out) {

@@ -1,0 +1,476 @@
+// moe_norm.cu -- root-mean-square norm of the hidden states, with the
+// residual's addition and an output in 8 bits, and its backward pass.
+//
+// What it computes, for each row of H elements:
+//   s = bf16(x + residual)                    (s = x without a residual)
+//   y = s rstd gain,  rstd = 1 / sqrt(mean(s^2) + eps)
+// y rounded to bf16 and, from the same unrounded values, to E4M3 with one scale
+// per 128 elements (amax/448, the rule of the fp8 dispatch); and
+//   u = s rstd,  g = dy gain
+//   d_x = rstd (g - u mean(g u)) + d_sum,     d_gain = sum over rows of dy u
+// from dy, the gradient d_sum that arrives at s by the residual stream, and s.
+// The norm is that of the rounded s, which is what the backward pass reads:
+// what is differentiated is what was computed.  Sums are binary32.
+//
+// How: one pass over the data.  WPR warps share a row, each lane has C chunks of
+// 16 bytes of it in registers between the sum of squares and the result, so that
+// every byte is read and written once.  A block of 8 warps takes 8 / WPR rows
+// at a time from a grid that fills the SMs; the gain stays in registers.  Backward,
+// a lane's columns are the same for all of its rows: their share of d_gain is
+// summed in registers, joined over the block's warps in shared memory, stored
+// once per block, and a second launch adds the blocks' shares, all in an order
+// that depends on the sizes alone.  Rows of more than 8192 elements do not fit
+// the registers: a block then reads its row twice (the second time from the
+// caches).
+#include <cuda_bf16.h>
+
+#include "moe_norm.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kNormThreads = 256;
+constexpr int kNormWarps = kNormThreads / 32;
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kNormMaxRow = kNormThreads * 4 * 8;   // elements of a row held in registers, at most
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_lo(w[i]);
+    f[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                    pack_bf16(f[6], f[7]));
+}
+__device__ __forceinline__ uint4 add8(const uint4 &a, const uint4 &b) {
+  float x[8], r[8];
+  unpack8(a, x);
+  unpack8(b, r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] += r[i];
+  return pack8(x);
+}
+__device__ __forceinline__ uint4 load16(const uint16_t *p, int64_t chunk) {
+  return __ldcs(reinterpret_cast<const uint4 *>(p) + chunk);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+  return v;
+}
+// The sum over a row's WPR warps, in the order of the warps.  `s` is used again
+// two calls later: the barrier of the call between keeps the reads before it.
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float *s, int warp) {
+  v = warp_sum(v);
+  if (WPR == 1) return v;
+  if ((threadIdx.x & 31) == 0) s[warp] = v;
+  __syncthreads();
+  float t = 0.0f;
+#pragma unroll
+  for (int i = 0; i < WPR; ++i) t += s[warp / WPR * WPR + i];
+  return t;
+}
+
+// A half-warp's 128 values -> E4M3 bytes and their scale.  All 32 lanes call it.
+__device__ __forceinline__ void store_fp8(const NormParams &p, int64_t row, int chunk, bool in, int nb,
+                                          const float (&f)[8]) {
+  const float amax = half_warp_amax(f);
+  const bool fast = amax >= 0x1p-120f && amax <= 3.4028234e38f;
+  const float scale[1] = {fast ? div448_fast(amax) : __fdiv_rn(amax, 448.0f)};
+  const bool zero[1] = {amax == 0.0f};
+  const float r[1] = {zero[0] ? 1.0f : __frcp_rn(scale[0])};
+  const float v[1][8] = {{f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]}};
+  uint2 q[1];
+  quantise_blocks<1>(v, scale, r, zero, q);
+  if (!in) return;
+  *reinterpret_cast<uint2 *>(p.y_q + row * p.H + (int64_t)chunk * 8) = q[0];
+  if ((chunk & 15) == 0) {
+    const int blk = chunk >> 4;
+    p.y_scale[p.scale_t ? (int64_t)blk * p.N + row : row * nb + blk] = scale[0];
+  }
+}
+
+template <int C, int WPR, bool RES, bool FP8>
+__global__ void __launch_bounds__(kNormThreads)
+norm_kernel(NormParams p) {
+  constexpr int kRows = kNormWarps / WPR;
+  __shared__ float s_sum[2][kNormWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c0 = (warp % WPR) * 32 + lane, cpr = p.H / 8, nb = (p.H + 127) / 128;
+  pdl_wait_for_previous();
+  uint4 gain[C];
+#pragma unroll
+  for (int u = 0; u < C; ++u) {
+    const int c = c0 + u * WPR * 32;
+    gain[u] = c < cpr ? __ldg(reinterpret_cast<const uint4 *>(p.gain) + c) : make_uint4(0, 0, 0, 0);
+  }
+  int buf = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < p.N; row0 += (int64_t)gridDim.x * kRows) {
+    const int64_t row = row0 + warp / WPR;
+    uint4 s[C];
+    if (RES) {
+      uint4 r[C];
+#pragma unroll
+      for (int u = 0; u < C; ++u) {
+        const int c = c0 + u * WPR * 32;
+        const bool in = row < p.N && c < cpr;
+        s[u] = in ? load16(p.x, row * cpr + c) : make_uint4(0, 0, 0, 0);
+        r[u] = in ? load16(p.residual, row * cpr + c) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < C; ++u) {
+        const int c = c0 + u * WPR * 32;
+        s[u] = add8(s[u], r[u]);
+        if (p.sum && row < p.N && c < cpr) reinterpret_cast<uint4 *>(p.sum)[row * cpr + c] = s[u];
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < C; ++u) {
+        const int c = c0 + u * WPR * 32;
+        s[u] = row < p.N && c < cpr ? load16(p.x, row * cpr + c) : make_uint4(0, 0, 0, 0);
+      }
+    }
+    float sq = 0.0f;
+#pragma unroll
+    for (int u = 0; u < C; ++u) {
+      float f[8];
+      unpack8(s[u], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sq = fmaf(f[i], f[i], sq);
+    }
+    const float rstd = rsqrtf(row_sum<WPR>(sq, s_sum[buf], warp) / (float)p.H + p.eps);
+    buf ^= 1;
+#pragma unroll
+    for (int u = 0; u < C; ++u) {
+      const int c = c0 + u * WPR * 32;
+      const bool in = row < p.N && c < cpr;
+      float f[8], g[8];
+      unpack8(s[u], f);
+      unpack8(gain[u], g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * g[i];
+      if ((!FP8 || p.y) && in) reinterpret_cast<uint4 *>(p.y)[row * cpr + c] = pack8(f);
+      if (FP8) store_fp8(p, row, c, in, nb, f);
+    }
+  }
+}
+
+// Rows of any length: a block reads its row twice.
+template <bool RES, bool FP8>
+__global__ void __launch_bounds__(kNormThreads)
+norm_long_kernel(NormParams p) {
+  __shared__ float s_sum[2][kNormWarps];
+  const int warp = threadIdx.x >> 5;
+  const int cpr = p.H / 8, nb = (p.H + 127) / 128;
+  pdl_wait_for_previous();
+  int buf = 0;
+  for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x) {
+    const auto read = [&](int c) {
+      uint4 s = reinterpret_cast<const uint4 *>(p.x)[row * cpr + c];
+      if (RES) s = add8(s, reinterpret_cast<const uint4 *>(p.residual)[row * cpr + c]);
+      return s;
+    };
+    float sq = 0.0f;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < cpr; c += kNormThreads) {
+      float f[8];
+      unpack8(read(c), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sq = fmaf(f[i], f[i], sq);
+    }
+    const float rstd = rsqrtf(row_sum<kNormWarps>(sq, s_sum[buf], warp) / (float)p.H + p.eps);
+    buf ^= 1;
+    for (int cb = 0; cb < cpr; cb += kNormThreads) {      // all lanes, for the half-warps' maxima
+      const int c = cb + threadIdx.x;
+      const bool in = c < cpr;
+      float f[8], g[8];
+      const uint4 s = in ? read(c) : make_uint4(0, 0, 0, 0);
+      unpack8(s, f);
+      unpack8(in ? __ldg(reinterpret_cast<const uint4 *>(p.gain) + c) : make_uint4(0, 0, 0, 0), g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * g[i];
+      if (RES && p.sum && in) reinterpret_cast<uint4 *>(p.sum)[row * cpr + c] = s;
+      if ((!FP8 || p.y) && in) reinterpret_cast<uint4 *>(p.y)[row * cpr + c] = pack8(f);
+      if (FP8) store_fp8(p, row, c, in, nb, f);
+    }
+  }
+}
+
+template <int C, int WPR, bool DSUM>
+__global__ void __launch_bounds__(kNormThreads)
+norm_backward_kernel(NormBackwardParams p) {
+  constexpr int kRows = kNormWarps / WPR;
+  __shared__ float s_sum[2][2][kNormWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c0 = (warp % WPR) * 32 + lane, cpr = p.H / 8;
+  pdl_wait_for_previous();
+  uint4 gain[C];
+  float acc[C][8];
+#pragma unroll
+  for (int u = 0; u < C; ++u) {
+    const int c = c0 + u * WPR * 32;
+    gain[u] = c < cpr ? __ldg(reinterpret_cast<const uint4 *>(p.gain) + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[u][i] = 0.0f;
+  }
+  int buf = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < p.N; row0 += (int64_t)gridDim.x * kRows) {
+    const int64_t row = row0 + warp / WPR;
+    uint4 s[C], dy[C], ds[C];
+#pragma unroll
+    for (int u = 0; u < C; ++u) {
+      const int c = c0 + u * WPR * 32;
+      const bool in = row < p.N && c < cpr;
+      s[u] = in ? load16(p.sum, row * cpr + c) : make_uint4(0, 0, 0, 0);
+      dy[u] = in ? load16(p.d_y, row * cpr + c) : make_uint4(0, 0, 0, 0);
+      if (DSUM) ds[u] = in ? load16(p.d_sum, row * cpr + c) : make_uint4(0, 0, 0, 0);
+    }
+    float sq = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int u = 0; u < C; ++u) {
+      float f[8], d[8], g[8];
+      unpack8(s[u], f);
+      unpack8(dy[u], d);
+      unpack8(gain[u], g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sq = fmaf(f[i], f[i], sq);
+        dot = fmaf(d[i] * g[i], f[i], dot);
+      }
+    }
+    // both sums behind one barrier
+    sq = warp_sum(sq);
+    dot = warp_sum(dot);
+    if (WPR > 1) {
+      if (lane == 0) {
+        s_sum[buf][0][warp] = sq;
+        s_sum[buf][1][warp] = dot;
+      }
+      __syncthreads();
+      sq = dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < WPR; ++i) {
+        sq += s_sum[buf][0][warp / WPR * WPR + i];
+        dot += s_sum[buf][1][warp / WPR * WPR + i];
+      }
+      buf ^= 1;
+    }
+    const float rstd = rsqrtf(sq / (float)p.H + p.eps);
+    const float mean = dot * rstd / (float)p.H;             // of g u
+#pragma unroll
+    for (int u = 0; u < C; ++u) {
+      const int c = c0 + u * WPR * 32;
+      float f[8], d[8], g[8], e[8];
+      unpack8(s[u], f);
+      unpack8(dy[u], d);
+      unpack8(gain[u], g);
+      if (DSUM) unpack8(ds[u], e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float un = f[i] * rstd;
+        if (row < p.N) acc[u][i] = fmaf(d[i], un, acc[u][i]);
+        f[i] = rstd * (d[i] * g[i] - un * mean);
+        if (DSUM) f[i] += e[i];
+      }
+      if (row < p.N && c < cpr) reinterpret_cast<uint4 *>(p.d_x)[row * cpr + c] = pack8(f);
+    }
+  }
+  // the block's share of d_gain: its row groups' in their order
+  if (kRows > 1) {
+    __shared__ float s_acc[kRows > 1 ? kRows - 1 : 1][WPR * 32 * C * 8];
+    const int group = warp / WPR, at = c0 * 8;
+    if (group > 0)
+#pragma unroll
+      for (int u = 0; u < C; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s_acc[group - 1][u * WPR * 256 + at + i] = acc[u][i];
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int k = 0; k < kRows - 1; ++k)
+#pragma unroll
+      for (int u = 0; u < C; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[u][i] += s_acc[k][u * WPR * 256 + at + i];
+  }
+#pragma unroll
+  for (int u = 0; u < C; ++u) {
+    const int c = c0 + u * WPR * 32;
+    if (c < cpr) {
+      float4 *q = reinterpret_cast<float4 *>(p.part + (int64_t)blockIdx.x * p.H) + 2 * c;
+      q[0] = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
+      q[1] = make_float4(acc[u][4], acc[u][5], acc[u][6], acc[u][7]);
+    }
+  }
+}
+
+// Rows of any length: a block reads its row twice and keeps its share of
+// d_gain in the workspace.
+template <bool DSUM>
+__global__ void __launch_bounds__(kNormThreads)
+norm_backward_long_kernel(NormBackwardParams p) {
+  __shared__ float s_sum[2][2][kNormWarps];
+  const int warp = threadIdx.x >> 5, cpr = p.H / 8;
+  float4 *part = reinterpret_cast<float4 *>(p.part + (int64_t)blockIdx.x * p.H);
+  pdl_wait_for_previous();
+  int buf = 0;
+  for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x) {
+    const uint4 *s = reinterpret_cast<const uint4 *>(p.sum) + row * cpr;
+    const uint4 *dy = reinterpret_cast<const uint4 *>(p.d_y) + row * cpr;
+    const uint4 *gain = reinterpret_cast<const uint4 *>(p.gain);
+    float sq = 0.0f, dot = 0.0f;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < cpr; c += kNormThreads) {
+      float f[8], d[8], g[8];
+      unpack8(s[c], f);
+      unpack8(dy[c], d);
+      unpack8(__ldg(gain + c), g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sq = fmaf(f[i], f[i], sq);
+        dot = fmaf(d[i] * g[i], f[i], dot);
+      }
+    }
+    sq = row_sum<kNormWarps>(sq, s_sum[buf][0], warp);
+    dot = row_sum<kNormWarps>(dot, s_sum[buf][1], warp);
+    buf ^= 1;
+    const float rstd = rsqrtf(sq / (float)p.H + p.eps);
+    const float mean = dot * rstd / (float)p.H;
+    for (int c = threadIdx.x; c < cpr; c += kNormThreads) {
+      float f[8], d[8], g[8], e[8];
+      unpack8(s[c], f);
+      unpack8(dy[c], d);
+      unpack8(__ldg(gain + c), g);
+      if (DSUM) unpack8(reinterpret_cast<const uint4 *>(p.d_sum)[row * cpr + c], e);
+      float4 a[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
+      if (row != (int64_t)blockIdx.x) {
+        a[0] = part[2 * c];
+        a[1] = part[2 * c + 1];
+      }
+      float *acc = reinterpret_cast<float *>(a);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float un = f[i] * rstd;
+        acc[i] = fmaf(d[i], un, acc[i]);
+        f[i] = rstd * (d[i] * g[i] - un * mean);
+        if (DSUM) f[i] += e[i];
+      }
+      part[2 * c] = a[0];
+      part[2 * c + 1] = a[1];
+      reinterpret_cast<uint4 *>(p.d_x)[row * cpr + c] = pack8(f);
+    }
+  }
+}
+
+struct GainParams {
+  const float *part;           // [parts][H]
+  float *d_gain;               // [H]
+  int parts, H;
+};
+constexpr int kGainThreads = 512;
+
+// 32 columns a block: each warp adds every 16th block's share, then the warps'
+// sums are added in their order.
+__global__ void __launch_bounds__(kGainThreads)
+norm_gain_kernel(GainParams p) {
+  constexpr int kWarps = kGainThreads / 32;
+  __shared__ float s[kWarps][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = blockIdx.x * 32 + lane;
+  pdl_wait_for_previous();
+  float v = 0.0f;
+  if (col < p.H) {
+#pragma unroll 8
+    for (int i = warp; i < p.parts; i += kWarps) v += __ldg(p.part + (int64_t)i * p.H + col);
+  }
+  s[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && col < p.H) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) t += s[i][lane];
+    p.d_gain[col] = t;
+  }
+}
+
+template <int C, int WPR, bool RES, bool FP8>
+cudaError_t launch_rows(const NormParams &p, cudaStream_t stream) {
+  const auto kern = norm_kernel<C, WPR, RES, FP8>;
+  return launch_after_previous(kern, persistent_grid((const void *)kern, kNormThreads, (int64_t)p.N * WPR),
+                               kNormThreads, p, stream);
+}
+
+template <bool RES, bool FP8>
+cudaError_t launch_width(const NormParams &p, cudaStream_t stream) {
+  const int cpr = p.H / 8;
+  if (cpr <= 32) return launch_rows<1, 1, RES, FP8>(p, stream);
+  if (cpr <= 64) return launch_rows<2, 1, RES, FP8>(p, stream);
+  if (cpr <= 128) return launch_rows<4, 1, RES, FP8>(p, stream);
+  if (cpr <= 256) return launch_rows<4, 2, RES, FP8>(p, stream);
+  if (cpr <= 512) return launch_rows<4, 4, RES, FP8>(p, stream);
+  if (p.H <= kNormMaxRow) return launch_rows<4, 8, RES, FP8>(p, stream);
+  const auto kern = norm_long_kernel<RES, FP8>;
+  return launch_after_previous(
+      kern, persistent_grid((const void *)kern, kNormThreads, (int64_t)p.N * kNormWarps), kNormThreads, p,
+      stream);
+}
+
+int backward_blocks(const void *kern, int64_t warps) {
+  const int g = persistent_grid(kern, kNormThreads, warps);
+  return g < kNormMaxBlocks ? g : kNormMaxBlocks;
+}
+
+template <int C, int WPR, bool DSUM>
+cudaError_t launch_backward_rows(const NormBackwardParams &p, int &parts, cudaStream_t stream) {
+  const auto kern = norm_backward_kernel<C, WPR, DSUM>;
+  parts = backward_blocks((const void *)kern, (int64_t)p.N * WPR);
+  return launch_after_previous(kern, parts, kNormThreads, p, stream);
+}
+
+template <bool DSUM>
+cudaError_t launch_backward_width(const NormBackwardParams &p, int &parts, cudaStream_t stream) {
+  const int cpr = p.H / 8;
+  if (cpr <= 32) return launch_backward_rows<1, 1, DSUM>(p, parts, stream);
+  if (cpr <= 64) return launch_backward_rows<2, 1, DSUM>(p, parts, stream);
+  if (cpr <= 128) return launch_backward_rows<4, 1, DSUM>(p, parts, stream);
+  if (cpr <= 256) return launch_backward_rows<4, 2, DSUM>(p, parts, stream);
+  if (cpr <= 512) return launch_backward_rows<4, 4, DSUM>(p, parts, stream);
+  if (p.H <= kNormMaxRow) return launch_backward_rows<4, 8, DSUM>(p, parts, stream);
+  const auto kern = norm_backward_long_kernel<DSUM>;
+  parts = backward_blocks((const void *)kern, (int64_t)p.N * kNormWarps);
+  return launch_after_previous(kern, parts, kNormThreads, p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_norm(const NormParams &p, cudaStream_t stream) {
+  if (p.y_q) return p.residual ? launch_width<true, true>(p, stream) : launch_width<false, true>(p, stream);
+  return p.residual ? launch_width<true, false>(p, stream) : launch_width<false, false>(p, stream);
+}
+
+cudaError_t launch_norm_backward(const NormBackwardParams &p, float *d_gain, cudaStream_t stream) {
+  GainParams g;
+  g.part = p.part;
+  g.d_gain = d_gain;
+  g.H = p.H;
+  g.parts = 0;
+  if (p.N > 0) {
+    const cudaError_t e = p.d_sum ? launch_backward_width<true>(p, g.parts, stream)
+                                  : launch_backward_width<false>(p, g.parts, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_after_previous(norm_gain_kernel, (p.H + 31) / 32, kGainThreads, g, stream);
+}
+
+}  // namespace moe

@@ -467,6 +467,113 @@ moe_status moe_clip_grad_norm(const moe_grad_tensor *tensors, int32_t num_tensor
                               float *total_norm, void *workspace, size_t workspace_bytes,
                               void *stream);
 
+/* Root-mean-square norm of the hidden states, with the residual's addition
+ * before it and an output in 8 bits:
+ *   s = bf16( x + residual )            (s = x without a residual)
+ *   y = s * gain / sqrt( mean over the row of s^2 + eps )
+ * for the N rows of H elements.  It makes the rows that the router, moe_dispatch
+ * and the shared expert read.  Sums are binary32; s is rounded before the norm,
+ * so that moe_add_rms_norm_backward, which reads s, differentiates what was
+ * computed; y is rounded once, to bf16, and from the same unrounded values to
+ * E4M3 by the rule of moe_dispatch ("Lower latency and higher throughput with
+ * multi-node DeepSeek deployment", Quantization: scale = amax / 448 per 128
+ * elements, all-zero block: scale 0 and q = 0).
+ * In:   x [N, H] bf16; residual [N, H] bf16, or NULL; gain [H] bf16; eps >= 0.
+ * Out:  sum [N, H] bf16, receives s: NULL without a residual, or when it is not
+ *       wanted; may be x or residual itself (in place).
+ *       y [N, H] bf16; may be x or residual, unless that is also sum.  NULL when
+ *       it is not wanted: payload FP8 only.
+ *       y_q [N, H] E4M3 and y_scale [N, nb] fp32 ([nb, N] for FP8_E4M3_TSCALE),
+ *       nb = ceil(H / 128): payload FP8 only, not touched for BF16.
+ * Uses N, H and the payload of `shape`.  A row whose squares overflow binary32
+ * (elements beyond 1.8e19) comes out 0.  The bf16 arrays and y_q are 16-byte
+ * aligned, y_scale 4-byte.
+ * Errors: INVALID_ARG (null pointer, eps negative or NaN, sum without a
+ *       residual, sum = y), UNSUPPORTED, ALIGNMENT, CUDA.  No workspace. */
+moe_status moe_add_rms_norm(const moe_shape *shape, const void *x, const void *residual,
+                            const void *gain, float eps, void *sum, void *y, void *y_q,
+                            float *y_scale, void *stream);
+
+/* Backward pass of moe_add_rms_norm.  With rstd = 1 / sqrt(mean(s^2) + eps),
+ * u = s * rstd and g = d_y * gain, for each row:
+ *   d_x = rstd * ( g - u * mean(g * u) ) + d_sum
+ *   d_gain = sum over the rows of d_y * u
+ * d_x is the gradient of x and of the residual alike.  Sums are binary32, in an
+ * order that depends on the sizes and the device alone.  The 8-bit output has no
+ * gradient of its own.
+ * In:   d_y [N, H] bf16; d_sum [N, H] bf16, the gradient that arrives at s
+ *       along the residual stream, or NULL; sum [N, H] bf16, the s of the
+ *       forward call (x, if that had no residual); gain [H] bf16; eps.
+ * Out:  d_x [N, H] bf16, may be d_y or d_sum (in place); d_gain [H] fp32, every
+ *       element written (0 for an empty batch).
+ * Work: moe_norm_workspace_size(shape) bytes, 16-byte aligned, of any content.
+ * Two launches.  Uses N and H of `shape`; payload BF16 (UNSUPPORTED otherwise).
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA. */
+size_t moe_norm_workspace_size(const moe_shape *shape);
+moe_status moe_add_rms_norm_backward(const moe_shape *shape, const void *d_y, const void *d_sum,
+                                     const void *sum, const void *gain, float eps, void *d_x,
+                                     float *d_gain, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+
+/* MXFP4 (OCP Microscaling Formats 1.0): 4-bit floating point in blocks of 32
+ * elements of a row with one scale.  For a block of x:
+ *   X = 2^( floor(log2 amax) - 2 ), not below 2^-127,
+ *   q = e2m1( x / X ): the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ *       negatives, ties to the even one, beyond 6 to 6.
+ * A block that holds an infinity or a NaN gets the scale NaN (and q = 0): it
+ * reads back as NaN.  An array of `rows` x `cols` elements for each of E
+ * experts, cols % 32 == 0, is
+ *   q      [E, rows, cols/2] bytes, element 2 i in the low half of byte i;
+ *   scale  [E, ceil(rows/128), ceil(cols/128), 512] bytes, the biased exponents
+ *          of X (255: NaN): row r and block b of a tile of 128 rows x 4 blocks
+ *          at 16 (r % 32) + 4 (r / 32) + b, as the tensor cores take them.
+ *          Blocks past the row's end in its last tile are 0; rows past the last
+ *          one are not written.
+ * With MOE_MXFP4_GATE_UP the rows are a gate and an up projection, rows/2 each,
+ * and a tile holds the scales of 64 rows of the gate, then of the same 64 of up:
+ * tile f / 64, row f % 64 for the gate's f, 64 + f % 64 for up's (q is in the
+ * rows' own order).  moe_ffn_mxfp4 takes its gate and up weights so. */
+enum { MOE_MXFP4_GATE_UP = 1u };
+
+/* Bytes of the scales of E x rows x cols elements (host only); 0 if a size is not
+ * positive or cols % 32 != 0. */
+size_t moe_mxfp4_scale_bytes(int32_t num_experts, int32_t rows, int32_t cols);
+
+/* Quantisation to MXFP4 of rows where they stand: weights, or rows that
+ * moe_dispatch or another kernel left in the experts' buffers.
+ * In:   src [E, rows, cols] bf16; expert_num_tokens [E] int32, or NULL: every
+ *       row exists.  Rows from clamp(count, 0, rows) on are neither read nor
+ *       written, and their scales are not.
+ * Out:  q, scale as above.
+ * Work: the workspace of the plan that produced the counts, or NULL: nothing is
+ *       written if its status word is set.
+ * Limits: cols % 32 == 0; E * rows < 2^31; E * rows * cols < 2^46.  src, q and
+ *       scale 16-byte aligned.  MOE_MXFP4_GATE_UP: rows even, no counts.
+ * Errors: INVALID_ARG (null pointer, size not positive, unknown flag, odd rows
+ *       or counts with GATE_UP), UNSUPPORTED, ALIGNMENT, CUDA. */
+moe_status moe_quant_mxfp4(int32_t num_experts, int32_t rows, int32_t cols, const void *src,
+                           const int32_t *expert_num_tokens, uint32_t flags, void *q, void *scale,
+                           void *workspace, void *stream);
+
+/* The other way: out [E, rows, cols] bf16 = q * X, exactly.  Everything else as
+ * moe_quant_mxfp4. */
+moe_status moe_dequant_mxfp4(int32_t num_experts, int32_t rows, int32_t cols, const void *q,
+                             const void *scale, const int32_t *expert_num_tokens, uint32_t flags,
+                             void *out, void *workspace, void *stream);
+
+/* Dispatch in MXFP4: the rows of moe_dispatch, quantised on the fly (the
+ * passages of moe_dispatch; the pages' payload is E4M3).  Each token is read
+ * and quantised once and written to its K rows.
+ * In:   x, topk_idx, slot_of as moe_dispatch.
+ * Out:  expert_x [E, cap, H/2] and expert_x_scale, the scales of [E, cap, H] as
+ *       above, both 16-byte aligned; the routed rows only.
+ * Work, ordering, device errors: as moe_dispatch (without flags).
+ * Limits: H % 32 == 0; payload BF16 (UNSUPPORTED otherwise).
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA. */
+moe_status moe_dispatch_mxfp4(const moe_shape *shape, const void *x, const int32_t *topk_idx,
+                              const int32_t *slot_of, void *expert_x, void *expert_x_scale,
+                              void *workspace, void *stream);
+
 /* Synchronise `stream` and read the workspace status word into *out (MOE_OK
  * or a device error).  The only call that waits for the device; meant for
  * tests and error handling, not for the hot path.
