@@ -110,6 +110,8 @@ SIGNATURES = {
     "moe_quant_mxfp4": ([_I32, _I32, _I32, _P, _P, _U32, _P, _P, _P, _P], ctypes.c_int),
     "moe_dequant_mxfp4": ([_I32, _I32, _I32, _P, _P, _P, _U32, _P, _P, _P], ctypes.c_int),
     "moe_dispatch_mxfp4": ([_SP, _P, _P, _P, _P, _P, _P, _P], ctypes.c_int),
+    "moe_ffn_mxfp4_workspace_size": ([_SP, _I32], _S),
+    "moe_ffn_mxfp4": ([_SP, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P], ctypes.c_int),
     "moe_plan_dispatch": ([_SP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P], ctypes.c_int),
 }
 
@@ -444,6 +446,23 @@ def dispatch_mxfp4(shape: Shape, x, topk_idx, slot_of, expert_x, expert_x_scale,
                                            _ptr(expert_x), _ptr(expert_x_scale), _ptr(workspace),
                                            _stream(stream))
     return _check(st, "moe_dispatch_mxfp4", check)
+
+
+def ffn_mxfp4_workspace_size(shape: Shape, intermediate: int) -> int:
+    return load_library().moe_ffn_mxfp4_workspace_size(ctypes.byref(shape), intermediate)
+
+
+def ffn_mxfp4(shape: Shape, intermediate: int, expert_x, expert_x_scale, w_gate_up, w_gate_up_scale,
+              w_down, w_down_scale, expert_num_tokens, expert_act, expert_act_scale, expert_y,
+              workspace, stream=None, check=True) -> Status:
+    """moe_ffn_mxfp4; ``expert_num_tokens`` may be None (every row exists)."""
+    st = load_library().moe_ffn_mxfp4(ctypes.byref(shape), intermediate, _ptr(expert_x),
+                                      _ptr(expert_x_scale), _ptr(w_gate_up), _ptr(w_gate_up_scale),
+                                      _ptr(w_down), _ptr(w_down_scale), _ptr(expert_num_tokens),
+                                      _ptr(expert_act), _ptr(expert_act_scale), _ptr(expert_y),
+                                      _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                      _stream(stream))
+    return _check(st, "moe_ffn_mxfp4", check)
 
 
 def read_status(workspace, stream=None) -> Status:

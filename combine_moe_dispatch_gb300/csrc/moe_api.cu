@@ -367,22 +367,22 @@ moe_status moe_silu_mul_quant(const moe_shape *shape, int32_t intermediate, cons
   return from_cuda(launch_silu_quant(p, (cudaStream_t)stream));
 }
 
-// Checks that moe_ffn and moe_ffn_backward share.
-static moe_status ffn_check(const moe_shape *shape, int32_t intermediate, const void *workspace,
-                            size_t workspace_bytes) {
+// Checks that moe_ffn, moe_ffn_backward and moe_ffn_mxfp4 share; `need` bytes of
+// workspace, rows of a multiple of `step` elements.
+static moe_status ffn_check(const moe_shape *shape, int32_t intermediate, int32_t step,
+                            const void *workspace, size_t workspace_bytes, size_t need) {
   moe_status st = check_shape(shape);
   if (st != MOE_OK) return st;
   if (intermediate <= 0) return MOE_ERR_INVALID_ARG;
-  if (shape->payload != MOE_PAYLOAD_BF16 || intermediate % 8 != 0 || intermediate >= (1 << 29) ||
-      shape->hidden >= (1 << 30))
+  if (shape->payload != MOE_PAYLOAD_BF16 || intermediate % step != 0 || shape->hidden % step != 0 ||
+      intermediate >= (1 << 29) || shape->hidden >= (1 << 30))
     return MOE_ERR_UNSUPPORTED;
   const int64_t rows = (int64_t)shape->num_experts * shape->capacity, lim = (int64_t)1 << 46;
   // rows < 2^31 and the widths < 2^32: no product here passes 2^63
   if (rows * 2 * intermediate >= lim || rows * shape->hidden >= lim ||
       (int64_t)4 * intermediate >= ((int64_t)1 << 40) / shape->hidden)
     return MOE_ERR_UNSUPPORTED;
-  if (!workspace || workspace_bytes < moe_ffn_workspace_size(shape, intermediate))
-    return MOE_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
   return aligned(workspace, 16) ? MOE_OK : MOE_ERR_ALIGNMENT;
 }
 
@@ -404,7 +404,8 @@ moe_status moe_ffn(const moe_shape *shape, int32_t intermediate, const void *exp
                    const void *w_gate_up, const void *w_down, const int32_t *expert_num_tokens,
                    void *expert_h, void *expert_act, void *expert_y, void *workspace,
                    size_t workspace_bytes, void *stream) {
-  const moe_status st = ffn_check(shape, intermediate, workspace, workspace_bytes);
+  const moe_status st = ffn_check(shape, intermediate, 8, workspace, workspace_bytes,
+                                  moe_ffn_workspace_size(shape, intermediate));
   if (st != MOE_OK && st != MOE_ERR_WORKSPACE && st != MOE_ERR_ALIGNMENT) return st;
   if (!expert_x || !w_gate_up || !w_down || !expert_act || !expert_y) return MOE_ERR_INVALID_ARG;
   if (st != MOE_OK) return st;
@@ -434,7 +435,8 @@ moe_status moe_ffn_backward(const moe_shape *shape, int32_t intermediate, const 
                             const void *w_down, const int32_t *expert_num_tokens, void *expert_act,
                             void *d_expert_h, void *d_expert_x, void *d_w_gate_up, void *d_w_down,
                             void *workspace, size_t workspace_bytes, void *stream) {
-  const moe_status st = ffn_check(shape, intermediate, workspace, workspace_bytes);
+  const moe_status st = ffn_check(shape, intermediate, 8, workspace, workspace_bytes,
+                                  moe_ffn_workspace_size(shape, intermediate));
   if (st != MOE_OK && st != MOE_ERR_WORKSPACE && st != MOE_ERR_ALIGNMENT) return st;
   if (!d_expert_y || !expert_x || !expert_h || !w_gate_up || !w_down || !expert_act || !d_expert_h)
     return MOE_ERR_INVALID_ARG;
@@ -668,6 +670,49 @@ moe_status moe_dispatch_mxfp4(const moe_shape *shape, const void *x, const int32
   p.E = shape->num_experts;
   p.K = shape->top_k;
   return from_cuda(launch_dispatch_mxfp4(p, (cudaStream_t)stream));
+}
+
+size_t moe_ffn_mxfp4_workspace_size(const moe_shape *shape, int32_t intermediate) {
+  const size_t plan = moe_workspace_size(shape);
+  if (plan == 0 || intermediate <= 0) return 0;
+  return plan + ffn_mxfp4_scratch(shape->num_experts, shape->capacity, shape->hidden, intermediate);
+}
+
+moe_status moe_ffn_mxfp4(const moe_shape *shape, int32_t intermediate, const void *expert_x,
+                         const void *expert_x_scale, const void *w_gate_up,
+                         const void *w_gate_up_scale, const void *w_down, const void *w_down_scale,
+                         const int32_t *expert_num_tokens, void *expert_act, void *expert_act_scale,
+                         void *expert_y, void *workspace, size_t workspace_bytes, void *stream) {
+  const moe_status st = ffn_check(shape, intermediate, 32, workspace, workspace_bytes,
+                                  moe_ffn_mxfp4_workspace_size(shape, intermediate));
+  if (st != MOE_OK && st != MOE_ERR_WORKSPACE && st != MOE_ERR_ALIGNMENT) return st;
+  if (!expert_x || !expert_x_scale || !w_gate_up || !w_gate_up_scale || !w_down || !w_down_scale ||
+      !expert_act || !expert_act_scale || !expert_y)
+    return MOE_ERR_INVALID_ARG;
+  if (st != MOE_OK) return st;
+  if (!aligned(expert_x, 16) || !aligned(expert_x_scale, 16) || !aligned(w_gate_up, 16) ||
+      !aligned(w_gate_up_scale, 16) || !aligned(w_down, 16) || !aligned(w_down_scale, 16) ||
+      !aligned(expert_act, 16) || !aligned(expert_act_scale, 16) || !aligned(expert_y, 16) ||
+      !aligned(expert_num_tokens, 4))
+    return MOE_ERR_ALIGNMENT;
+  FfnMxfp4Params f = {};
+  f.counts = expert_num_tokens;
+  f.hdr = header(workspace);
+  f.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + ws_layout(*shape).total);
+  f.E = shape->num_experts;
+  f.cap = shape->capacity;
+  f.H = shape->hidden;
+  f.I = intermediate;
+  f.x = static_cast<const uint8_t *>(expert_x);
+  f.x_scale = static_cast<const uint8_t *>(expert_x_scale);
+  f.w_gate_up = static_cast<const uint8_t *>(w_gate_up);
+  f.w_gate_up_scale = static_cast<const uint8_t *>(w_gate_up_scale);
+  f.w_down = static_cast<const uint8_t *>(w_down);
+  f.w_down_scale = static_cast<const uint8_t *>(w_down_scale);
+  f.act = static_cast<uint8_t *>(expert_act);
+  f.act_scale = static_cast<uint8_t *>(expert_act_scale);
+  f.y = static_cast<uint16_t *>(expert_y);
+  return from_cuda(launch_ffn_mxfp4(f, (cudaStream_t)stream));
 }
 
 moe_status moe_read_status(const void *workspace, void *stream, moe_status *out) {

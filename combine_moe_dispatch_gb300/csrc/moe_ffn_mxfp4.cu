@@ -1,0 +1,608 @@
+// moe_ffn_mxfp4.cu -- the experts' gated feed-forward on 4-bit operands, as
+// grouped block-scaled matrix products on the tensor cores.
+//
+// What it computes, for expert e and its count[e] rows x, all operands MXFP4
+// (blocks of 32 elements with a power of two each):
+//   h = x Wgu^T (gate | up),  a = SiLU(gate) * up,  a4 = MXFP4(a),  y = a4 Wd^T.
+//
+// How: one launch.  The order of the work, the pairs of CTAs, their warps' roles
+// and the wait between a and y are moe_ffn.cu's (moe_pairs.cuh): weights' output
+// features on the 256-row side, the expert's tokens on the column side, a ring of
+// stages filled by TMA, tcgen05.mma.cta_group::2, accumulators in tensor memory
+// two tiles deep, eight epilogue warps.  What 4 bits change:
+//  - A stage is 256 k (128 bytes of a row, as 64 k of bf16 are): 16 KB of weights
+//    per CTA, up to 16 KB of tokens, 1 KB of the weights' scales and up to 2 KB of
+//    the tokens'.  The scales stand in memory in the tiles that a copy into tensor
+//    memory takes (tcgen05.cp), so that they come by TMA and go on without passing
+//    through registers.  Both CTAs need the scales of all the tile's tokens.
+//  - Gate and up of the same 64 features are the two halves of a CTA's 128 rows;
+//    their scales lie so in memory (MOE_MXFP4_GATE_UP).
+//  - Scales take 24 columns of tensor memory, which leaves 480 for two
+//    accumulators of 256: they overlap by 32 columns.  The epilogue reads those
+//    first, and the next tile starts when it has.  Tiles of up to 224 columns do
+//    not overlap.
+//  - a is quantised where it is computed: a block's 32 features are 8 lanes' 4, so
+//    that its maximum is three shuffles.
+//
+// Rounding: products of E2M1 numbers and powers of two, summed in binary32; a is
+// rounded to MXFP4 from binary32, y to bf16, once each.
+#include <mutex>
+
+#include "moe_mxfp4.cuh"
+#include "moe_pairs.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 384;          // warps: 0 TMA, 1 MMA, 2 none, 3 scheduling, 4-11 epilogue
+constexpr int kStages = 5;
+constexpr int kBlockK = 256;           // one 128-byte swizzled line of 4-bit elements
+constexpr uint32_t kHalfBytes = 128 * 128;               // a CTA's half of one operand: 16 KB
+constexpr uint32_t kScaleOff = 2 * kHalfBytes;           // A's scales: 2 tiles, one for each 128 k
+constexpr uint32_t kScaleStage = 2 * kScaleTileBytes;
+constexpr uint32_t kStageBytes = kScaleOff + 3 * kScaleStage;   // and B's: 2 or 4 tiles
+constexpr uint32_t kStagingBytes = 2 * 16384;            // epilogue, one buffer per group
+constexpr uint32_t kBarOff = kStages * kStageBytes + kStagingBytes;
+constexpr uint32_t kRingOff = kBarOff + 256;
+constexpr uint32_t kSmem = kRingOff + kRing * 64 + 1024;        // + alignment slack
+static_assert(kSmem <= 232448, "shared memory of one CTA");
+static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1024 bytes");
+// Tensor memory: the scales, then two accumulators of 256 columns that share
+// kShared of them.
+constexpr uint32_t kAcc0 = 32, kAcc1 = 256;
+constexpr int kShared = (int)(kAcc0 + kTileCols - kAcc1);       // a multiple of the epilogue's chunks of 32
+constexpr int kApart = kTileCols - kShared;                     // tiles of so many columns share none
+static_assert(kShared == 32, "the epilogue reads the shared columns as one chunk");
+
+// Words of a tile's record that the matrix instructions need.
+constexpr uint32_t kMxWords = kMathWords | kK0;
+
+struct MxJob {
+  CUtensorMap a, a_scale;
+  CUtensorMap b[4], b_scale[2];        // boxes of 16, 32, 64 and 128 tokens; of 128 and 256 tokens' scales
+  uint8_t *q, *scale;                  // gate and up: a4
+  uint16_t *out;                       // y
+  int M, K, N;                         // features, contraction; N is not used
+  int mt;                              // tiles of 256 accumulator rows (gate and up: of 128 features)
+  int row_tiles, block_tiles;          // of a4's scales
+};
+
+struct MxParams {
+  static constexpr int kKind = kForward, kBlock = kBlockK, kJobs = 2;
+  static constexpr bool kWholeTiles = true;
+  MxJob job[kJobs];                    // a, y
+  const int32_t *counts;               // [E], or null (cap rows each)
+  WsHeader *hdr;
+  float *part;                         // partial sums of split contractions
+  uint32_t *tickets;                   // finished parts, 4 bits for each split tile and CTA of the pair
+  UnitCounter *units;
+  int E, cap;
+};
+
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t *smem_p = smem_raw + (smem - smem_u32(smem_raw));
+  // the same value in every lane, and known to be
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_cta_rank();
+
+  const uint32_t bars = smem + kBarOff;
+  const uint32_t full = bars, empty = bars + 8 * kStages;
+  const uint32_t tm_full = bars + 16 * kStages, tm_empty = tm_full + 16, tm_shared = tm_empty + 16;
+  const uint32_t tm_slot = tm_shared + 16;
+  constexpr uint32_t kSlotOff = kBarOff + 16 * kStages + 48, kLastOff = kSlotOff + 8;
+  static_assert(kLastOff + 4 <= kBarOff + 192, "the barriers fit");
+  // barriers of the ring of tiles
+  const uint32_t rec_full = bars + 192, rec_empty = bars + 224;
+  Tile *ring = reinterpret_cast<Tile *>(smem_p + kRingOff);
+  volatile uint32_t *last_in = reinterpret_cast<uint32_t *>(smem_p + kLastOff);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init_at(full + 8 * s, 1);     // the leader's arrival, and the bytes of both CTAs
+      tc::mbar_init_at(empty + 8 * s, 1);    // the commit of the stage's instructions
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init_at(tm_full + 8 * b, 1);
+      tc::mbar_init_at(tm_empty + 8 * b, 2 * kEpiWarps);   // the epilogue warps of both CTAs
+      tc::mbar_init_at(tm_shared + 8 * b, 2 * kEpiWarps);
+    }
+    for (int r = 0; r < kRing; ++r) {
+      tc::mbar_init_at(rec_full + 8 * r, 1);
+      // in the leader: TMA and epilogue of both CTAs, and the MMA warp
+      tc::mbar_init_at(rec_empty + 8 * r, 2 * (kEpiWarps + 1) + 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (threadIdx.x == 32) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      tc::prefetch_map(&p.job[j].a);
+      tc::prefetch_map(&p.job[j].a_scale);
+    }
+    tc::prefetch_map(&p.job[0].b[0]);
+    tc::prefetch_map(&p.job[0].b_scale[0]);
+  }
+  if (warp == 2) tc::tmem_alloc_pair(tm_slot, kTmemCols);
+  tc::fence_before();
+  __syncthreads();
+  cluster_arrive_relaxed();              // the barriers' initial values are released above
+  cluster_wait();
+  tc::fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem_p + kSlotOff);
+
+  pdl_allow_dependents();
+  pdl_wait_for_previous();
+  // After a plan error, or a wait of an earlier launch that ran out, no tile is
+  // computed and nothing is written.  The block's threads decide together: both
+  // words may change under them when another pair's wait runs out.
+  const uint64_t tmo = p.hdr->timeout_ns;
+  const StatusWords words = read_status_words(p.hdr);
+  const bool broken = (words.flags & kFfnBroken) != 0;
+  const bool live = __syncthreads_and(words.status == MOE_OK && !broken);
+  if (broken && threadIdx.x == 0) report_status(p.hdr, MOE_ERR_TIMEOUT);
+  const uint64_t limit = tmo ? tmo : kDefaultTimeoutNs;
+  bool ok = true;
+  Tile t;
+  Feed feed(ring, rec_full, tc::map_rank(rec_empty, 0), limit);
+
+  if (warp == 3) {
+    // ---- scheduling: one warp of the leader takes units and announces their
+    // tiles to both CTAs.  A unit belongs to a pair that runs, since others will
+    // wait for it.
+    Schedule<MxParams> sched(p);
+    const uint32_t peer_full = tc::map_rank(rec_full, 1), peer_ring = tc::map_rank(smem + kRingOff, 1);
+    bool written = false;                    // all of a
+    const uint32_t epoch = rank == 0 ? __ldcg(&p.units->epoch) & 1u : 0u;
+    uint32_t c = 0;
+    for (; live && rank == 0; ++c) {
+      const uint32_t s = c % kRing;
+      // A unit is taken as late as its tile allows: once the record 2 or kRing
+      // before it has been read by every warp of both CTAs.
+      const uint32_t ahead = c > 0 && t.nk >= kLongTile ? 2 : kRing;
+      if (c >= ahead) {
+        const uint32_t r = c - ahead;
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(rec_empty + 8 * (r % kRing), (r / kRing) & 1u, limit));
+        if (!ok) break;
+      }
+      // one tile of y for each pair until all of a is written
+      if (c > 0 && t.need != 0 && !written) {
+        written = ok = __all_sync(0xFFFFFFFFu, wait_count(p.units->ready + epoch, (uint32_t)t.need, limit));
+        if (!ok) break;
+      }
+      unsigned long long n = 0;
+      if (lane == 0) n = atomicAdd(&p.units->next, 1ull);
+      t.valid = sched.find((int64_t)__shfl_sync(0xFFFFFFFFu, n, 0), t);
+      t.epoch = epoch;
+      if (lane == 0) {
+        ring[s] = t;
+        tc::mbar_arrive_local(rec_full + 8 * s);
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_expect_at(peer_full + 8 * s, sizeof(Tile));
+      if (lane < 4)
+        tc::store_async(peer_ring + s * (uint32_t)sizeof(Tile) + lane * 16,
+                        reinterpret_cast<const uint4 *>(ring + s)[lane], peer_full + 8 * s);
+      if (!t.valid) break;
+    }
+    // the other CTA's arrivals for the records before the last (number c) land
+    // before this one may exit
+    if (live && rank == 0)
+      for (uint32_t r = c < kRing ? 0 : c - kRing + 1; ok && r < c; ++r)
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(rec_empty + 8 * (r % kRing), (r / kRing) & 1u, limit));
+    if (rank == 0 && lane == 0 && atomicAdd(&p.units->done, 1u) == (gridDim.x >> 1) - 1) {
+      // every pair knows this launch's epoch by now: the next one counts in the
+      // other counter, which nobody uses any more
+      p.units->next = 0;
+      p.units->done = 0;
+      p.units->ready[epoch ^ 1u] = 0;
+      p.units->epoch = epoch ^ 1u;
+    }
+  } else if (live && warp == 0) {
+    // ---- TMA: both CTAs load their halves; bytes complete on the leader's barrier
+    int s = 0;
+    uint32_t ph = 0;
+    const uint32_t full0 = tc::map_rank(full, 0);
+    bool written = false;                    // all of a
+    while (ok && feed.next_uniform<kCopyWords>(t, ok)) {
+      const MxJob &j = p.job[t.job];
+      const uint32_t half_n = t.n >> 1;
+      const int bsel = half_n <= 16 ? 0 : half_n <= 32 ? 1 : half_n <= 64 ? 2 : 3;
+      const int wide = t.n > 128;
+      const uint32_t bytes = kHalfBytes + (16u << bsel) * 128u + (2u + wide) * kScaleStage;
+      const int n0 = t.n0 + (int)(rank * half_n), rt = t.m * 2 + (int)rank;
+      // 64 gate rows and the same 64 features of up in one copy, or 128 features
+      const int a0 = rt * (t.job == 0 ? 64 : 128);
+      if (t.need != 0 && !written) {
+        written = ok = __all_sync(0xFFFFFFFFu, wait_count(p.units->ready + t.epoch, (uint32_t)t.need, limit));
+        if (!ok) break;
+      }
+      for (int kb = 0; kb < t.nk; ++kb) {
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(empty + 8 * s, ph ^ 1u, limit));
+        if (!ok) break;
+        const uint32_t sa = smem + s * kStageBytes;
+        const int k = t.k0 + kb;
+        const uint32_t bar = full0 + 8 * s;
+        if (rank == 0) tc::mbar_expect_warp(full + 8 * s, 2 * bytes);
+        tc::tma_load_pair(sa, &j.a, bar, k * 128, a0, 0, t.e);
+        tc::tma_load_pair(sa + kHalfBytes, &j.b[bsel], bar, k * 128, n0, 0, t.e);
+        tc::tma_load_pair(sa + kScaleOff, &j.a_scale, bar, 0, 2 * k, rt, t.e);
+        tc::tma_load_pair(sa + kScaleOff + kScaleStage, &j.b_scale[wide], bar, 0, 2 * k, t.n0 >> 7, t.e);
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    // the last commits on this CTA's barriers land before it may exit
+    for (int i = 0; ok && i < kStages; ++i) {
+      ok = __all_sync(0xFFFFFFFFu, wait_bar(empty + 8 * s, ph ^ 1u, limit));
+      if (++s == kStages) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+  } else if (live && warp == 1 && rank == 0) {
+    // ---- matrix instructions, one warp of the leading CTA.  What it needs
+    // next (the next stage, tile and accumulator) is asked for while the
+    // instructions of a stage run, so that the tensor cores have work meanwhile.
+    int s = 0;
+    uint32_t ph = 0, it = 0;
+    bool stage_ready = false, acc_ready = false;
+    int before = 0;                          // columns of the tile before
+    const uint64_t desc_a0 = tc::smem_desc(smem, 16u), desc_b0 = tc::smem_desc(smem + kHalfBytes, 16u);
+    const uint64_t desc_sa0 = tc::scale_desc(smem + kScaleOff);
+    const uint64_t desc_sb0 = tc::scale_desc(smem + kScaleOff + kScaleStage);
+    bool more = feed.next_uniform<kMxWords>(t, ok);
+    while (ok && more) {
+      const uint32_t buf = it & 1u;
+      const uint32_t d = tmem + (buf ? kAcc1 : kAcc0);
+      const uint32_t idesc = tc::instr_desc_mx(256, t.n);
+      // 64 k an instruction; the row's end cuts the last block
+      const int left = p.job[t.job].K - (t.k0 + t.nk - 1) * kBlockK;
+      const uint32_t tail = left >= kBlockK ? 4u : (uint32_t)((left + 63) >> 6);
+      if (!acc_ready)
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(tm_empty + 8 * buf, ((it >> 1) & 1u) ^ 1u, limit));
+      acc_ready = false;
+      // the columns that it shares with the tile before, if either has so many
+      if (ok && it > 0 && (buf ? before : t.n) > kApart)
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(tm_shared + 8 * (buf ^ 1u), ((it - 1) >> 1) & 1u, limit));
+      before = t.n;
+      tc::fence_after();
+      Feed::Raw next_raw;
+      bool have = false;                     // the next tile's record is being read
+      for (int kb = 0; ok && kb < t.nk; ++kb) {
+        if (!stage_ready) {
+          ok = __all_sync(0xFFFFFFFFu, wait_bar(full + 8 * s, ph, limit));
+          if (!ok) break;
+        }
+        const bool last = kb == t.nk - 1;
+        const uint32_t steps = last ? tail : 4u;
+        tc::fence_after();
+        const uint64_t at = (uint64_t)(s * (kStageBytes >> 4));
+        const uint32_t stage = empty + 8 * s;
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+        // the last block asks for the next accumulator, the others for the next record
+        const uint32_t bar1 = last || have ? tm_empty + 8 * (buf ^ 1u) : feed.full + 8 * feed.s;
+        const uint32_t p1 = last || have ? (((it + 1) >> 1) & 1u) ^ 1u : feed.ph;
+        tc::load_scales(tmem, desc_sa0 + at, desc_sb0 + at, steps > 2, t.n > 128);
+        const tc::Asked r = tc::mma_stage_mx(d, desc_a0 + at, desc_b0 + at, idesc, tmem, kb > 0, steps, stage,
+                                             full + 8 * s, ph, bar1, p1);
+        stage_ready = __all_sync(0xFFFFFFFFu, r.first);
+        const bool second = __all_sync(0xFFFFFFFFu, r.second);
+        if (last) {
+          acc_ready = second;
+        } else if (!have && second) {
+          have = true;
+          next_raw = feed.read();
+        }
+      }
+      if (ok) tc::mma_commit_pair(tm_full + 8 * buf);
+      if (ok) more = have ? feed.spread<kMxWords>(next_raw, t) : feed.next_uniform<kMxWords>(t, ok);
+      ++it;
+    }
+    // the other CTA's arrivals for both accumulators land before this one may exit
+    for (int i = 0; ok && i < 2; ++i, ++it) {
+      const uint32_t parity = ((it >> 1) & 1u) ^ 1u;
+      ok = __all_sync(0xFFFFFFFFu, wait_bar(tm_empty + 8 * (it & 1u), parity, limit) &&
+                                       wait_bar(tm_shared + 8 * (it & 1u), parity, limit));
+    }
+  } else if (live && warp >= 4) {
+    // ---- epilogue: tensor memory -> registers -> shared memory -> results
+    uint32_t it = 0;
+    const int wq = warp & 3, grp = (warp - 4) >> 2, tid = (threadIdx.x - 128) & 127;
+    const uint32_t empty0 = tc::map_rank(tm_empty, 0), shared0 = tc::map_rank(tm_shared, 0);
+    float *const st = reinterpret_cast<float *>(smem_p + kStages * kStageBytes + grp * 16384);
+    // a thread's place in the staged chunk: 4 features of rows r8, r8 + 8, ...
+    const int i4 = tid & 15, r8 = tid >> 4;
+    while (true) {
+      const bool more = feed.next(t, ok);
+      const uint32_t buf = it & 1u;
+      const MxJob &j = p.job[t.job];
+      const bool gate = t.job == 0;
+      const int rt = t.m * 2 + (int)rank;
+      const int f0 = rt * (gate ? 64 : 128) + 4 * i4;
+      const int64_t row0 = (int64_t)t.e * p.cap + t.n0;
+      // one token's 4 + 4 features: sums lo, hi -> results.  Whole half-warps
+      // have one token; all 32 lanes call it, `in`: the token exists.
+      const auto emit = [&](int tok, bool in, const float4 &lo4, const float4 &hi4) {
+        const int64_t row = row0 + tok;
+        if (gate) {                          // lo: gate, hi: up of the same features
+          const float lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
+          float a[4];
+          uint32_t most = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            a[k] = lo[k] * sigmoid(lo[k]) * hi[k];
+            most = max(most, __float_as_uint(a[k]) & 0x7FFFFFFFu);
+          }
+#pragma unroll
+          for (int d = 4; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+          const uint32_t byte = mx_scale(most >> 23);
+          const float inv = mx_inverse(byte);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) a[k] = byte == 255u ? 0.0f : a[k] * inv;
+          // features past the last have a scale of 0 in the last tile of blocks
+          const uint32_t scale = f0 < j.M ? byte : 0u;
+          const uint32_t scale2 = scale | __shfl_down_sync(0xFFFFFFFFu, scale, 8) << 8;
+          if (in && f0 < j.M) {
+            *reinterpret_cast<uint16_t *>(j.q + (row * j.M + f0) / 2) = (uint16_t)e2m1x4(a);
+          }
+          if (in && i4 == 0) {
+            const int r = t.n0 + tok;
+            const int64_t tile = ((int64_t)t.e * j.row_tiles + (r >> 7)) * j.block_tiles + t.m;
+            *reinterpret_cast<uint16_t *>(j.scale + tile * kScaleTileBytes + (r & 31) * 16 +
+                                          ((r >> 5) & 3) * 4 + 2 * rank) = (uint16_t)scale2;
+          }
+        } else if (in) {
+          const float lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
+          uint16_t *q = j.out + row * j.M + f0;
+          if (f0 < j.M) *reinterpret_cast<uint2 *>(q) = make_uint2(pack2(lo[0], lo[1]), pack2(lo[2], lo[3]));
+          if (f0 + 64 < j.M)
+            *reinterpret_cast<uint2 *>(q + 64) = make_uint2(pack2(hi[0], hi[1]), pack2(hi[2], hi[3]));
+        }
+      };
+      if (more) {
+        ok = wait_bar(tm_full + 8 * buf, (it >> 1) & 1u, limit);
+        tc::fence_after();
+      }
+      // all the warps agree to go on, and are done with the staging buffers
+      ok = named_sync_and(3, 32 * kEpiWarps, ok);
+      if (!ok || !more) break;
+      const uint32_t src = tmem + ((uint32_t)(wq * 32) << 16) + (buf ? kAcc1 : kAcc0);
+      const auto arrive = [&](uint32_t bar) {     // this warp has read its part of the columns
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_remote(bar + 8 * buf);
+      };
+      // The group's chunks of 32 columns, those that the accumulators share first:
+      // the first accumulator's last, the second's first.
+      const int chunks = (t.n - grp * 32 + 63) >> 6;       // t.n >= 32
+      const bool shares = buf ? grp == 0 : grp == 1 && t.n > kApart;
+      if (!shares) arrive(shared0);
+      if (chunks <= 0) arrive(empty0);
+      const auto chunk = [&](int i) { return grp * 32 + 64 * (buf ? i : chunks - 1 - i); };
+      const auto read = [&](int i, uint32_t (&v)[32]) {
+        tc::tmem_ld32(v, src + chunk(i));
+        tc::tmem_ld_wait();
+        if (i == 0 && shares) arrive(shared0);
+        if (i == chunks - 1) arrive(empty0);
+      };
+      bool wrote = true;                     // this was the tile's last part
+      if (t.split > 1) {
+        // A part of a split contraction leaves its sums in the workspace
+        // ([tile][part][CTA][column][128 features]); the last part to finish
+        // adds all of them, in the order of the parts.
+        const int64_t size = (int64_t)t.part_cols * 128;
+        const float *part = p.part + (t.slot * t.split * 2 + (int)rank) * size;
+        float *own = p.part + ((t.slot * t.split + t.part) * 2 + (int)rank) * size;
+        for (int i = 0; i < chunks; ++i) {
+          uint32_t v[32];
+          read(i, v);
+#pragma unroll
+          for (int q = 0; q < 32; ++q)
+            __stcg(own + (chunk(i) + q) * 128 + wq * 32 + lane, __uint_as_float(v[q]));
+        }
+        __threadfence();
+        named_sync(3, 32 * kEpiWarps);
+        if (threadIdx.x == 128) {
+          const uint32_t ticket = t.slot * 2 + rank, shift = 4 * (ticket & 7);
+          const uint32_t was = atomicAdd(p.tickets + (ticket >> 3), 1u << shift);
+          const bool last = ((was >> shift) & 15u) == (uint32_t)t.split - 1;
+          if (last) atomicSub(p.tickets + (ticket >> 3), (uint32_t)t.split << shift);
+          *last_in = last;
+          __threadfence();
+        }
+        named_sync(3, 32 * kEpiWarps);
+        wrote = *last_in != 0;
+        if (wrote)
+          for (int c = grp * 32; c < t.n; c += 64) {
+            float4 lo[4], hi[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) lo[r] = hi[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+            for (int s = 0; s < t.split; ++s)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float *q = part + s * 2 * size + (c + r * 8 + r8) * 128 + 4 * i4;
+                const float4 a = __ldcg(reinterpret_cast<const float4 *>(q));
+                const float4 b = __ldcg(reinterpret_cast<const float4 *>(q + 64));
+                lo[r] = make_float4(lo[r].x + a.x, lo[r].y + a.y, lo[r].z + a.z, lo[r].w + a.w);
+                hi[r] = make_float4(hi[r].x + b.x, hi[r].y + b.y, hi[r].z + b.z, hi[r].w + b.w);
+              }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) emit(c + r * 8 + r8, c + r * 8 + r8 < t.cols, lo[r], hi[r]);
+          }
+      } else {
+        for (int i = 0; i < chunks; ++i) {
+          uint32_t v[32];
+          read(i, v);
+          if (i > 0) named_sync(1 + grp, 128);             // the last chunk has been read
+#pragma unroll
+          for (int q = 0; q < 32; ++q) st[q * 128 + wq * 32 + lane] = __uint_as_float(v[q]);
+          named_sync(1 + grp, 128);
+          const int c = chunk(i);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int tok = r * 8 + r8;
+            emit(c + tok, c + tok < t.cols, *reinterpret_cast<const float4 *>(st + tok * 128 + 4 * i4),
+                 *reinterpret_cast<const float4 *>(st + tok * 128 + 64 + 4 * i4));
+          }
+        }
+      }
+      if (gate && wrote) {
+        // half a tile of a is written, for copies of other CTAs to read
+        tc::fence_async_global();
+        __threadfence();
+        named_sync(3, 32 * kEpiWarps);
+        if (threadIdx.x == 128) {
+          __threadfence();
+          atomicAdd(p.units->ready + t.epoch, 1u);
+        }
+      }
+      ++it;
+    }
+  }
+
+  if (!ok) {
+    // a wait ran out: report it, and give the copies and products that are
+    // already issued (microseconds of work) time to land before the exit
+    if (lane == 0) {
+      atomicOr(&p.hdr->debug_flags, kFfnBroken);
+      report_status(p.hdr, MOE_ERR_TIMEOUT);
+      for (int i = 0; i < 1000; ++i) __nanosleep(10000);
+    }
+  }
+  // Neither CTA leaves while the other may still use its shared or tensor memory
+  // or its barriers: every arrival, copy and commit that comes from the other CTA
+  // has been waited for above, by the warp that needed it or by its owner.
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  cluster_arrive_relaxed();
+  cluster_wait();
+  tc::fence_after();
+  if (warp == 2) tc::tmem_free_pair(tmem, kTmemCols);
+}
+
+// --- host --------------------------------------------------------------------
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Bytes [d3][d2][d1][d0] of 4-bit rows, dense: boxes of deep x rows x 128 bytes,
+// 128-byte swizzle.
+bool map_rows(CUtensorMap *m, const void *base, int64_t d0, int64_t d1, int64_t d2, int64_t d3, int rows,
+              int deep = 1) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2, (cuuint64_t)d3};
+  const cuuint64_t strides[3] = {(cuuint64_t)d0, (cuuint64_t)(d0 * d1), (cuuint64_t)(d0 * d1 * d2)};
+  const cuuint32_t box[4] = {128, (cuuint32_t)rows, (cuuint32_t)deep, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The scales' tiles [E][row tiles][block tiles][512 bytes]: boxes of `deep` x 2
+// tiles, as they stand.
+bool map_scales(CUtensorMap *m, const void *base, const ScaleLayout &l, int64_t E, int deep) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {kScaleTileBytes / 4, (cuuint64_t)l.block_tiles, (cuuint64_t)l.row_tiles,
+                              (cuuint64_t)E};
+  const cuuint64_t s1 = kScaleTileBytes, s2 = s1 * l.block_tiles, s3 = s2 * l.row_tiles;
+  const cuuint64_t strides[3] = {s1, s2, s3};
+  const cuuint32_t box[4] = {kScaleTileBytes / 4, 2, (cuuint32_t)deep, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<void *>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The tokens' operand: the boxes that tiles of at most cap tokens use.
+bool map_tokens(MxJob &j, const void *rows, const void *scales, int64_t width, int64_t cap, int64_t E) {
+  for (int i = 0; i < 4; ++i) {
+    if (!map_rows(&j.b[i], rows, width / 2, cap, 1, E, 16 << i)) return false;
+    if (cap <= (32 << i)) break;
+  }
+  const ScaleLayout l = scale_layout(cap, width);
+  return map_scales(&j.b_scale[0], scales, l, E, 1) &&
+         (cap <= 128 || map_scales(&j.b_scale[1], scales, l, E, 2));
+}
+
+// Units of a product: its most tiles, each in up to kMaxSplit parts.
+int64_t units(const MxJob &j, const FfnMxfp4Params &f) {
+  return j.mt * f.E * cdiv(f.cap, kTileCols) * (cdiv(j.K, kBlockK) < 16 ? 1 : kMaxSplit);
+}
+
+}  // namespace
+
+size_t ffn_mxfp4_scratch(int64_t E, int64_t cap, int64_t H, int64_t I) {
+  const int64_t mt = cdiv(I, 128) > cdiv(H, 256) ? cdiv(I, 128) : cdiv(H, 256);
+  const int64_t most = mt * E * cdiv(cap, kTileCols) * kMaxSplit;
+  const int64_t cols = cap < kTileCols ? (cap + 31) / 32 * 32 : kTileCols;
+  return (size_t)((most < kMaxPairs ? most : kMaxPairs) * cols) * 256 * sizeof(float);
+}
+
+cudaError_t launch_ffn_mxfp4(const FfnMxfp4Params &f, cudaStream_t stream) {
+  MxParams p = {};
+  p.counts = f.counts;
+  p.hdr = f.hdr;
+  p.part = f.part;
+  p.tickets = f.hdr->reserved + kTicketWord;
+  p.units = reinterpret_cast<UnitCounter *>(f.hdr->reserved + kUnitWord);
+  p.E = f.E;
+  p.cap = f.cap;
+  MxJob &gu = p.job[0], &d = p.job[1];
+  const ScaleLayout act = scale_layout(f.cap, f.I);
+  if (!map_rows(&gu.a, f.w_gate_up, f.H / 2, f.I, 2, f.E, 64, 2) ||
+      !map_scales(&gu.a_scale, f.w_gate_up_scale, scale_layout(2 * (int64_t)f.I, f.H), f.E, 1) ||
+      !map_tokens(gu, f.x, f.x_scale, f.H, f.cap, f.E) ||
+      !map_rows(&d.a, f.w_down, f.I / 2, f.H, 1, f.E, 128) ||
+      !map_scales(&d.a_scale, f.w_down_scale, scale_layout(f.H, f.I), f.E, 1) ||
+      !map_tokens(d, f.act, f.act_scale, f.I, f.cap, f.E))
+    return cudaErrorInvalidValue;
+  gu.q = f.act;
+  gu.scale = f.act_scale;
+  gu.row_tiles = act.row_tiles;
+  gu.block_tiles = act.block_tiles;
+  gu.M = f.I;
+  gu.K = f.H;
+  gu.mt = (int)cdiv(f.I, 128);
+  d.out = f.y;
+  d.M = f.H;
+  d.K = f.I;
+  d.mt = (int)cdiv(f.H, 256);
+
+  static std::once_flag once[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t attr = cudaSuccess;
+  std::call_once(once[dev & 63], [&] {
+    attr = cudaFuncSetAttribute(ffn_mxfp4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  });
+  if (attr != cudaSuccess) return attr;
+  const int64_t tiles = units(gu, f) + units(d, f);
+  int64_t most = device_sm_count() / 2;
+  if (most > kMaxPairs) most = kMaxPairs;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(2 * (tiles < most ? tiles : most)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, ffn_mxfp4_kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace moe

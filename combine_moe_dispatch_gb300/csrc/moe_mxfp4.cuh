@@ -57,6 +57,21 @@ struct DispatchMxfp4Params {
   int N, E, K;
 };
 
+// The experts' feed-forward on MXFP4 operands.
+struct FfnMxfp4Params {
+  const int32_t *counts;       // [E] rows per expert, or null (cap each)
+  WsHeader *hdr;
+  float *part;                 // scratch: partial sums of split contractions
+  int E, cap, H, I;
+  const uint8_t *x, *x_scale;                  // rows [E, cap, H]
+  const uint8_t *w_gate_up, *w_gate_up_scale;  // rows [E, 2I, H], the scales 64 and 64
+  const uint8_t *w_down, *w_down_scale;        // rows [E, H, I]
+  uint8_t *act, *act_scale;                    // rows [E, cap, I]
+  uint16_t *y;                                 // [E, cap, H] bf16
+};
+size_t ffn_mxfp4_scratch(int64_t E, int64_t cap, int64_t H, int64_t I);
+
+cudaError_t launch_ffn_mxfp4(const FfnMxfp4Params &p, cudaStream_t stream);
 cudaError_t launch_quant_mxfp4(const QuantParams &p, cudaStream_t stream);
 cudaError_t launch_dequant_mxfp4(const DequantParams &p, cudaStream_t stream);
 cudaError_t launch_dispatch_mxfp4(const DispatchMxfp4Params &p, cudaStream_t stream);
@@ -84,8 +99,8 @@ __device__ __forceinline__ uint32_t mx_scale(uint32_t exponent) {
 __device__ __forceinline__ float mx_inverse(uint32_t scale) {
   return scale == 255u ? 0.0f : __uint_as_float((254u - scale) << 23);
 }
-// Two values -> two E2M1 in a byte, the first in the low half: to nearest, ties
-// to even, at most 6 in magnitude.
+// 8 values -> 8 E2M1, 4 bits each, the first lowest: to nearest, ties to even, at
+// most 6 in magnitude.
 __device__ __forceinline__ uint32_t e2m1x8(const float (&f)[8]) {
   uint32_t r;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
@@ -96,6 +111,18 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&f)[8]) {
       "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
       : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return r;
+}
+// The same of 4 values.
+__device__ __forceinline__ uint32_t e2m1x4(const float (&f)[4]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, z;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.u8.u32 z, 0;\n\t"
+      "mov.b32 %0, {a, b, z, z};\n\t}"
+      : "=r"(r)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]));
   return r;
 }
 #endif

@@ -1,4 +1,5 @@
-// moe_tc.cuh -- PTX helpers of the experts' products (moe_ffn.cu): TMA tile
+// moe_tc.cuh -- PTX helpers of the experts' products (moe_ffn.cu and
+// moe_ffn_mxfp4.cu): TMA tile
 // copies, tcgen05 matrix instructions on a pair of SMs, tensor memory, and
 // cluster-scope mbarriers.
 #pragma once
@@ -214,6 +215,85 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
   asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
                "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
                "[%0], %1;\n\t}" ::"r"(bar), "h"((uint16_t)3) : "memory");
+}
+
+// --- block-scaled 4-bit matrix instructions ---
+// Instruction descriptor of kind::mxf4: fp32 accumulator, E2M1 operands, K-major,
+// UE8M0 scales, 64 k.  Which two of a column's four scale bytes an instruction
+// takes stands in bits 4 and 29 (0: the first two, 2: the last two).
+__host__ __device__ constexpr uint32_t instr_desc_mx(uint32_t m, uint32_t n) {
+  return (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (1u << 23) | ((m >> 4) << 24);
+}
+// Shared-memory descriptor of a tile of scales: 32 lanes of 16 bytes, no swizzle,
+// 128 bytes from one group of 8 lanes to the next.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(128u >> 4) << 16) | ((uint64_t)(128u >> 4) << 32) |
+         (1ull << 46);
+}
+// A stage's scales into tensor memory on both CTAs of the pair, each from its
+// own shared memory, by a whole warp: two tiles of A's 128 rows, one for each 128
+// k, into columns [to, to + 4) and [to + 4, to + 8), and as many for every 128
+// columns of the product into [to + 8, to + 16) and [to + 16, to + 24).  In
+// shared memory the tiles of 128 k follow one another, those of the next 128
+// columns come after.  `second_k`: the stage has more than 128 k; `second_n`: the
+// product has more than 128 columns.
+__device__ __forceinline__ void load_scales(uint32_t to, uint64_t a, uint64_t b, uint32_t second_k,
+                                            uint32_t second_n) {
+  asm volatile("{\n\t.reg .pred e, ek, en, ekn;\n\t"
+               ".reg .b32 t;\n\t"
+               ".reg .b64 s;\n\t"
+               "elect.sync _|e, 0xFFFFFFFF;\n\t"
+               "setp.ne.and.u32 ek, %3, 0, e;\n\t"
+               "setp.ne.and.u32 en, %4, 0, e;\n\t"
+               "setp.ne.and.u32 ekn, %4, 0, ek;\n\t"
+               "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t"
+               "add.u32 t, %0, 8;\n\t"
+               "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t], %2;\n\t"
+               "add.u32 t, %0, 12;\n\tadd.s64 s, %2, 64;\n\t"
+               "@en tcgen05.cp.cta_group::2.32x128b.warpx4 [t], s;\n\t"
+               "add.u32 t, %0, 4;\n\tadd.s64 s, %1, 32;\n\t"
+               "@ek tcgen05.cp.cta_group::2.32x128b.warpx4 [t], s;\n\t"
+               "add.u32 t, %0, 16;\n\tadd.s64 s, %2, 32;\n\t"
+               "@ek tcgen05.cp.cta_group::2.32x128b.warpx4 [t], s;\n\t"
+               "add.u32 t, %0, 20;\n\tadd.s64 s, %2, 96;\n\t"
+               "@ekn tcgen05.cp.cta_group::2.32x128b.warpx4 [t], s;\n\t}"
+               ::"r"(to), "l"(a), "l"(b), "r"(second_k), "r"(second_n) : "memory");
+}
+// mma_stage for kind::mxf4, after load_scales(scales, ...): `steps` (1 to 4) times
+// 64 k.
+__device__ __forceinline__ Asked mma_stage_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                              uint32_t scales, uint32_t accumulate, uint32_t steps,
+                                              uint32_t done, uint32_t bar0, uint32_t p0, uint32_t bar1,
+                                              uint32_t p1) {
+  Asked r;
+  asm volatile("{\n\t.reg .pred e, e1, e2, e3, c, q0, q1;\n\t"
+               ".reg .b64 a1, b1, a2, b2, a3, b3;\n\t"
+               ".reg .b32 odd, sb, sa1, sb1;\n\t"
+               "elect.sync _|e, 0xFFFFFFFF;\n\t"
+               "setp.ne.u32 c, %7, 0;\n\t"
+               "setp.gt.and.u32 e1, %8, 1, e;\n\t"
+               "setp.gt.and.u32 e2, %8, 2, e;\n\t"
+               "setp.gt.and.u32 e3, %8, 3, e;\n\t"
+               "or.b32 odd, %5, 0x40000020;\n\t"
+               "add.u32 sb, %6, 8;\n\tadd.u32 sa1, %6, 4;\n\tadd.u32 sb1, %6, 16;\n\t"
+               "add.s64 a1, %3, 2;\n\tadd.s64 b1, %4, 2;\n\t"
+               "add.s64 a2, %3, 4;\n\tadd.s64 b2, %4, 4;\n\t"
+               "add.s64 a3, %3, 6;\n\tadd.s64 b3, %4, 6;\n\t"
+               "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%2], %3, %4, %5, [%6], [sb], c;\n\t"
+               "mbarrier.test_wait.parity.shared::cta.b64 q0, [%10], %11;\n\t"
+               "mbarrier.test_wait.parity.shared::cta.b64 q1, [%12], %13;\n\t"
+               "@e1 tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%2], a1, b1, odd, [%6], [sb], 1;\n\t"
+               "@e2 tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%2], a2, b2, %5, [sa1], [sb1], 1;\n\t"
+               "@e3 tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%2], a3, b3, odd, [sa1], [sb1], 1;\n\t"
+               "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+               "[%9], %14;\n\t"
+               "selp.u32 %0, 1, 0, q0;\n\t"
+               "selp.u32 %1, 1, 0, q1;\n\t}"
+               : "=r"(r.first), "=r"(r.second)
+               : "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(scales), "r"(accumulate), "r"(steps), "r"(done),
+                 "r"(bar0), "r"(p0), "r"(bar1), "r"(p1), "h"((uint16_t)3)
+               : "memory");
+  return r;
 }
 
 }  // namespace tc

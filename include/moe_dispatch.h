@@ -574,6 +574,38 @@ moe_status moe_dispatch_mxfp4(const moe_shape *shape, const void *x, const int32
                               const int32_t *slot_of, void *expert_x, void *expert_x_scale,
                               void *workspace, void *stream);
 
+/* The experts' gated feed-forward of moe_ffn on MXFP4 operands: for expert e
+ * and row s < clamp(expert_num_tokens[e], 0, cap),
+ *   h = x Wgu^T,  a = SiLU(gate) * up  (from h in binary32),  a4 = MXFP4(a),
+ *   y = a4 Wd^T.
+ * One launch on the tensor cores' block-scaled 4-bit instructions; sums in
+ * binary32; a is quantised from its binary32 values, y rounded once to bf16.
+ * For serving: the weights are quantised once by moe_quant_mxfp4 and then read
+ * at 17/32 of a byte per element, 3.8 times less than moe_ffn's.
+ * In:   expert_x, expert_x_scale (from moe_dispatch_mxfp4 or moe_quant_mxfp4);
+ *       w_gate_up [E, 2*intermediate, H] with MOE_MXFP4_GATE_UP and w_down
+ *       [E, H, intermediate], each with its scales; expert_num_tokens [E] int32
+ *       (from moe_plan), or NULL: every expert has cap rows.  Rows from the
+ *       count on and their scales may hold anything.
+ * Out:  expert_act [E, cap, intermediate] MXFP4, and expert_act_scale, always
+ *       written (y is computed from it); expert_y [E, cap, H] bf16.  Rows below
+ *       the count only; other rows, and their scales, are not touched.
+ * Work: as moe_ffn, of moe_ffn_mxfp4_workspace_size(shape, intermediate) bytes;
+ *       one workspace serves moe_plan, moe_ffn, moe_ffn_backward and this call
+ *       in turn, and a TIMEOUT of one of the three stops all of them until
+ *       moe_workspace_init.
+ * Limits: payload BF16; H % 32 == 0, intermediate % 32 == 0; intermediate
+ *       < 2^29, H < 2^30; E * cap * 2 * intermediate and E * cap * H < 2^46;
+ *       4 * intermediate * H < 2^40.  All arrays 16-byte aligned, the counts
+ *       4-byte.  No output may overlap an input.
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA. */
+size_t moe_ffn_mxfp4_workspace_size(const moe_shape *shape, int32_t intermediate);
+moe_status moe_ffn_mxfp4(const moe_shape *shape, int32_t intermediate, const void *expert_x,
+                         const void *expert_x_scale, const void *w_gate_up,
+                         const void *w_gate_up_scale, const void *w_down, const void *w_down_scale,
+                         const int32_t *expert_num_tokens, void *expert_act, void *expert_act_scale,
+                         void *expert_y, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Synchronise `stream` and read the workspace status word into *out (MOE_OK
  * or a device error).  The only call that waits for the device; meant for
  * tests and error handling, not for the hot path.
