@@ -34,7 +34,7 @@
 // before the current one is computed.  Each block's scale
 // and reciprocal are computed once, by the lane that stores the scale, and
 // handed to the half-warp that quantises the block by shuffle.
-#include "moe_common.cuh"
+#include "moe_rows.cuh"
 
 namespace moe {
 
@@ -80,53 +80,6 @@ __device__ __forceinline__ void silu8_table(const uint4 &g, const float *s_tab, 
     sv[2 * i] = *reinterpret_cast<const float *>(tab + o0);
     sv[2 * i + 1] = *reinterpret_cast<const float *>(tab + o1);
   }
-}
-
-
-// Exclusive prefix of clamp(count[e], 0, cap) over e into out[0..E], by the
-// whole block (any E).
-__device__ void count_prefix(const int32_t *count, int E, int cap, int32_t *out) {
-  __shared__ int32_t s_warp[kActThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (E + kActThreads - 1) / kActThreads;     // consecutive entries per thread
-  const int e0 = tid * per;
-  int local = 0;
-  for (int i = 0; i < per; ++i) {
-    const int e = e0 + i;
-    if (e < E) local += min(max(__ldg(count + e), 0), cap);
-  }
-  int incl = local;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int v = __shfl_up_sync(kWarpAll, incl, off);
-    if (lane >= off) incl += v;
-  }
-  if (lane == 31) s_warp[warp] = incl;
-  __syncthreads();
-  int before = 0;
-  for (int w = 0; w < warp; ++w) before += s_warp[w];
-  int run = before + incl - local;
-  for (int i = 0; i < per; ++i) {
-    const int e = e0 + i;
-    if (e < E) {
-      out[e] = run;
-      run += min(max(__ldg(count + e), 0), cap);
-    }
-  }
-  if (tid == kActThreads - 1) out[E] = run;
-  __syncthreads();
-}
-
-// The expert whose populated rows hold row number rg: the last e with
-// prefix[e] <= rg.
-__device__ __forceinline__ int populated_expert(const int32_t *s_prefix, int E, int rg) {
-  int lo = 0, hi = E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (s_prefix[mid] <= rg) lo = mid;
-    else hi = mid;
-  }
-  return lo;
 }
 
 // The 2P blocks of task (row, seg): lane (half, sub) loads elements
@@ -252,7 +205,7 @@ silu_quant_kernel(ActParams p) {
     reinterpret_cast<uint4 *>(s_tab)[i] = __ldg(reinterpret_cast<const uint4 *>(g_silu_table) + i);
   pdl_wait_for_previous();
   if (threadIdx.x == 0) s_status = read_status(p.hdr);
-  count_prefix(p.expert_num_tokens, p.E, p.cap, s_prefix);   // ends with __syncthreads
+  count_prefix<kActThreads>(p.expert_num_tokens, p.E, p.cap, s_prefix);   // ends with __syncthreads
   if (s_status != MOE_OK) return;
 
   const int lane = threadIdx.x & 31;

@@ -609,7 +609,8 @@ static moe_status mxfp4_check(int32_t E, int32_t rows, int32_t cols, const void 
       (flags != 0u && (counts || rows % 2 != 0)))
     return MOE_ERR_INVALID_ARG;
   const int64_t all = (int64_t)E * rows;
-  if (cols % 32 != 0 || all >= ((int64_t)1 << 31) || all >= ((int64_t)1 << 46) / cols)
+  if (cols % 32 != 0 || all >= ((int64_t)1 << 31) || all >= ((int64_t)1 << 46) / cols ||
+      (counts && E > kMaxExperts))
     return MOE_ERR_UNSUPPORTED;
   if (!wide || !q || !scale) return MOE_ERR_INVALID_ARG;
   if (!aligned(wide, 16) || !aligned(q, 16) || !aligned(scale, 16) || !aligned(counts, 4) ||

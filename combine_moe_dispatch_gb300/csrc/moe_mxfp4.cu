@@ -10,18 +10,25 @@
 // block's largest magnitude, found on the bf16 bit patterns as integers (an
 // infinity or a NaN is above every number there, and makes the block NaN).
 //
-// How: bound by memory.  A warp takes a segment of a row, U chunks of 32 x 16
-// bytes, 4 lanes to a block: the maximum is two shuffles, a lane's 8 elements
-// are 4 bytes, a half-warp's 4 scale bytes one word.  The dispatch reads a
-// token once and writes the bytes and scales to its K rows.  Rows from an
-// expert's count on are not touched.
+// How: bound by memory.  A lane takes a whole block: 64 bytes of bf16 as two
+// 32-byte accesses (four of 16 where the array is not aligned to 32), 16 bytes of
+// codes, no exchange for the maximum; four neighbouring lanes join their scale
+// bytes into one word.  Lanes are dealt out over the rows' blocks, each row's
+// rounded up to whole words of 4, so that short rows fill the warps as long ones
+// do; a lane has UNROLL blocks in flight.  Where counts say which rows exist,
+// those are numbered through by a prefix sum in shared memory, so that empty
+// places cost nothing.  The dispatch reads a token's block once and writes its
+// bytes and scales to its K rows.
 #include "moe_mxfp4.cuh"
+#include "moe_rows.cuh"
 
 namespace moe {
 
 namespace {
 
 constexpr int kMxThreads = 256;
+constexpr int kUnroll = 2;
+constexpr int kRoutes = 4;     // of a token, loaded together
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -30,32 +37,76 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// A lane's 8 elements of a block that 4 lanes share -> their bytes and the
-// half-warp's word of 4 scales.  All 32 lanes call it.
+// A block's 64 bytes of bf16, WIDE: 32-byte aligned.
+template <bool WIDE>
+__device__ __forceinline__ void load_block(const uint16_t *p, uint32_t (&w)[16]) {
+  if (WIDE) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("ld.global.cs.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[8 * i]), "=r"(w[8 * i + 1]), "=r"(w[8 * i + 2]), "=r"(w[8 * i + 3]),
+                     "=r"(w[8 * i + 4]), "=r"(w[8 * i + 5]), "=r"(w[8 * i + 6]), "=r"(w[8 * i + 7])
+                   : "l"(p + 16 * i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
+    }
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store_block(uint16_t *p, const uint32_t (&w)[16]) {
+  if (WIDE) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("st.global.cs.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(w[8 * i]),
+                   "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]), "r"(w[8 * i + 4]),
+                   "r"(w[8 * i + 5]), "r"(w[8 * i + 6]), "r"(w[8 * i + 7]), "l"(p + 16 * i)
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      __stcs(reinterpret_cast<uint4 *>(p) + i,
+             make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+  }
+}
+
+// A block -> its codes, and the word of scales of its 4 lanes.  All 32 lanes
+// call it.
 struct Quantised {
-  uint32_t q, scales;
+  uint4 q;
+  uint32_t scales;
 };
-__device__ __forceinline__ Quantised quantise8(const uint4 &v) {
+__device__ __forceinline__ Quantised quantise(const uint32_t (&w)[16]) {
   constexpr uint32_t kMag = 0x7FFF7FFFu;
-  uint32_t m = max_u16x2(max_u16x2(v.x & kMag, v.y & kMag), max_u16x2(v.z & kMag, v.w & kMag));
-  m = max_u16x2(m, __shfl_xor_sync(kFull, m, 1));
-  m = max_u16x2(m, __shfl_xor_sync(kFull, m, 2));
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max_u16x2(m, w[i] & kMag);
   const uint32_t byte = mx_scale(max(m & 0xFFFFu, m >> 16) >> 7);
   const float inv = mx_inverse(byte);
   // a NaN times 0 would still be a NaN: such a block's elements become 0 here
   const uint32_t keep = byte == 255u ? 0u : 0xFFFFFFFFu;
-  const uint32_t w[4] = {v.x & keep, v.y & keep, v.z & keep, v.w & keep};
-  float f[8];
+  uint32_t q[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(w[i]) * inv;
-    f[2 * i + 1] = bf16_hi(w[i]) * inv;
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t v = w[4 * i + k] & keep;
+      f[2 * k] = bf16_lo(v) * inv;
+      f[2 * k + 1] = bf16_hi(v) * inv;
+    }
+    q[i] = e2m1x8(f);
   }
   Quantised r;
-  r.q = e2m1x8(f);
-  uint32_t s = byte << (8 * ((threadIdx.x >> 2) & 3));
-  s |= __shfl_xor_sync(kFull, s, 4);
-  s |= __shfl_xor_sync(kFull, s, 8);
+  r.q = make_uint4(q[0], q[1], q[2], q[3]);
+  uint32_t s = byte << (8 * (threadIdx.x & 3));
+  s |= __shfl_xor_sync(kFull, s, 1);
+  s |= __shfl_xor_sync(kFull, s, 2);
   r.scales = s;
   return r;
 }
@@ -63,205 +114,218 @@ __device__ __forceinline__ Quantised quantise8(const uint4 &v) {
 __device__ __forceinline__ bool plan_failed(const WsHeader *hdr) {
   return hdr && read_status(hdr) != MOE_OK;
 }
-__device__ __forceinline__ int rows_below(const int32_t *counts, int e, int rows) {
-  return counts ? min(max(__ldg(counts + e), 0), rows) : rows;
-}
 
-// Walks (expert, row, segment) with a constant stride without divisions.
-struct RowCursor {
-  int e, row, seg;
-  int de, drow, dseg;
-  __device__ __forceinline__ RowCursor(int64_t task, int64_t stride, int rows, int segs) {
-    const int64_t r = task / segs, dr = stride / segs;
-    seg = (int)(task - r * segs);
-    dseg = (int)(stride - dr * segs);
-    e = (int)(r / rows);
-    row = (int)(r - (int64_t)e * rows);
-    de = (int)(dr / rows);
-    drow = (int)(dr - (int64_t)de * rows);
-  }
-  __device__ __forceinline__ void next(int rows, int segs) {
-    seg += dseg;
-    if (seg >= segs) {
-      seg -= segs;
-      ++row;
-    }
-    row += drow;
-    e += de;
-    if (row >= rows) {
-      row -= rows;
-      ++e;
+// A lane's place among the rows' blocks, `nbp` to a row, and how it moves on by
+// the grid's lanes.
+struct Place {
+  int64_t row;
+  int b;
+};
+struct Steps {
+  int64_t rows;
+  int blocks, nbp;
+  __device__ __forceinline__ Steps(int64_t lanes, int nbp_)
+      : rows(lanes / nbp_), blocks((int)(lanes % nbp_)), nbp(nbp_) {}
+  __device__ __forceinline__ void next(Place &p) const {
+    p.row += rows;
+    p.b += blocks;
+    if (p.b >= nbp) {
+      p.b -= nbp;
+      ++p.row;
     }
   }
 };
+__device__ __forceinline__ Place first_place(int nbp) {
+  const int64_t at = (int64_t)blockIdx.x * kMxThreads + threadIdx.x;
+  return Place{at / nbp, (int)(at % nbp)};
+}
+__device__ __forceinline__ int64_t grid_lanes() { return (int64_t)gridDim.x * kMxThreads; }
 
-template <int U>
+// Calls body(places, exists, experts, rows) for UNROLL places of every lane at a
+// time until the warp has none left: rows of the experts' buffers, the populated
+// ones alone with counts.
+template <bool COUNTED, typename Body>
+__device__ __forceinline__ void for_rows(const Mxfp4Rows &m, const int32_t *counts, int E, const Body &body) {
+  __shared__ int32_t s_prefix[COUNTED ? kMaxExperts + 1 : 1];
+  if (COUNTED) count_prefix<kMxThreads>(counts, E, m.rows, s_prefix);
+  const int64_t total = COUNTED ? s_prefix[E] : (int64_t)E * m.rows;
+  const int nb = m.cols / 32, nbp = (nb + 3) & ~3;
+  const Steps steps(grid_lanes(), nbp);
+  Place p = first_place(nbp);
+  while (__any_sync(kFull, p.row < total)) {
+    int e[kUnroll], row[kUnroll], b[kUnroll];
+    bool in[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      in[u] = p.row < total;
+      const int r = in[u] ? (int)p.row : 0;
+      b[u] = p.b;
+      e[u] = COUNTED ? populated_expert(s_prefix, E, r) : (int)((unsigned)r / (unsigned)m.rows);
+      row[u] = r - (COUNTED ? s_prefix[e[u]] : e[u] * m.rows);
+      steps.next(p);
+    }
+    body(e, row, b, in, nb);
+  }
+}
+
+template <bool COUNTED, bool WIDE>
 __global__ void __launch_bounds__(kMxThreads)
 quant_kernel(QuantParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warp0 = ((int64_t)blockIdx.x * kMxThreads + threadIdx.x) >> 5;
-  const int64_t nwarps = ((int64_t)gridDim.x * kMxThreads) >> 5;
-  const Mxfp4Rows &m = p.out;
-  const int cpr = m.cols / 8, segs = (cpr + 32 * U - 1) / (32 * U);
   pdl_wait_for_previous();
   if (plan_failed(p.hdr)) return;
-  RowCursor c(warp0, nwarps, m.rows, segs);
-  for (; c.e < p.E; c.next(m.rows, segs)) {
-    if (c.row >= rows_below(p.counts, c.e, m.rows)) continue;
-    const int64_t row = (int64_t)c.e * m.rows + c.row;
-    const uint4 *src = reinterpret_cast<const uint4 *>(p.src) + row * cpr;
-    const int c0 = c.seg * 32 * U + lane;
-    uint4 v[U];
+  const Mxfp4Rows &m = p.out;
+  for_rows<COUNTED>(m, p.counts, p.E, [&](const int (&e)[kUnroll], const int (&row)[kUnroll],
+                                          const int (&b)[kUnroll], const bool (&in)[kUnroll], int nb) {
+    uint32_t w[kUnroll][16];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      v[u] = c0 + 32 * u < cpr ? __ldcs(src + c0 + 32 * u) : make_uint4(0, 0, 0, 0);
-    uint32_t *q = reinterpret_cast<uint32_t *>(m.q) + row * cpr;
-    uint8_t *tiles = m.scale + expert_tiles(m, c.e);
+    for (int u = 0; u < kUnroll; ++u) {
+      if (in[u] && b[u] < nb) {
+        load_block<WIDE>(p.src + ((int64_t)e[u] * m.rows + row[u]) * m.cols + b[u] * 32, w[u]);
+      } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const Quantised r = quantise8(v[u]);
-      const int at = c0 + 32 * u;
-      if (at < cpr) q[at] = r.q;
-      if ((lane & 15) == 0 && at < cpr)
-        *reinterpret_cast<uint32_t *>(tiles + scale_word(m, c.row, at >> 4)) = r.scales;
+        for (int i = 0; i < 16; ++i) w[u][i] = 0u;
+      }
     }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const Quantised r = quantise(w[u]);
+      if (!in[u]) continue;
+      const int64_t at = ((int64_t)e[u] * m.rows + row[u]) * nb + b[u];
+      if (b[u] < nb) reinterpret_cast<uint4 *>(m.q)[at] = r.q;
+      if ((b[u] & 3) == 0)
+        *reinterpret_cast<uint32_t *>(m.scale + expert_tiles(m, e[u]) + scale_word(m, row[u], b[u] >> 2)) = r.scales;
+    }
+  });
+}
+
+// The 8 E2M1 of a word times x -> 8 bf16.  The products are exact in bf16: their
+// upper halves are the values.
+__device__ __forceinline__ void dequantise8(uint32_t q, float x, uint32_t (&o)[4]) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(q));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(lo), "=f"(hi) : "r"(h[i]));
+    o[i] = __byte_perm(__float_as_uint(lo * x), __float_as_uint(hi * x), 0x7632);
   }
 }
 
-// Two E2M1 of a byte -> floats.
-__device__ __forceinline__ float2 e2m1x2_to_float(uint32_t byte) {
-  uint32_t h;
-  asm("{\n\t.reg .b8 a;\n\tcvt.u8.u32 a, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(h) : "r"(byte));
-  float2 r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-      "cvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}" : "=f"(r.x), "=f"(r.y) : "r"(h));
-  return r;
-}
-
-template <int U>
+template <bool COUNTED, bool WIDE>
 __global__ void __launch_bounds__(kMxThreads)
 dequant_kernel(DequantParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warp0 = ((int64_t)blockIdx.x * kMxThreads + threadIdx.x) >> 5;
-  const int64_t nwarps = ((int64_t)gridDim.x * kMxThreads) >> 5;
-  const Mxfp4Rows &m = p.in;
-  const int cpr = m.cols / 8, segs = (cpr + 32 * U - 1) / (32 * U);
   pdl_wait_for_previous();
   if (plan_failed(p.hdr)) return;
-  RowCursor c(warp0, nwarps, m.rows, segs);
-  for (; c.e < p.E; c.next(m.rows, segs)) {
-    if (c.row >= rows_below(p.counts, c.e, m.rows)) continue;
-    const int64_t row = (int64_t)c.e * m.rows + c.row;
-    const uint32_t *q = reinterpret_cast<const uint32_t *>(m.q) + row * cpr;
-    const uint8_t *tiles = m.scale + expert_tiles(m, c.e);
-    const int c0 = c.seg * 32 * U + lane;
-    uint32_t v[U], s[U];
+  const Mxfp4Rows &m = p.in;
+  for_rows<COUNTED>(m, p.counts, p.E, [&](const int (&e)[kUnroll], const int (&row)[kUnroll],
+                                          const int (&b)[kUnroll], const bool (&in)[kUnroll], int nb) {
+    uint4 q[kUnroll];
+    uint32_t s[kUnroll];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = c0 + 32 * u;
-      const bool in = at < cpr;
-      v[u] = in ? __ldcs(q + at) : 0u;
-      s[u] = in ? __ldg(tiles + scale_word(m, c.row, at >> 4) + ((at >> 2) & 3)) : 0u;
+    for (int u = 0; u < kUnroll; ++u) {
+      const bool is = in[u] && b[u] < nb;
+      const int64_t at = ((int64_t)e[u] * m.rows + row[u]) * nb + b[u];
+      q[u] = is ? __ldcs(reinterpret_cast<const uint4 *>(m.q) + at) : make_uint4(0, 0, 0, 0);
+      s[u] = is ? __ldg(m.scale + expert_tiles(m, e[u]) + scale_word(m, row[u], b[u] >> 2) + (b[u] & 3)) : 0u;
     }
-    uint4 *out = reinterpret_cast<uint4 *>(p.out) + row * cpr;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = c0 + 32 * u;
+    for (int u = 0; u < kUnroll; ++u) {
       const float x = s[u] == 255u ? __uint_as_float(0x7FC00000u)
                                    : __uint_as_float(s[u] ? s[u] << 23 : 1u << 22);
-      uint32_t o[4];
+      const uint32_t c[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+      uint32_t w[16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 f = e2m1x2_to_float((v[u] >> (8 * i)) & 0xFFu);
-        // exact in bf16: the upper halves are the values
-        o[i] = __byte_perm(__float_as_uint(f.x * x), __float_as_uint(f.y * x), 0x7632);
+        uint32_t o[4];
+        dequantise8(c[i], x, o);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[4 * i + k] = o[k];
       }
-      if (at < cpr) __stcs(out + at, make_uint4(o[0], o[1], o[2], o[3]));
+      if (in[u] && b[u] < nb)
+        store_block<WIDE>(p.out + ((int64_t)e[u] * m.rows + row[u]) * m.cols + b[u] * 32, w);
     }
-  }
+  });
 }
 
-template <int U>
+template <bool WIDE>
 __global__ void __launch_bounds__(kMxThreads)
 dispatch_mxfp4_kernel(DispatchMxfp4Params p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warp0 = ((int64_t)blockIdx.x * kMxThreads + threadIdx.x) >> 5;
-  const int64_t nwarps = ((int64_t)gridDim.x * kMxThreads) >> 5;
   const Mxfp4Rows &m = p.out;
-  const int cpr = m.cols / 8, segs = (cpr + 32 * U - 1) / (32 * U);
-  const int64_t ntasks = (int64_t)p.N * segs;
+  const int nb = m.cols / 32, nbp = (nb + 3) & ~3;
+  const Steps steps(grid_lanes(), nbp);
+  Place c = first_place(nbp);
   pdl_wait_for_previous();
   if (plan_failed(p.hdr)) return;
-  TaskCursor cur(warp0, nwarps, segs);
-  for (int64_t task = warp0; task < ntasks; task += nwarps, cur = cur.next()) {
-    const int64_t g = cur.g;
-    int e_l = -1, s_l = -1;
-    if (lane < p.K) {
-      e_l = __ldg(p.topk_idx + g * p.K + lane);
-      s_l = __ldg(p.slot_of + g * p.K + lane);
+  for (; __any_sync(kFull, c.row < p.N); steps.next(c)) {
+    const bool in = c.row < p.N;
+    const int64_t g = in ? c.row : 0;
+    uint32_t w[16];
+    if (in && c.b < nb) {
+      load_block<WIDE>(p.x + g * m.cols + c.b * 32, w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = 0u;
     }
-    const int c0 = cur.seg * 32 * U + lane;
-    uint4 v[U];
+    const Quantised r = quantise(w);
+    for (int k0 = 0; in && k0 < p.K; k0 += kRoutes) {
+      int e[kRoutes], s[kRoutes];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      v[u] = c0 + 32 * u < cpr ? __ldcs(reinterpret_cast<const uint4 *>(p.x) + g * cpr + c0 + 32 * u)
-                               : make_uint4(0, 0, 0, 0);
-    Quantised r[U];
+      for (int j = 0; j < kRoutes; ++j) {
+        const bool is = k0 + j < p.K;
+        e[j] = is ? __ldg(p.topk_idx + g * p.K + k0 + j) : -1;
+        s[j] = is ? __ldg(p.slot_of + g * p.K + k0 + j) : -1;
+      }
 #pragma unroll
-    for (int u = 0; u < U; ++u) r[u] = quantise8(v[u]);
-    const bool routed = lane < p.K && s_l != -1;
-    const bool e_ok = e_l >= 0 && e_l < p.E;
-    const bool ok = routed && e_ok && s_l >= 0 && s_l < m.rows;
-    if (cur.seg == 0 && routed && !ok) report_status(p.hdr, e_ok ? MOE_ERR_CAPACITY : MOE_ERR_BAD_EXPERT);
-    for (unsigned left = __ballot_sync(kFull, ok); left != 0; left &= left - 1) {
-      const int k = __ffs(left) - 1;
-      const int e = __shfl_sync(kFull, e_l, k), s = __shfl_sync(kFull, s_l, k);
-      uint32_t *q = reinterpret_cast<uint32_t *>(m.q) + ((int64_t)e * m.rows + s) * cpr;
-      uint8_t *tiles = m.scale + expert_tiles(m, e);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int at = c0 + 32 * u;
-        if (at < cpr) q[at] = r[u].q;
-        if ((lane & 15) == 0 && at < cpr)
-          *reinterpret_cast<uint32_t *>(tiles + scale_word(m, s, at >> 4)) = r[u].scales;
+      for (int j = 0; j < kRoutes; ++j) {
+        if (s[j] == -1) continue;            // not routed
+        const bool e_ok = e[j] >= 0 && e[j] < p.E;
+        if (!e_ok || s[j] < 0 || s[j] >= m.rows) {
+          if (c.b == 0) report_status(p.hdr, e_ok ? MOE_ERR_CAPACITY : MOE_ERR_BAD_EXPERT);
+          continue;
+        }
+        if (c.b < nb) reinterpret_cast<uint4 *>(m.q)[((int64_t)e[j] * m.rows + s[j]) * nb + c.b] = r.q;
+        if ((c.b & 3) == 0)
+          *reinterpret_cast<uint32_t *>(m.scale + expert_tiles(m, e[j]) + scale_word(m, s[j], c.b >> 2)) = r.scales;
       }
     }
   }
 }
 
-// Chunks per lane: as many as the row has, 4 at most.
-int chunks(int cols) {
-  const int w = (cols / 8 + 31) / 32;
-  return w >= 4 ? 4 : w >= 2 ? 2 : 1;
-}
-
+// `rows` rows of m.cols elements, `unroll` blocks of a lane at a time.
 template <typename P>
-cudaError_t launch_rows(void (*kern)(P), int64_t rows, int cols, int U, const P &p, cudaStream_t stream) {
-  const int64_t tasks = rows * ((cols / 8 + 32 * U - 1) / (32 * U));
-  return launch_after_previous(kern, persistent_grid((const void *)kern, kMxThreads, tasks), kMxThreads, p,
+cudaError_t launch(void (*kern)(P), int64_t rows, int cols, int unroll, const P &p, cudaStream_t stream) {
+  const int64_t lanes = rows * ((cols / 32 + 3) & ~3);
+  const int64_t warps = (lanes + 32 * unroll - 1) / (32 * unroll);
+  return launch_after_previous(kern, persistent_grid((const void *)kern, kMxThreads, warps), kMxThreads, p,
                                stream);
 }
+bool wide(const void *p) { return (uintptr_t)p % 32 == 0; }
 
 }  // namespace
 
 cudaError_t launch_quant_mxfp4(const QuantParams &p, cudaStream_t stream) {
-  const int64_t rows = (int64_t)p.E * p.out.rows;
-  const int U = chunks(p.out.cols);
-  const auto kern = U == 4 ? quant_kernel<4> : U == 2 ? quant_kernel<2> : quant_kernel<1>;
-  return launch_rows(kern, rows, p.out.cols, U, p, stream);
+  const auto kern = p.counts ? (wide(p.src) ? quant_kernel<true, true> : quant_kernel<true, false>)
+                             : (wide(p.src) ? quant_kernel<false, true> : quant_kernel<false, false>);
+  return launch(kern, (int64_t)p.E * p.out.rows, p.out.cols, kUnroll, p, stream);
 }
 
 cudaError_t launch_dequant_mxfp4(const DequantParams &p, cudaStream_t stream) {
-  const int64_t rows = (int64_t)p.E * p.in.rows;
-  const int U = chunks(p.in.cols);
-  const auto kern = U == 4 ? dequant_kernel<4> : U == 2 ? dequant_kernel<2> : dequant_kernel<1>;
-  return launch_rows(kern, rows, p.in.cols, U, p, stream);
+  const auto kern = p.counts ? (wide(p.out) ? dequant_kernel<true, true> : dequant_kernel<true, false>)
+                             : (wide(p.out) ? dequant_kernel<false, true> : dequant_kernel<false, false>);
+  return launch(kern, (int64_t)p.E * p.in.rows, p.in.cols, kUnroll, p, stream);
 }
 
 cudaError_t launch_dispatch_mxfp4(const DispatchMxfp4Params &p, cudaStream_t stream) {
-  const int U = chunks(p.out.cols);
-  const auto kern = U == 4 ? dispatch_mxfp4_kernel<4> : U == 2 ? dispatch_mxfp4_kernel<2> : dispatch_mxfp4_kernel<1>;
-  return launch_rows(kern, p.N, p.out.cols, U, p, stream);
+  const auto kern = wide(p.x) ? dispatch_mxfp4_kernel<true> : dispatch_mxfp4_kernel<false>;
+  return launch(kern, p.N, p.out.cols, 1, p, stream);
 }
 
 }  // namespace moe

@@ -547,8 +547,8 @@ size_t moe_mxfp4_scale_bytes(int32_t num_experts, int32_t rows, int32_t cols);
  * Out:  q, scale as above.
  * Work: the workspace of the plan that produced the counts, or NULL: nothing is
  *       written if its status word is set.
- * Limits: cols % 32 == 0; E * rows < 2^31; E * rows * cols < 2^46.  src, q and
- *       scale 16-byte aligned.  MOE_MXFP4_GATE_UP: rows even, no counts.
+ * Limits: cols % 32 == 0; E * rows < 2^31; E * rows * cols < 2^46; with counts
+ *       E <= 2048.  src, q and scale 16-byte aligned.  MOE_MXFP4_GATE_UP: rows even, no counts.
  * Errors: INVALID_ARG (null pointer, size not positive, unknown flag, odd rows
  *       or counts with GATE_UP), UNSUPPORTED, ALIGNMENT, CUDA. */
 moe_status moe_quant_mxfp4(int32_t num_experts, int32_t rows, int32_t cols, const void *src,

@@ -102,6 +102,36 @@ def test_every_bf16_number():
     _check(src, q, scale, _below(1, src.shape[1], None))
 
 
+def test_unaligned_arrays():
+    """bf16 arrays at 16 bytes past a boundary of 32, on both sides."""
+    import combine_moe_dispatch_gb300 as moe
+    for counted in (False, True):
+        flat = torch.full((8 + 3 * 40 * 288 + 8,), -7.0, dtype=torch.bfloat16, device="cuda")
+        src = flat[8:-8].view(3, 40, 288)
+        src.copy_(_rows((3, 40, 288), 12))
+        counts = torch.tensor([40, 0, 33], dtype=torch.int32, device="cuda") if counted else None
+        below = _below(3, 40, counts)
+        q, scale = _call(src, counts)
+        _check(src, q, scale, below)
+        want = torch.where(below[..., None], ref.values(*ref.quantise(src)), src.double())
+        moe.dequant_mxfp4(q, scale, counts, src)
+        assert torch.equal(src.double(), want)
+        assert bool((flat[:8] == -7.0).all()) and bool((flat[-8:] == -7.0).all())
+
+
+def test_most_experts():
+    """2048 experts with counts, most of them empty; more without."""
+    counts = torch.zeros(2048, dtype=torch.int32, device="cuda")
+    counts[::77] = 1
+    counts[2047] = 3
+    src = _rows((2048, 3, 160), 13)
+    q, scale = _call(src, counts)
+    _check(src, q, scale, _below(2048, 3, counts))
+    src = _rows((5000, 1, 64), 14)
+    q, scale = _call(src)
+    _check(src, q, scale, _below(5000, 1, None))
+
+
 def test_infinities_and_nan():
     import combine_moe_dispatch_gb300 as moe
     src = _rows((1, 6, 128), 4)
@@ -154,6 +184,17 @@ def _dispatch(R, T, H, E, K, cap, seed, masked=0.0, idx=None):
     q = torch.full((E, cap, H // 2), FILL, dtype=torch.uint8, device="cuda")
     scale = ref.scale_tensor(E, cap, H, FILL)
     return moe, shape, x, idx.contiguous(), b, q, scale
+
+
+def test_dispatch_of_an_unaligned_array():
+    moe, shape, x, idx, b, q, scale = _dispatch(1, 64, 288, 8, 2, 64, 15)
+    flat = torch.empty(8 + x.numel(), dtype=torch.bfloat16, device="cuda")
+    off = flat[8:].view_as(x)
+    off.copy_(x)
+    moe.dispatch_mxfp4(shape, off, idx, b.slot_of, q, scale, b.workspace)
+    q2, scale2 = torch.full_like(q, FILL), torch.full_like(scale, FILL)
+    moe.dispatch_mxfp4(shape, x, idx, b.slot_of, q2, scale2, b.workspace)
+    assert torch.equal(q, q2) and torch.equal(scale, scale2)
 
 
 @pytest.mark.parametrize("R,T,H,E,K,cap,masked", [

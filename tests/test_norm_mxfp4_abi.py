@@ -120,10 +120,13 @@ def test_quantisation_arguments(lib, name):
         assert call(**{size: 0}) == Status.INVALID_ARG
         assert call(**{size: -32}) == Status.INVALID_ARG
     assert call(cols=48) == Status.UNSUPPORTED
-    assert call(E=1 << 16, rows=1 << 15, src=None) == Status.UNSUPPORTED                  # 2^31 rows
-    assert call(E=1 << 16, rows=(1 << 15) - 1, src=None) == Status.INVALID_ARG
-    assert call(E=1 << 15, rows=1 << 15, cols=1 << 16, src=None) == Status.UNSUPPORTED    # 2^46
-    assert call(E=1 << 15, rows=1 << 15, cols=(1 << 16) - 32, src=None) == Status.INVALID_ARG
+    assert call(E=1 << 16, rows=1 << 15, src=None, counts=None) == Status.UNSUPPORTED                  # 2^31 rows
+    assert call(E=1 << 16, rows=(1 << 15) - 1, src=None, counts=None) == Status.INVALID_ARG
+    assert call(E=1 << 15, rows=1 << 15, cols=1 << 16, src=None, counts=None) == Status.UNSUPPORTED    # 2^46
+    assert call(E=1 << 15, rows=1 << 15, cols=(1 << 16) - 32, src=None, counts=None) == Status.INVALID_ARG
+    assert call(E=2049, src=None) == Status.UNSUPPORTED                                    # with counts
+    assert call(E=2049, counts=None, src=None) == Status.INVALID_ARG
+    assert call(E=2048, src=None) == Status.INVALID_ARG
     # the gate and up layout: whole arrays of an even number of rows
     assert call(flags=2) == Status.INVALID_ARG
     assert call(flags=1) == Status.INVALID_ARG                                             # with counts
