@@ -11,13 +11,13 @@
 // stages filled by TMA, tcgen05.mma.cta_group::2, accumulators in tensor memory
 // two tiles deep, eight epilogue warps.  What 4 bits change:
 //  - A stage is 256 k (128 bytes of a row, as 64 k of bf16 are): 16 KB of weights
-//    per CTA, up to 16 KB of tokens, 1 KB of the weights' scales and up to 2 KB of
+//    per CTA, up to 16 KB of tokens, 1 KB of the weights' scales and up to 3 KB of
 //    the tokens'.  The scales stand in memory in the tiles that a copy into tensor
 //    memory takes (tcgen05.cp), so that they come by TMA and go on without passing
 //    through registers.  Both CTAs need the scales of all the tile's tokens.
 //  - Gate and up of the same 64 features are the two halves of a CTA's 128 rows;
 //    their scales lie so in memory (MOE_MXFP4_GATE_UP).
-//  - Scales take 24 columns of tensor memory, which leaves 480 for two
+//  - Scales take 32 columns of tensor memory, which leaves 480 for two
 //    accumulators of 256: they overlap by 32 columns.  The epilogue reads those
 //    first, and the next tile starts when it has.  Tiles of up to 224 columns do
 //    not overlap.
@@ -35,14 +35,19 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 384;          // warps: 0 TMA, 1 MMA, 2 none, 3 scheduling, 4-11 epilogue
+constexpr int kGroups = 2;             // of four epilogue warps; each takes every kGroups-th chunk of columns
+constexpr int kOutWarps = 4 * kGroups;
+constexpr int kThreads = 128 + 32 * kOutWarps;     // warps: 0 TMA, 1 MMA, 2 publishing, 3 scheduling, then the epilogue
 constexpr int kStages = 5;
 constexpr int kBlockK = 256;           // one 128-byte swizzled line of 4-bit elements
 constexpr uint32_t kHalfBytes = 128 * 128;               // a CTA's half of one operand: 16 KB
 constexpr uint32_t kScaleOff = 2 * kHalfBytes;           // A's scales: 2 tiles, one for each 128 k
 constexpr uint32_t kScaleStage = 2 * kScaleTileBytes;
-constexpr uint32_t kStageBytes = kScaleOff + 3 * kScaleStage;   // and B's: 2 or 4 tiles
-constexpr uint32_t kStagingBytes = 2 * 16384;            // epilogue, one buffer per group
+constexpr uint32_t kStageBytes = kScaleOff + 4 * kScaleStage;   // and B's: 2, 4 or 6 tiles
+// Epilogue: 32 tokens of gate and up for each group, 128 features in a row, which
+// 16-byte reads of different tokens find in different banks.
+constexpr int kStagedRow = 132;
+constexpr uint32_t kStagingBytes = kGroups * 32 * kStagedRow * 4;
 constexpr uint32_t kBarOff = kStages * kStageBytes + kStagingBytes;
 constexpr uint32_t kRingOff = kBarOff + 256;
 constexpr uint32_t kSmem = kRingOff + kRing * 64 + 1024;        // + alignment slack
@@ -56,11 +61,14 @@ constexpr int kApart = kTileCols - kShared;                     // tiles of so m
 static_assert(kShared == 32, "the epilogue reads the shared columns as one chunk");
 
 // Words of a tile's record that the matrix instructions need.
-constexpr uint32_t kMxWords = kMathWords | kK0;
+constexpr uint32_t kMxWords = kMathWords | kN0 | kK0;
+
+// Row tiles of scales that a tile's columns lie in: its first is row 0 or 64 of one.
+__device__ __forceinline__ int scale_tiles(const Tile &t) { return ((t.n0 & 64) + t.n + 127) >> 7; }
 
 struct MxJob {
   CUtensorMap a, a_scale;
-  CUtensorMap b[4], b_scale[2];        // boxes of 16, 32, 64 and 128 tokens; of 128 and 256 tokens' scales
+  CUtensorMap b[4], b_scale[3];        // boxes of 16, 32, 64 and 128 tokens; of 1, 2 and 3 row tiles of scales
   uint8_t *q, *scale;                  // gate and up: a4
   uint16_t *out;                       // y
   int M, K, N;                         // features, contraction; N is not used
@@ -70,7 +78,7 @@ struct MxJob {
 
 struct MxParams {
   static constexpr int kKind = kForward, kBlock = kBlockK, kJobs = 2;
-  static constexpr bool kWholeTiles = true;
+  static constexpr int kTileStep = 64;   // block scales come 128 rows at a time, from row 0 or 64 on
   MxJob job[kJobs];                    // a, y
   const int32_t *counts;               // [E], or null (cap rows each)
   WsHeader *hdr;
@@ -94,26 +102,30 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
   const uint32_t tm_full = bars + 16 * kStages, tm_empty = tm_full + 16, tm_shared = tm_empty + 16;
   const uint32_t tm_slot = tm_shared + 16;
   constexpr uint32_t kSlotOff = kBarOff + 16 * kStages + 48, kLastOff = kSlotOff + 8;
-  static_assert(kLastOff + 4 <= kBarOff + 192, "the barriers fit");
-  // barriers of the ring of tiles
+  static_assert(kLastOff + 8 <= kBarOff + 144 && 144 + 8 * kRing <= 192, "the barriers fit");
+  // barriers of the ring of tiles: announced, read by all, results written
+  const uint32_t rec_done = bars + 144;
   const uint32_t rec_full = bars + 192, rec_empty = bars + 224;
   Tile *ring = reinterpret_cast<Tile *>(smem_p + kRingOff);
+  volatile uint32_t *gave_up = reinterpret_cast<uint32_t *>(smem_p + kLastOff + 4);
   volatile uint32_t *last_in = reinterpret_cast<uint32_t *>(smem_p + kLastOff);
 
   if (threadIdx.x == 0) {
+    *gave_up = 0u;
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init_at(full + 8 * s, 1);     // the leader's arrival, and the bytes of both CTAs
       tc::mbar_init_at(empty + 8 * s, 1);    // the commit of the stage's instructions
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init_at(tm_full + 8 * b, 1);
-      tc::mbar_init_at(tm_empty + 8 * b, 2 * kEpiWarps);   // the epilogue warps of both CTAs
-      tc::mbar_init_at(tm_shared + 8 * b, 2 * kEpiWarps);
+      tc::mbar_init_at(tm_empty + 8 * b, 2 * kOutWarps);   // the epilogue warps of both CTAs
+      tc::mbar_init_at(tm_shared + 8 * b, 2 * kOutWarps);
     }
     for (int r = 0; r < kRing; ++r) {
       tc::mbar_init_at(rec_full + 8 * r, 1);
-      // in the leader: TMA and epilogue of both CTAs, and the MMA warp
-      tc::mbar_init_at(rec_empty + 8 * r, 2 * (kEpiWarps + 1) + 1);
+      // in the leader: TMA, publishing and epilogue of both CTAs, and the MMA warp
+      tc::mbar_init_at(rec_empty + 8 * r, 2 * (kOutWarps + 2) + 1);
+      tc::mbar_init_at(rec_done + 8 * r, kOutWarps);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   } else if (threadIdx.x == 32) {
@@ -210,26 +222,41 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
       const MxJob &j = p.job[t.job];
       const uint32_t half_n = t.n >> 1;
       const int bsel = half_n <= 16 ? 0 : half_n <= 32 ? 1 : half_n <= 64 ? 2 : 3;
-      const int wide = t.n > 128;
-      const uint32_t bytes = kHalfBytes + (16u << bsel) * 128u + (2u + wide) * kScaleStage;
+      const int tiles = scale_tiles(t);
+      const uint32_t bytes = kHalfBytes + (16u << bsel) * 128u + (1u + tiles) * kScaleStage;
       const int n0 = t.n0 + (int)(rank * half_n), rt = t.m * 2 + (int)rank;
       // 64 gate rows and the same 64 features of up in one copy, or 128 features
       const int a0 = rt * (t.job == 0 ? 64 : 128);
-      if (t.need != 0 && !written) {
+      // The first tile of y takes its first stages' weights before it waits for all
+      // of a.
+      const int early = t.need != 0 && !written ? min(t.nk, kStages) : 0;
+      for (int kb = 0; ok && kb < early; ++kb) {
+        const int at = s + kb < kStages ? s + kb : s + kb - kStages;
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(empty + 8 * at, ph ^ (s + kb < kStages ? 1u : 0u), limit));
+        if (!ok) break;
+        const uint32_t sa = smem + at * kStageBytes;
+        if (rank == 0) tc::mbar_expect_warp(full + 8 * at, 2 * bytes);
+        tc::tma_load_pair(sa, &j.a, full0 + 8 * at, (t.k0 + kb) * 128, a0, 0, t.e);
+        tc::tma_load_pair(sa + kScaleOff, &j.a_scale, full0 + 8 * at, 0, 2 * (t.k0 + kb), rt, t.e);
+      }
+      if (!ok) break;
+      if (early > 0) {
         written = ok = __all_sync(0xFFFFFFFFu, wait_count(p.units->ready + t.epoch, (uint32_t)t.need, limit));
         if (!ok) break;
       }
       for (int kb = 0; kb < t.nk; ++kb) {
-        ok = __all_sync(0xFFFFFFFFu, wait_bar(empty + 8 * s, ph ^ 1u, limit));
-        if (!ok) break;
         const uint32_t sa = smem + s * kStageBytes;
         const int k = t.k0 + kb;
         const uint32_t bar = full0 + 8 * s;
-        if (rank == 0) tc::mbar_expect_warp(full + 8 * s, 2 * bytes);
-        tc::tma_load_pair(sa, &j.a, bar, k * 128, a0, 0, t.e);
+        if (kb >= early) {
+          ok = __all_sync(0xFFFFFFFFu, wait_bar(empty + 8 * s, ph ^ 1u, limit));
+          if (!ok) break;
+          if (rank == 0) tc::mbar_expect_warp(full + 8 * s, 2 * bytes);
+          tc::tma_load_pair(sa, &j.a, bar, k * 128, a0, 0, t.e);
+          tc::tma_load_pair(sa + kScaleOff, &j.a_scale, bar, 0, 2 * k, rt, t.e);
+        }
         tc::tma_load_pair(sa + kHalfBytes, &j.b[bsel], bar, k * 128, n0, 0, t.e);
-        tc::tma_load_pair(sa + kScaleOff, &j.a_scale, bar, 0, 2 * k, rt, t.e);
-        tc::tma_load_pair(sa + kScaleOff + kScaleStage, &j.b_scale[wide], bar, 0, 2 * k, t.n0 >> 7, t.e);
+        tc::tma_load_pair(sa + kScaleOff + kScaleStage, &j.b_scale[tiles - 1], bar, 0, 2 * k, t.n0 >> 7, t.e);
         if (++s == kStages) {
           s = 0;
           ph ^= 1u;
@@ -248,9 +275,14 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
     // ---- matrix instructions, one warp of the leading CTA.  What it needs
     // next (the next stage, tile and accumulator) is asked for while the
     // instructions of a stage run, so that the tensor cores have work meanwhile.
-    int s = 0;
-    uint32_t ph = 0, it = 0;
-    bool stage_ready = false, acc_ready = false;
+    // An answer takes about 200 cycles, more beside the epilogue's shared-memory
+    // traffic: it is looked at one stage later, and the stage that is asked for is
+    // the one after next (asked for the next and looked at at once, an iteration
+    // took longer than the stage's instructions).
+    int s = 0, s2 = 1;                       // this stage, the next one
+    uint32_t ph = 0, ph2 = 0, it = 0;
+    uint32_t ready = 0, ready_next = 0;      // answers: this stage, the next one
+    bool acc_ready = false;
     int before = 0;                          // columns of the tile before
     const uint64_t desc_a0 = tc::smem_desc(smem, 16u), desc_b0 = tc::smem_desc(smem + kHalfBytes, 16u);
     const uint64_t desc_sa0 = tc::scale_desc(smem + kScaleOff);
@@ -260,6 +292,7 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
       const uint32_t buf = it & 1u;
       const uint32_t d = tmem + (buf ? kAcc1 : kAcc0);
       const uint32_t idesc = tc::instr_desc_mx(256, t.n);
+      const uint32_t tiles = scale_tiles(t), skip = (uint32_t)(t.n0 & 64) >> 5;
       // 64 k an instruction; the row's end cuts the last block
       const int left = p.job[t.job].K - (t.k0 + t.nk - 1) * kBlockK;
       const uint32_t tail = left >= kBlockK ? 4u : (uint32_t)((left + 63) >> 6);
@@ -271,39 +304,46 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
         ok = __all_sync(0xFFFFFFFFu, wait_bar(tm_shared + 8 * (buf ^ 1u), ((it - 1) >> 1) & 1u, limit));
       before = t.n;
       tc::fence_after();
+      const uint32_t acc_bar = tm_empty + 8 * (buf ^ 1u), acc_parity = (((it + 1) >> 1) & 1u) ^ 1u;
       Feed::Raw next_raw;
       bool have = false;                     // the next tile's record is being read
+      uint32_t answer = 0;                   // to the last question: the record, or the accumulator
       for (int kb = 0; ok && kb < t.nk; ++kb) {
-        if (!stage_ready) {
+        if (!__all_sync(0xFFFFFFFFu, ready)) {
           ok = __all_sync(0xFFFFFFFFu, wait_bar(full + 8 * s, ph, limit));
           if (!ok) break;
         }
-        const bool last = kb == t.nk - 1;
-        const uint32_t steps = last ? tail : 4u;
+        if (__all_sync(0xFFFFFFFFu, answer)) {
+          if (have) {
+            acc_ready = true;
+          } else {
+            have = true;
+            next_raw = feed.read();
+          }
+        }
+        const uint32_t steps = kb == t.nk - 1 ? tail : 4u;
         tc::fence_after();
         const uint64_t at = (uint64_t)(s * (kStageBytes >> 4));
         const uint32_t stage = empty + 8 * s;
-        if (++s == kStages) {
-          s = 0;
-          ph ^= 1u;
+        s = s2;
+        ph = ph2;
+        if (++s2 == kStages) {
+          s2 = 0;
+          ph2 ^= 1u;
         }
-        // the last block asks for the next accumulator, the others for the next record
-        const uint32_t bar1 = last || have ? tm_empty + 8 * (buf ^ 1u) : feed.full + 8 * feed.s;
-        const uint32_t p1 = last || have ? (((it + 1) >> 1) & 1u) ^ 1u : feed.ph;
-        tc::load_scales(tmem, desc_sa0 + at, desc_sb0 + at, steps > 2, t.n > 128);
-        const tc::Asked r = tc::mma_stage_mx(d, desc_a0 + at, desc_b0 + at, idesc, tmem, kb > 0, steps, stage,
-                                             full + 8 * s, ph, bar1, p1);
-        stage_ready = __all_sync(0xFFFFFFFFu, r.first);
-        const bool second = __all_sync(0xFFFFFFFFu, r.second);
-        if (last) {
-          acc_ready = second;
-        } else if (!have && second) {
-          have = true;
-          next_raw = feed.read();
-        }
+        tc::load_scales(tmem, desc_sa0 + at, desc_sb0 + at, steps > 2, tiles);
+        const tc::Asked r = tc::mma_stage_mx(d, desc_a0 + at, desc_b0 + at, idesc, tmem, skip, kb > 0, steps, stage,
+                                             full + 8 * s2, ph2, have ? acc_bar : feed.full + 8 * feed.s,
+                                             have ? acc_parity : feed.ph);
+        ready = ready_next;
+        ready_next = r.first;
+        answer = r.second;
       }
       if (ok) tc::mma_commit_pair(tm_full + 8 * buf);
-      if (ok) more = have ? feed.spread<kMxWords>(next_raw, t) : feed.next_uniform<kMxWords>(t, ok);
+      if (ok) {
+        if (have) acc_ready = acc_ready || __all_sync(0xFFFFFFFFu, answer);
+        more = have ? feed.spread<kMxWords>(next_raw, t) : feed.next_uniform<kMxWords>(t, ok);
+      }
       ++it;
     }
     // the other CTA's arrivals for both accumulators land before this one may exit
@@ -312,68 +352,128 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
       ok = __all_sync(0xFFFFFFFFu, wait_bar(tm_empty + 8 * (it & 1u), parity, limit) &&
                                        wait_bar(tm_shared + 8 * (it & 1u), parity, limit));
     }
-  } else if (live && warp >= 4) {
-    // ---- epilogue: tensor memory -> registers -> shared memory -> results
-    uint32_t it = 0;
-    const int wq = warp & 3, grp = (warp - 4) >> 2, tid = (threadIdx.x - 128) & 127;
-    const uint32_t empty0 = tc::map_rank(tm_empty, 0), shared0 = tc::map_rank(tm_shared, 0);
-    float *const st = reinterpret_cast<float *>(smem_p + kStages * kStageBytes + grp * 16384);
-    // a thread's place in the staged chunk: 4 features of rows r8, r8 + 8, ...
-    const int i4 = tid & 15, r8 = tid >> 4;
+  } else if (live && warp == 2) {
+    // ---- publishing: says that half a tile of a is written, for copies of other
+    // CTAs to read, when all epilogue warps are done with it.  The fence waits for
+    // their stores: in the epilogue it delayed the next tile by 0.6 us.
     while (true) {
+      ok = __all_sync(0xFFFFFFFFu, wait_bar(rec_full + 8 * feed.s, feed.ph, limit));
+      if (!ok) break;
+      t = ring[feed.s];
+      __syncwarp();
+      if (!t.valid) break;
+      // (Such tiles come before all others: their places' phases are the ring's.)
+      if (t.job == 0 && t.split == 1) {
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(rec_done + 8 * feed.s, feed.ph, limit));
+        if (!ok) break;
+        tc::fence_async_global();
+        __threadfence();
+        if (lane == 0) atomicAdd(p.units->ready + t.epoch, 1u);
+      }
+      feed.leave();
+    }
+  } else if (live && warp >= 4) {
+    // ---- epilogue: tensor memory -> registers (a lane has one feature of 32
+    // tokens) -> results
+    uint32_t it = 0;
+    const int wq = warp & 3, grp = (warp - 4) >> 2;
+    const uint32_t empty0 = tc::map_rank(tm_empty, 0), shared0 = tc::map_rank(tm_shared, 0);
+    float *const staged = reinterpret_cast<float *>(smem_p + kStages * kStageBytes) + grp * 32 * kStagedRow;
+    while (true) {
+      const int slot = feed.s;
       const bool more = feed.next(t, ok);
       const uint32_t buf = it & 1u;
       const MxJob &j = p.job[t.job];
       const bool gate = t.job == 0;
       const int rt = t.m * 2 + (int)rank;
-      const int f0 = rt * (gate ? 64 : 128) + 4 * i4;
       const int64_t row0 = (int64_t)t.e * p.cap + t.n0;
-      // one token's 4 + 4 features: sums lo, hi -> results.  Whole half-warps
-      // have one token; all 32 lanes call it, `in`: the token exists.
-      const auto emit = [&](int tok, bool in, const float4 &lo4, const float4 &hi4) {
-        const int64_t row = row0 + tok;
-        if (gate) {                          // lo: gate, hi: up of the same features
-          const float lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
-          float a[4];
+      // 32 tokens' sums of this lane's feature, from column c on -> results.  The
+      // four warps of a group call it together.
+      const auto emit = [&](int c, const uint32_t (&v)[32]) {
+        if (gate) {
+          // Through shared memory, so that a lane gets 16 features of one token: half
+          // of a block, whose largest magnitude is then one exchange away.  (With a
+          // lane per feature and the maximum over the warp's lanes the chunk took
+          // twice as long.)
+          float *const own = staged + wq * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) own[i * kStagedRow] = __uint_as_float(v[i]);
+          named_sync(1 + grp, 128);
+          const int at = 16 * (wq >> 1) + (lane & 15), f = 32 * (wq & 1) + 16 * (lane >> 4);
+          const float4 *const in = reinterpret_cast<const float4 *>(staged + at * kStagedRow + f);
+          float a[16];
           uint32_t most = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            a[k] = lo[k] * sigmoid(lo[k]) * hi[k];
-            most = max(most, __float_as_uint(a[k]) & 0x7FFFFFFFu);
-          }
+          for (int i = 0; i < 4; ++i) {
+            const float4 g4 = in[i], u4 = in[16 + i];
+            const float g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
-          for (int d = 4; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+            for (int k = 0; k < 4; ++k) {
+              a[4 * i + k] = g[k] * sigmoid(g[k]) * u[k];
+              most = max(most, __float_as_uint(a[4 * i + k]) & 0x7FFFFFFFu);
+            }
+          }
+          named_sync(1 + grp, 128);          // all have read: the next chunk may be staged
+          most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
           const uint32_t byte = mx_scale(most >> 23);
           const float inv = mx_inverse(byte);
+          uint32_t code[2];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) a[k] = byte == 255u ? 0.0f : a[k] * inv;
-          // features past the last have a scale of 0 in the last tile of blocks
-          const uint32_t scale = f0 < j.M ? byte : 0u;
-          const uint32_t scale2 = scale | __shfl_down_sync(0xFFFFFFFFu, scale, 8) << 8;
-          if (in && f0 < j.M) {
-            *reinterpret_cast<uint16_t *>(j.q + (row * j.M + f0) / 2) = (uint16_t)e2m1x4(a);
+          for (int i = 0; i < 2; ++i) {
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = byte == 255u ? 0.0f : a[8 * i + k] * inv;
+            code[i] = e2m1x8(x);
           }
-          if (in && i4 == 0) {
-            const int r = t.n0 + tok;
-            const int64_t tile = ((int64_t)t.e * j.row_tiles + (r >> 7)) * j.block_tiles + t.m;
-            *reinterpret_cast<uint16_t *>(j.scale + tile * kScaleTileBytes + (r & 31) * 16 +
-                                          ((r >> 5) & 3) * 4 + 2 * rank) = (uint16_t)scale2;
+          const int tok = c + at, feature = rt * 64 + f;
+          if (tok < t.cols) {
+            if (feature < j.M)
+              *reinterpret_cast<uint2 *>(j.q + ((row0 + tok) * j.M + feature) / 2) = make_uint2(code[0], code[1]);
+            if (lane < 16) {
+              // features past the last have a scale of 0 in the last tile of blocks
+              const int r = t.n0 + tok;
+              const int64_t tile = ((int64_t)t.e * j.row_tiles + (r >> 7)) * j.block_tiles + t.m;
+              j.scale[tile * kScaleTileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4 + 2 * rank + (wq & 1)] =
+                  feature < j.M ? (uint8_t)byte : (uint8_t)0;
+            }
           }
-        } else if (in) {
-          const float lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
-          uint16_t *q = j.out + row * j.M + f0;
-          if (f0 < j.M) *reinterpret_cast<uint2 *>(q) = make_uint2(pack2(lo[0], lo[1]), pack2(lo[2], lo[3]));
-          if (f0 + 64 < j.M)
-            *reinterpret_cast<uint2 *>(q + 64) = make_uint2(pack2(hi[0], hi[1]), pack2(hi[2], hi[3]));
+        } else {
+          // two tokens in a word, then two features of one: even lanes the first
+          // token, odd ones the second
+          const int f = rt * 128 + wq * 32;
+          uint16_t *q = j.out + (row0 + c + (lane & 1)) * j.M + f + (lane & ~1);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const uint32_t w = pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
+            if (f < j.M && c + i + (lane & 1) < t.cols)
+              *reinterpret_cast<uint32_t *>(q + (int64_t)i * j.M) =
+                  (lane & 1) ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
+          }
         }
       };
       if (more) {
         ok = wait_bar(tm_full + 8 * buf, (it >> 1) & 1u, limit);
         tc::fence_after();
       }
-      // all the warps agree to go on, and are done with the staging buffers
-      ok = named_sync_and(3, 32 * kEpiWarps, ok);
-      if (!ok || !more) break;
+      // A group's warps agree to go on.  Both groups do where a tile is cut, which
+      // they finish together; one that has given up says so at that barrier.  (Both
+      // agreeing on every tile cost the batch's tiles 0.3 us each.)
+      ok = named_sync_and(1 + grp, 128, ok);
+      if (!ok) {
+        *gave_up = 1u;
+        __threadfence_block();
+        named_arrive(3, 32 * kOutWarps);
+        break;
+      }
+      if (!more) break;
+      if (t.split > 1) {
+        named_sync(3, 32 * kOutWarps);
+        if (*gave_up) {
+          ok = false;
+          break;
+        }
+      }
       const uint32_t src = tmem + ((uint32_t)(wq * 32) << 16) + (buf ? kAcc1 : kAcc0);
       const auto arrive = [&](uint32_t bar) {     // this warp has read its part of the columns
         tc::fence_before();
@@ -382,11 +482,11 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
       };
       // The group's chunks of 32 columns, those that the accumulators share first:
       // the first accumulator's last, the second's first.
-      const int chunks = (t.n - grp * 32 + 63) >> 6;       // t.n >= 32
-      const bool shares = buf ? grp == 0 : grp == 1 && t.n > kApart;
+      const int chunks = (t.n - grp * 32 + 32 * kGroups - 1) / (32 * kGroups);     // t.n >= 32
+      const bool shares = buf ? grp == 0 : grp == (kApart / 32) % kGroups && t.n > kApart;
       if (!shares) arrive(shared0);
       if (chunks <= 0) arrive(empty0);
-      const auto chunk = [&](int i) { return grp * 32 + 64 * (buf ? i : chunks - 1 - i); };
+      const auto chunk = [&](int i) { return grp * 32 + 32 * kGroups * (buf ? i : chunks - 1 - i); };
       const auto read = [&](int i, uint32_t (&v)[32]) {
         tc::tmem_ld32(v, src + chunk(i));
         tc::tmem_ld_wait();
@@ -394,23 +494,24 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
         if (i == chunks - 1) arrive(empty0);
       };
       bool wrote = true;                     // this was the tile's last part
+      const int64_t size = (int64_t)t.part_cols * 128;
+      const float *const part = p.part + (t.slot * t.split * 2 + (int)rank) * size + wq * 32 + lane;
       if (t.split > 1) {
         // A part of a split contraction leaves its sums in the workspace
         // ([tile][part][CTA][column][128 features]); the last part to finish
         // adds all of them, in the order of the parts.
-        const int64_t size = (int64_t)t.part_cols * 128;
-        const float *part = p.part + (t.slot * t.split * 2 + (int)rank) * size;
-        float *own = p.part + ((t.slot * t.split + t.part) * 2 + (int)rank) * size;
+        float *own = p.part + ((t.slot * t.split + t.part) * 2 + (int)rank) * size + wq * 32 + lane;
         for (int i = 0; i < chunks; ++i) {
           uint32_t v[32];
           read(i, v);
+          const int c = chunk(i);
 #pragma unroll
           for (int q = 0; q < 32; ++q)
-            __stcg(own + (chunk(i) + q) * 128 + wq * 32 + lane, __uint_as_float(v[q]));
+            if (c + q < t.cols) __stcg(own + (c + q) * 128, __uint_as_float(v[q]));
         }
-        __threadfence();
-        named_sync(3, 32 * kEpiWarps);
+        named_sync(3, 32 * kOutWarps);
         if (threadIdx.x == 128) {
+          __threadfence();
           const uint32_t ticket = t.slot * 2 + rank, shift = 4 * (ticket & 7);
           const uint32_t was = atomicAdd(p.tickets + (ticket >> 3), 1u << shift);
           const bool last = ((was >> shift) & 15u) == (uint32_t)t.split - 1;
@@ -418,48 +519,32 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
           *last_in = last;
           __threadfence();
         }
-        named_sync(3, 32 * kEpiWarps);
+        named_sync(3, 32 * kOutWarps);
         wrote = *last_in != 0;
-        if (wrote)
-          for (int c = grp * 32; c < t.n; c += 64) {
-            float4 lo[4], hi[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) lo[r] = hi[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
-            for (int s = 0; s < t.split; ++s)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const float *q = part + s * 2 * size + (c + r * 8 + r8) * 128 + 4 * i4;
-                const float4 a = __ldcg(reinterpret_cast<const float4 *>(q));
-                const float4 b = __ldcg(reinterpret_cast<const float4 *>(q + 64));
-                lo[r] = make_float4(lo[r].x + a.x, lo[r].y + a.y, lo[r].z + a.z, lo[r].w + a.w);
-                hi[r] = make_float4(hi[r].x + b.x, hi[r].y + b.y, hi[r].z + b.z, hi[r].w + b.w);
-              }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) emit(c + r * 8 + r8, c + r * 8 + r8 < t.cols, lo[r], hi[r]);
-          }
-      } else {
-        for (int i = 0; i < chunks; ++i) {
-          uint32_t v[32];
-          read(i, v);
-          if (i > 0) named_sync(1 + grp, 128);             // the last chunk has been read
-#pragma unroll
-          for (int q = 0; q < 32; ++q) st[q * 128 + wq * 32 + lane] = __uint_as_float(v[q]);
-          named_sync(1 + grp, 128);
-          const int c = chunk(i);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int tok = r * 8 + r8;
-            emit(c + tok, c + tok < t.cols, *reinterpret_cast<const float4 *>(st + tok * 128 + 4 * i4),
-                 *reinterpret_cast<const float4 *>(st + tok * 128 + 64 + 4 * i4));
-          }
-        }
       }
-      if (gate && wrote) {
-        // half a tile of a is written, for copies of other CTAs to read
+      for (int i = 0; wrote && i < chunks; ++i) {
+        uint32_t v[32];
+        const int c = chunk(i);
+        if (t.split > 1) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) v[q] = 0u;
+#pragma unroll 1
+          for (int s = 0; s < t.split; ++s)
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              if (c + q < t.cols)
+                v[q] = __float_as_uint(__uint_as_float(v[q]) + __ldcg(part + s * 2 * size + (c + q) * 128));
+        } else {
+          read(i, v);
+        }
+        emit(c, v);
+      }
+      if (gate && t.split == 1) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_local(rec_done + 8 * slot);
+      } else if (gate && wrote) {
         tc::fence_async_global();
-        __threadfence();
-        named_sync(3, 32 * kEpiWarps);
+        named_sync(3, 32 * kOutWarps);
         if (threadIdx.x == 128) {
           __threadfence();
           atomicAdd(p.units->ready + t.epoch, 1u);
@@ -532,8 +617,9 @@ bool map_tokens(MxJob &j, const void *rows, const void *scales, int64_t width, i
     if (cap <= (32 << i)) break;
   }
   const ScaleLayout l = scale_layout(cap, width);
-  return map_scales(&j.b_scale[0], scales, l, E, 1) &&
-         (cap <= 128 || map_scales(&j.b_scale[1], scales, l, E, 2));
+  for (int i = 0; i < 3 && i < l.row_tiles; ++i)
+    if (!map_scales(&j.b_scale[i], scales, l, E, i + 1)) return false;
+  return true;
 }
 
 // Units of a product: its most tiles, each in up to kMaxSplit parts.

@@ -80,8 +80,9 @@ __device__ __forceinline__ int rows_of(const P &p, int e) {
 // Tiles of `rows` tokens, and the columns of each but the last: as few tiles as
 // 256 columns allow, equal, a multiple of 32 (the granularity of a matrix
 // instruction's columns).  With n tiles rows > 256 (n - 1) and the columns are
-// at most 256, so that the last tile is never empty.  With kWholeTiles all but
-// the last have 256: block scales come 128 rows at a time.
+// at most 256, so that the last tile is never empty.  Where tiles start on
+// multiples of kTileStep > 32, the steps are dealt out evenly: some tiles have one
+// more than the others.
 __device__ __forceinline__ int token_tiles(int rows) { return (int)(((unsigned)rows + 255u) >> 8); }
 __device__ __forceinline__ int tile_cols(int rows, int tiles) {
   return (int)((((unsigned)rows + tiles - 1) / tiles + 31) & ~31u);
@@ -210,10 +211,17 @@ struct Schedule {
     o.n0 = 0;
     o.cols = o.rows;
     if (nt > 1) {
-      const int c = P::kWholeTiles ? kTileCols : tile_cols(o.rows, nt);
       o.m = r / nt;
-      o.n0 = (r - o.m * nt) * c;
-      o.cols = min(c, o.rows - o.n0);
+      const int i = r - o.m * nt;
+      if constexpr (P::kTileStep == 32) {
+        const int c = tile_cols(o.rows, nt);
+        o.n0 = i * c;
+        o.cols = min(c, o.rows - o.n0);
+      } else {
+        const int steps = (o.rows + P::kTileStep - 1) / P::kTileStep, each = steps / nt, more = steps - each * nt;
+        o.n0 = P::kTileStep * (i * each + min(i, more));
+        o.cols = min(P::kTileStep * (each + (i < more)), o.rows - o.n0);
+      }
     }
     o.n = (o.cols + 31) & ~31;
     const int nk = (p.job[KIND == kForward ? row : 0].K + kBlockK - 1) / kBlockK;
@@ -337,16 +345,21 @@ struct Feed {
     return spread<WORDS>(read(), t);
   }
 
- private:
-  // Every lane has read the record.  The last one's place is not used again, and
-  // nobody waits for it.
-  __device__ __forceinline__ bool done(const Tile &t) {
-    if (t.valid == 0) return false;
+  // Every lane is done with the record: its place is free, on to the next.
+  __device__ __forceinline__ void leave() {
     tc::mbar_arrive_warp_at(empty + 8 * s);
     if (++s == kRing) {
       s = 0;
       ph ^= 1u;
     }
+  }
+
+ private:
+  // Every lane has read the record.  The last one's place is not used again, and
+  // nobody waits for it.
+  __device__ __forceinline__ bool done(const Tile &t) {
+    if (t.valid == 0) return false;
+    leave();
     return true;
   }
 };

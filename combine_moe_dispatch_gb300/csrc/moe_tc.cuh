@@ -232,38 +232,44 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
 }
 // A stage's scales into tensor memory on both CTAs of the pair, each from its
 // own shared memory, by a whole warp: two tiles of A's 128 rows, one for each 128
-// k, into columns [to, to + 4) and [to + 4, to + 8), and as many for every 128
-// columns of the product into [to + 8, to + 16) and [to + 16, to + 24).  In
-// shared memory the tiles of 128 k follow one another, those of the next 128
-// columns come after.  `second_k`: the stage has more than 128 k; `second_n`: the
-// product has more than 128 columns.
+// k, into columns [to, to + 4) and [to + 4, to + 8), and `tiles` (1 to 3) of B's,
+// 128 rows each, into [to + 8, to + 20) and [to + 20, to + 32), 4 columns a
+// tile.  In shared memory the tiles of 128 k follow one another, those of the next
+// 128 rows come after.  `second_k`: the stage has more than 128 k.
 __device__ __forceinline__ void load_scales(uint32_t to, uint64_t a, uint64_t b, uint32_t second_k,
-                                            uint32_t second_n) {
-  asm volatile("{\n\t.reg .pred e, ek, en, ekn;\n\t"
+                                            uint32_t tiles) {
+  asm volatile("{\n\t.reg .pred e, ek, e1, e2, f1, f2;\n\t"
                ".reg .b32 t;\n\t"
                ".reg .b64 s;\n\t"
                "elect.sync _|e, 0xFFFFFFFF;\n\t"
                "setp.ne.and.u32 ek, %3, 0, e;\n\t"
-               "setp.ne.and.u32 en, %4, 0, e;\n\t"
-               "setp.ne.and.u32 ekn, %4, 0, ek;\n\t"
+               "setp.gt.and.u32 e1, %4, 1, e;\n\t"
+               "setp.gt.and.u32 e2, %4, 2, e;\n\t"
+               "setp.gt.and.u32 f1, %4, 1, ek;\n\t"
+               "setp.gt.and.u32 f2, %4, 2, ek;\n\t"
                "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t"
                "add.u32 t, %0, 8;\n\t"
                "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [t], %2;\n\t"
                "add.u32 t, %0, 12;\n\tadd.s64 s, %2, 64;\n\t"
-               "@en tcgen05.cp.cta_group::2.32x128b.warpx4 [t], s;\n\t"
+               "@e1 tcgen05.cp.cta_group::2.32x128b.warpx4 [t], s;\n\t"
+               "add.u32 t, %0, 16;\n\tadd.s64 s, %2, 128;\n\t"
+               "@e2 tcgen05.cp.cta_group::2.32x128b.warpx4 [t], s;\n\t"
                "add.u32 t, %0, 4;\n\tadd.s64 s, %1, 32;\n\t"
                "@ek tcgen05.cp.cta_group::2.32x128b.warpx4 [t], s;\n\t"
-               "add.u32 t, %0, 16;\n\tadd.s64 s, %2, 32;\n\t"
+               "add.u32 t, %0, 20;\n\tadd.s64 s, %2, 32;\n\t"
                "@ek tcgen05.cp.cta_group::2.32x128b.warpx4 [t], s;\n\t"
-               "add.u32 t, %0, 20;\n\tadd.s64 s, %2, 96;\n\t"
-               "@ekn tcgen05.cp.cta_group::2.32x128b.warpx4 [t], s;\n\t}"
-               ::"r"(to), "l"(a), "l"(b), "r"(second_k), "r"(second_n) : "memory");
+               "add.u32 t, %0, 24;\n\tadd.s64 s, %2, 96;\n\t"
+               "@f1 tcgen05.cp.cta_group::2.32x128b.warpx4 [t], s;\n\t"
+               "add.u32 t, %0, 28;\n\tadd.s64 s, %2, 160;\n\t"
+               "@f2 tcgen05.cp.cta_group::2.32x128b.warpx4 [t], s;\n\t}"
+               ::"r"(to), "l"(a), "l"(b), "r"(second_k), "r"(tiles) : "memory");
 }
 // mma_stage for kind::mxf4, after load_scales(scales, ...): `steps` (1 to 4) times
-// 64 k.
+// 64 k.  The product's first column is row 0 of B's first tile of scales, or with
+// `skip` 2 row 64: a column of scales holds those of 32 rows.
 __device__ __forceinline__ Asked mma_stage_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                              uint32_t scales, uint32_t accumulate, uint32_t steps,
-                                              uint32_t done, uint32_t bar0, uint32_t p0, uint32_t bar1,
+                                              uint32_t scales, uint32_t skip, uint32_t accumulate,
+                                              uint32_t steps, uint32_t done, uint32_t bar0, uint32_t p0, uint32_t bar1,
                                               uint32_t p1) {
   Asked r;
   asm volatile("{\n\t.reg .pred e, e1, e2, e3, c, q0, q1;\n\t"
@@ -275,7 +281,7 @@ __device__ __forceinline__ Asked mma_stage_mx(uint32_t d, uint64_t a, uint64_t b
                "setp.gt.and.u32 e2, %8, 2, e;\n\t"
                "setp.gt.and.u32 e3, %8, 3, e;\n\t"
                "or.b32 odd, %5, 0x40000020;\n\t"
-               "add.u32 sb, %6, 8;\n\tadd.u32 sa1, %6, 4;\n\tadd.u32 sb1, %6, 16;\n\t"
+               "add.u32 sa1, %6, 4;\n\tadd.u32 sb, %6, %15;\n\tadd.u32 sb, sb, 8;\n\tadd.u32 sb1, sb, 12;\n\t"
                "add.s64 a1, %3, 2;\n\tadd.s64 b1, %4, 2;\n\t"
                "add.s64 a2, %3, 4;\n\tadd.s64 b2, %4, 4;\n\t"
                "add.s64 a3, %3, 6;\n\tadd.s64 b3, %4, 6;\n\t"
@@ -291,7 +297,7 @@ __device__ __forceinline__ Asked mma_stage_mx(uint32_t d, uint64_t a, uint64_t b
                "selp.u32 %1, 1, 0, q1;\n\t}"
                : "=r"(r.first), "=r"(r.second)
                : "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(scales), "r"(accumulate), "r"(steps), "r"(done),
-                 "r"(bar0), "r"(p0), "r"(bar1), "r"(p1), "h"((uint16_t)3)
+                 "r"(bar0), "r"(p0), "r"(bar1), "r"(p1), "h"((uint16_t)3), "r"(skip)
                : "memory");
   return r;
 }
