@@ -392,14 +392,15 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
       const auto emit = [&](int c, const uint32_t (&v)[32]) {
         if (gate) {
           // Through shared memory, so that a lane gets 16 features of one token: half
-          // of a block, whose largest magnitude is then one exchange away.  (With a
+          // of a block, whose largest magnitude is then one exchange away, and four
+          // lanes the token's 64, a whole sector of codes.  (With a
           // lane per feature and the maximum over the warp's lanes the chunk took
           // twice as long.)
           float *const own = staged + wq * 32 + lane;
 #pragma unroll
           for (int i = 0; i < 32; ++i) own[i * kStagedRow] = __uint_as_float(v[i]);
           named_sync(1 + grp, 128);
-          const int at = 16 * (wq >> 1) + (lane & 15), f = 32 * (wq & 1) + 16 * (lane >> 4);
+          const int at = 8 * wq + (lane & 7), f = 16 * (lane >> 3);
           const float4 *const in = reinterpret_cast<const float4 *>(staged + at * kStagedRow + f);
           float a[16];
           uint32_t most = 0;
@@ -414,7 +415,7 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
             }
           }
           named_sync(1 + grp, 128);          // all have read: the next chunk may be staged
-          most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
+          most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 8));
           const uint32_t byte = mx_scale(most >> 23);
           const float inv = mx_inverse(byte);
           uint32_t code[2];
@@ -426,15 +427,17 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
             code[i] = e2m1x8(x);
           }
           const int tok = c + at, feature = rt * 64 + f;
+          // features past the last have a scale of 0 in the last tile of blocks
+          const uint32_t scale = feature < j.M ? byte : 0u;
+          const uint32_t scales = scale | __shfl_down_sync(0xFFFFFFFFu, scale, 16) << 8;
           if (tok < t.cols) {
             if (feature < j.M)
               *reinterpret_cast<uint2 *>(j.q + ((row0 + tok) * j.M + feature) / 2) = make_uint2(code[0], code[1]);
-            if (lane < 16) {
-              // features past the last have a scale of 0 in the last tile of blocks
+            if (lane < 8) {
               const int r = t.n0 + tok;
               const int64_t tile = ((int64_t)t.e * j.row_tiles + (r >> 7)) * j.block_tiles + t.m;
-              j.scale[tile * kScaleTileBytes + (r & 31) * 16 + ((r >> 5) & 3) * 4 + 2 * rank + (wq & 1)] =
-                  feature < j.M ? (uint8_t)byte : (uint8_t)0;
+              *reinterpret_cast<uint16_t *>(j.scale + tile * kScaleTileBytes + (r & 31) * 16 +
+                                            ((r >> 5) & 3) * 4 + 2 * rank) = (uint16_t)scales;
             }
           }
         } else {
@@ -456,6 +459,30 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
         ok = wait_bar(tm_full + 8 * buf, (it >> 1) & 1u, limit);
         tc::fence_after();
       }
+      const uint32_t src = tmem + ((uint32_t)(wq * 32) << 16) + (buf ? kAcc1 : kAcc0);
+      const auto arrive = [&](uint32_t bar) {     // this warp has read its part of the columns
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_remote(bar + 8 * buf);
+      };
+      // The group's chunks of 32 columns, those that the accumulators share first:
+      // the first accumulator's last, the second's first.
+      const int chunks = (t.n - grp * 32 + 32 * kGroups - 1) / (32 * kGroups);     // t.n >= 32
+      const bool shares = buf ? grp == 0 : grp == (kApart / 32) % kGroups && t.n > kApart;
+      const auto chunk = [&](int i) { return grp * 32 + 32 * kGroups * (buf ? i : chunks - 1 - i); };
+      const auto read = [&](int i, uint32_t (&v)[32]) {
+        tc::tmem_ld32(v, src + chunk(i));
+        tc::tmem_ld_wait();
+        if (i == 0 && shares) arrive(shared0);
+        if (i == chunks - 1) arrive(empty0);
+      };
+      // The first chunk at once: the next tile may be waiting for it.
+      uint32_t v[32];
+      if (ok && more) {
+        if (!shares) arrive(shared0);
+        if (chunks > 0) read(0, v);
+        else arrive(empty0);
+      }
       // A group's warps agree to go on.  Both groups do where a tile is cut, which
       // they finish together; one that has given up says so at that barrier.  (Both
       // agreeing on every tile cost the batch's tiles 0.3 us each.)
@@ -474,25 +501,6 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
           break;
         }
       }
-      const uint32_t src = tmem + ((uint32_t)(wq * 32) << 16) + (buf ? kAcc1 : kAcc0);
-      const auto arrive = [&](uint32_t bar) {     // this warp has read its part of the columns
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive_remote(bar + 8 * buf);
-      };
-      // The group's chunks of 32 columns, those that the accumulators share first:
-      // the first accumulator's last, the second's first.
-      const int chunks = (t.n - grp * 32 + 32 * kGroups - 1) / (32 * kGroups);     // t.n >= 32
-      const bool shares = buf ? grp == 0 : grp == (kApart / 32) % kGroups && t.n > kApart;
-      if (!shares) arrive(shared0);
-      if (chunks <= 0) arrive(empty0);
-      const auto chunk = [&](int i) { return grp * 32 + 32 * kGroups * (buf ? i : chunks - 1 - i); };
-      const auto read = [&](int i, uint32_t (&v)[32]) {
-        tc::tmem_ld32(v, src + chunk(i));
-        tc::tmem_ld_wait();
-        if (i == 0 && shares) arrive(shared0);
-        if (i == chunks - 1) arrive(empty0);
-      };
       bool wrote = true;                     // this was the tile's last part
       const int64_t size = (int64_t)t.part_cols * 128;
       const float *const part = p.part + (t.slot * t.split * 2 + (int)rank) * size + wq * 32 + lane;
@@ -502,8 +510,7 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
         // adds all of them, in the order of the parts.
         float *own = p.part + ((t.slot * t.split + t.part) * 2 + (int)rank) * size + wq * 32 + lane;
         for (int i = 0; i < chunks; ++i) {
-          uint32_t v[32];
-          read(i, v);
+          if (i > 0) read(i, v);
           const int c = chunk(i);
 #pragma unroll
           for (int q = 0; q < 32; ++q)
@@ -523,7 +530,6 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
         wrote = *last_in != 0;
       }
       for (int i = 0; wrote && i < chunks; ++i) {
-        uint32_t v[32];
         const int c = chunk(i);
         if (t.split > 1) {
 #pragma unroll
@@ -534,7 +540,7 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
             for (int q = 0; q < 32; ++q)
               if (c + q < t.cols)
                 v[q] = __float_as_uint(__uint_as_float(v[q]) + __ldcg(part + s * 2 * size + (c + q) * 128));
-        } else {
+        } else if (i > 0) {
           read(i, v);
         }
         emit(c, v);
