@@ -374,9 +374,9 @@ struct GainParams {
   float *d_gain;               // [H]
   int parts, H;
 };
-constexpr int kGainThreads = 512;
+constexpr int kGainThreads = 1024;
 
-// 32 columns a block: each warp adds every 16th block's share, then the warps'
+// 32 columns a block: each warp adds every 32nd block's share, then the warps'
 // sums are added in their order.
 __global__ void __launch_bounds__(kGainThreads)
 norm_gain_kernel(GainParams p) {

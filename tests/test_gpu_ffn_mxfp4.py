@@ -143,3 +143,203 @@ def test_ffn(E, cap, H, I, counts):
             s[k].fill_(f)
         _run(moe, s)
         assert all(torch.equal(w, s[k]) for w, k in zip(want, ("act", "act_scale", "y")))
+
+
+def _clear(s):
+    for k, f in (("act", FILL), ("act_scale", FILL), ("y", SENTINEL)):
+        s[k].fill_(f)
+
+
+def _untouched(s):
+    return bool((s["act"] == FILL).all()) and bool((s["act_scale"] == FILL).all()) and \
+        bool((s["y"] == SENTINEL).all())
+
+
+def _results(s):
+    return [s[k].clone() for k in ("act", "act_scale", "y")]
+
+
+def _same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_without_counts():
+    moe, s = _case(3, 33, 256, 160, [33] * 3, 30)
+    _run(moe, s)
+    want = _results(s)
+    _clear(s)
+    _run(moe, s, cnt=None)
+    assert _same(want, _results(s))
+
+
+def test_rows_keep_to_themselves():
+    """NaN and infinity in one block of two tokens: their rows alone."""
+    moe, s = _case(2, 70, 256, 160, [70, 9], 31)
+    _run(moe, s)
+    want = _results(s)
+    at = ref.places(70, 256, False, "cuda")
+    s["xs"][0].view(-1)[at[5, 3]] = 255
+    s["xs"][0].view(-1)[at[69, 0]] = 254                   # times 6: beyond binary32
+    s["xq"][0, 69, :16] = 0x77
+    _run(moe, s)
+    fine = [i for i in range(70) if i not in (5, 69)]
+    assert torch.equal(s["y"][0, fine], want[2][0, fine]) and torch.equal(s["y"][1], want[2][1])
+    assert bool(s["y"][0, 5].isnan().all())
+    assert not bool(s["y"][0, 69].isfinite().any())
+
+
+def test_beyond_32_bits():
+    """Weights of more than 2^32 bytes; the last expert alone has rows."""
+    import combine_moe_dispatch_gb300 as moe
+    E, cap, H, I = 44, 40, 7168, 14336
+    _, one = _case(1, cap, H, I, [37], 32)
+    s = dict(one, c=[0] * (E - 1) + [37], shape=moe.make_shape(1, E * cap, H, E, 1, cap))
+    s["cnt"] = torch.tensor(s["c"], dtype=torch.int32, device="cuda")
+
+    def widen(t, fill):
+        w = torch.full((E, *t.shape[1:]), fill, dtype=t.dtype, device="cuda")
+        w[-1] = t[0]
+        return w
+
+    s["xq"], s["xs"] = widen(one["xq"], 0), widen(one["xs"], 255)
+    s["wgu"] = (widen(one["wgu"][0], 0), widen(one["wgu"][1], 255))
+    s["wd"] = (widen(one["wd"][0], 0), widen(one["wd"][1], 255))
+    assert s["wgu"][0].numel() > 2 ** 32
+    for k in ("act", "act_scale", "y"):
+        s[k] = widen(one[k], FILL if k != "y" else SENTINEL)
+    s["ws"] = torch.zeros(moe.ffn_mxfp4_workspace_size(s["shape"], I), dtype=torch.uint8, device="cuda")
+    _run(moe, s)
+    assert moe.read_status(s["ws"]) == moe.Status.OK
+    assert bool((s["y"][:-1] == SENTINEL).all()) and bool((s["act"][:-1] == FILL).all())
+    last = dict(one, c=[37], act=s["act"][-1:], act_scale=s["act_scale"][-1:], y=s["y"][-1:])
+    _check(last, 1, cap, H, I)
+
+
+# WsHeader: the status is word 4, flags word 5, the counters start at word 10
+FLAGS, NEXT_UNIT = 5, 10
+BROKEN = -2 ** 31
+
+
+def _planned(seed=33):
+    """The case of 12 tokens over 2 experts, 2 x 2 tiles of a and 2 of y."""
+    moe, s = _case(2, 8, 128, 256, [6, 6], seed)
+    s["shape"] = moe.make_shape(1, 12, 128, 2, 1, 8)
+    b = moe.Buffers(s["shape"], expert_x=False, expert_y=False)
+    b.workspace = s["ws"] = torch.zeros(moe.ffn_mxfp4_workspace_size(s["shape"], 256), dtype=torch.uint8,
+                                        device="cuda")
+    idx = torch.tensor([[i % 2] for i in range(12)], dtype=torch.int32, device="cuda")
+
+    def step(bad=False):
+        b.plan(torch.full_like(idx, 2) if bad else idx)
+        _run(moe, s)
+        return moe.read_status(s["ws"])
+
+    return moe, s, b, idx, step
+
+
+def test_failed_plan():
+    moe, s, _, _, step = _planned()
+    assert step(bad=True) == moe.Status.BAD_EXPERT and _untouched(s)
+    assert step() == moe.Status.OK
+    _check(s, 2, 8, 128, 256)
+
+
+def test_wait_that_runs_out():
+    """The launch's unit counter is set past the tiles of a, so that nobody
+    computes them and the tiles of y wait, 20 ms at most, for a count that
+    nothing raises: the kernel returns, reports TIMEOUT and writes nothing, and so
+    do later calls until the workspace is initialised."""
+    moe, s, b, idx, step = _planned()
+    assert step() == moe.Status.OK
+    want = _results(s)
+    moe.workspace_set_debug(s["ws"], 0, 20_000_000)
+    _clear(s)
+    b.plan(idx)
+    s["ws"].view(torch.int32)[NEXT_UNIT] = 4
+    _run(moe, s)
+    assert moe.read_status(s["ws"]) == moe.Status.TIMEOUT and _untouched(s)
+    moe.workspace_set_debug(s["ws"], 0, 0)
+    for _ in range(2):
+        assert step() == moe.Status.TIMEOUT and _untouched(s)
+    moe.workspace_init(s["ws"])
+    assert step() == moe.Status.OK and _same(want, _results(s))
+
+
+def test_refused_with_the_mark_of_another_call():
+    """A wait of moe_ffn that ran out stops this call too."""
+    moe, s, _, _, step = _planned()
+    _clear(s)
+    s["ws"].view(torch.int32)[FLAGS] = BROKEN
+    assert step() == moe.Status.TIMEOUT and _untouched(s)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_back_to_back_with_the_bf16_calls(graph):
+    """Calls of different shapes, and moe_ffn between them, on one workspace:
+    each gives what it gives alone."""
+    import combine_moe_dispatch_gb300 as moe
+    cases = [_case(*c, 40 + 3 * i)[1] for i, c in enumerate(
+        [(1, 1, 32, 32, [1]), (3, 40, 288, 160, [40, 0, 7]), (1, 300, 160, 96, [290]), (2, 4, 64, 64, [0, 0]),
+         (1, 20, 5152, 4128, [20]), (90, 2, 64, 96, [1, 2, 0] * 30)])]
+    E, cap, H, I = 3, 40, 264, 136
+    x = torch.randn((E, cap, H), device="cuda").bfloat16()
+    wgu, wd = torch.randn((E, 2 * I, H), device="cuda").bfloat16(), torch.randn((E, H, I), device="cuda").bfloat16()
+    act, y = torch.zeros((E, cap, I), device="cuda").bfloat16(), torch.zeros((E, cap, H), device="cuda").bfloat16()
+    shape = moe.make_shape(1, E * cap, H, E, 1, cap)
+    size = max([moe.ffn_workspace_size(shape, I)] + [s["ws"].numel() for s in cases])
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+
+    def bf16():
+        moe.ffn(shape, I, x, wgu, wd, None, None, act, y, ws)
+
+    want = []
+    for s in cases:
+        _run(moe, s)
+        want.append(_results(s))
+        _clear(s)
+        s["ws"] = ws
+    bf16()
+    y_want = y.clone()
+
+    def run():
+        for s in cases:
+            _run(moe, s)
+            bf16()
+            _run(moe, s)
+
+    if graph:
+        side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+            run()
+        run_it = g.replay
+    else:
+        run_it = run
+    for _ in range(10):
+        for s in cases:
+            _clear(s)
+        y.zero_()
+        run_it()
+        torch.cuda.synchronize()
+        assert moe.read_status(ws) == moe.Status.OK
+        assert all(_same(w, _results(s)) for w, s in zip(want, cases)) and torch.equal(y, y_want)
+
+
+def test_two_streams_at_once():
+    """Two calls with workspaces of their own that share the GPU."""
+    import combine_moe_dispatch_gb300 as moe
+    cases = [_case(3, 600, 512, 1056, [600, 33, 500], 70)[1], _case(40, 30, 1056, 544, [30, 0, 7, 16] * 10, 73)[1]]
+    want = []
+    for s in cases:
+        _run(moe, s)
+        want.append(_results(s))
+        _clear(s)
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, stream in zip(cases, streams):
+            with torch.cuda.stream(stream):
+                _run(moe, s)
+    torch.cuda.synchronize()
+    for s, w in zip(cases, want):
+        assert moe.read_status(s["ws"]) == moe.Status.OK and _same(w, _results(s))

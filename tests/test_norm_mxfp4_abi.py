@@ -150,3 +150,59 @@ def test_dispatch_mxfp4_arguments(lib):
         assert call(SHAPE[:6] + (payload,)) == Status.UNSUPPORTED
     assert call((1, 16, 272, 4, 2, 16, 0)) == Status.UNSUPPORTED             # H % 32
     assert call(EMPTY, x=None, idx=None, slot=None, ex=None, scale=None, ws=None) == Status.OK
+
+
+I = 128
+
+
+def _ffn(lib, shape=SHAPE, inter=I, **bad):
+    a = dict(x=A, xs=A, wgu=A, wgus=A, wd=A, wds=A, cnt=A, act=A, acts=A, y=A, ws=A, nbytes=1 << 40)
+    a.update(bad)
+    s = Shape(*shape)
+    return lib.moe_ffn_mxfp4(ctypes.byref(s), inter, *a.values(), None)
+
+
+def test_ffn_mxfp4_arguments(lib):
+    required = ["x", "xs", "wgu", "wgus", "wd", "wds", "act", "acts", "y"]
+    for name in required:
+        assert _ffn(lib, **{name: None}) == Status.INVALID_ARG, name
+        assert _ffn(lib, **{name: A + 8}) == Status.ALIGNMENT, name
+    assert _ffn(lib, cnt=None, x=A + 8) == Status.ALIGNMENT
+    assert _ffn(lib, cnt=A + 2) == Status.ALIGNMENT
+    need = moe.ffn_mxfp4_workspace_size(Shape(*SHAPE), I)
+    assert _ffn(lib, nbytes=need - 1) == Status.WORKSPACE
+    assert _ffn(lib, ws=None) == Status.WORKSPACE
+    assert _ffn(lib, ws=A + 8) == Status.ALIGNMENT
+    assert _ffn(lib, nbytes=need, x=A + 8) == Status.ALIGNMENT
+    assert _ffn(lib, inter=0) == Status.INVALID_ARG
+    assert _ffn(lib, inter=-32) == Status.INVALID_ARG
+    assert _ffn(lib, inter=144) == Status.UNSUPPORTED                        # not a multiple of 32
+    assert _ffn(lib, shape=(1, 16, 272, 4, 2, 16, 0)) == Status.UNSUPPORTED  # H % 32
+    for payload in (1, 2):
+        assert _ffn(lib, shape=SHAPE[:6] + (payload,)) == Status.UNSUPPORTED
+
+
+def test_ffn_mxfp4_size_limits(lib):
+    """Each limit just passed, and just kept (the call then fails at the next
+    check, a null pointer)."""
+    null = dict(x=None)
+    big = (1, 4, 256, 1024, 2, 1 << 20, 0)                 # E * cap = 2^30
+    assert _ffn(lib, big, 1 << 15, **null) == Status.UNSUPPORTED             # rows * 2I = 2^46
+    assert _ffn(lib, big, (1 << 15) - 32, **null) == Status.INVALID_ARG
+    assert _ffn(lib, (1, 4, 1 << 16, 1024, 2, 1 << 20, 0), 32, **null) == Status.UNSUPPORTED
+    assert _ffn(lib, (1, 4, (1 << 16) - 32, 1024, 2, 1 << 20, 0), 32, **null) == Status.INVALID_ARG
+    one = (1, 4, 1 << 20, 1, 1, 1, 0)                      # 4 I H = 2^40
+    assert _ffn(lib, one, 1 << 18, **null) == Status.UNSUPPORTED
+    assert _ffn(lib, one, (1 << 18) - 32, **null) == Status.INVALID_ARG
+    thin = (1, 4, 32, 1, 1, 1, 0)
+    assert _ffn(lib, thin, 1 << 29, **null) == Status.UNSUPPORTED
+    assert _ffn(lib, (1, 4, 1 << 30, 1, 1, 1, 0), 32, **null) == Status.UNSUPPORTED
+
+
+def test_ffn_mxfp4_workspace_size(lib):
+    s = Shape(*SHAPE)
+    assert moe.ffn_mxfp4_workspace_size(s, I) >= moe.workspace_size(s)
+    assert moe.ffn_mxfp4_workspace_size(s, 0) == 0
+    assert moe.ffn_mxfp4_workspace_size(Shape(1, 16, 260, 4, 2, 16, 0), I) == 0
+    big = Shape(8, 512, 7168, 256, 8, 8192, 0)             # bounded: sums of 128 tiles of 256 x 256 floats
+    assert moe.ffn_mxfp4_workspace_size(big, 2048) <= moe.workspace_size(big) + (128 << 18)
