@@ -19,7 +19,7 @@
 // a lane's columns are the same for all of its rows: their share of d_gain is
 // summed in registers, joined over the block's warps in shared memory, stored
 // once per block, and a second launch adds the blocks' shares, all in an order
-// that depends on the sizes alone.  Rows of more than 8192 elements do not fit
+// that depends on the sizes alone.  Rows of more than 16384 elements do not fit
 // the registers: a block then reads its row twice (the second time from the
 // caches).
 #include <cuda_bf16.h>
@@ -30,10 +30,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 256;      // a block, but 512 for rows of 8193 to 16384 elements
 constexpr int kNormWarps = kNormThreads / 32;
 constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kNormMaxRow = kNormThreads * 4 * 8;   // elements of a row held in registers, at most
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -107,11 +106,11 @@ __device__ __forceinline__ void store_fp8(const NormParams &p, int64_t row, int 
   }
 }
 
-template <int C, int WPR, bool RES, bool FP8>
-__global__ void __launch_bounds__(kNormThreads, C == 1 ? 6 : 4)
+template <int C, int WPR, bool RES, bool FP8, int WARPS = kNormWarps>
+__global__ void __launch_bounds__(32 * WARPS, C == 1 ? 6 : 32 / WARPS)
 norm_kernel(NormParams p) {
-  constexpr int kRows = kNormWarps / WPR;
-  __shared__ float s_sum[2][kNormWarps];
+  constexpr int kRows = WARPS / WPR;
+  __shared__ float s_sum[2][WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = (warp % WPR) * 32 + lane, cpr = p.H / 8, nb = (p.H + 127) / 128;
   pdl_wait_for_previous();
@@ -207,11 +206,11 @@ norm_long_kernel(NormParams p) {
   }
 }
 
-template <int C, int WPR, bool DSUM>
-__global__ void __launch_bounds__(kNormThreads, 2)
+template <int C, int WPR, bool DSUM, int WARPS = kNormWarps>
+__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
 norm_backward_kernel(NormBackwardParams p) {
-  constexpr int kRows = kNormWarps / WPR;
-  __shared__ float s_sum[2][2][kNormWarps];
+  constexpr int kRows = WARPS / WPR;
+  __shared__ float s_sum[2][2][WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = (warp % WPR) * 32 + lane, cpr = p.H / 8;
   pdl_wait_for_previous();
@@ -400,11 +399,11 @@ norm_gain_kernel(GainParams p) {
   }
 }
 
-template <int C, int WPR, bool RES, bool FP8>
+template <int C, int WPR, bool RES, bool FP8, int WARPS = kNormWarps>
 cudaError_t launch_rows(const NormParams &p, cudaStream_t stream) {
-  const auto kern = norm_kernel<C, WPR, RES, FP8>;
-  return launch_after_previous(kern, persistent_grid((const void *)kern, kNormThreads, (int64_t)p.N * WPR),
-                               kNormThreads, p, stream);
+  const auto kern = norm_kernel<C, WPR, RES, FP8, WARPS>;
+  return launch_after_previous(kern, persistent_grid((const void *)kern, 32 * WARPS, (int64_t)p.N * WPR),
+                               32 * WARPS, p, stream);
 }
 
 template <bool RES, bool FP8>
@@ -415,23 +414,24 @@ cudaError_t launch_width(const NormParams &p, cudaStream_t stream) {
   if (cpr <= 128) return launch_rows<4, 1, RES, FP8>(p, stream);
   if (cpr <= 256) return launch_rows<4, 2, RES, FP8>(p, stream);
   if (cpr <= 512) return launch_rows<4, 4, RES, FP8>(p, stream);
-  if (p.H <= kNormMaxRow) return launch_rows<4, 8, RES, FP8>(p, stream);
+  if (cpr <= 1024) return launch_rows<4, 8, RES, FP8>(p, stream);
+  if (cpr <= 2048) return launch_rows<4, 16, RES, FP8, 16>(p, stream);
   const auto kern = norm_long_kernel<RES, FP8>;
   return launch_after_previous(
       kern, persistent_grid((const void *)kern, kNormThreads, (int64_t)p.N * kNormWarps), kNormThreads, p,
       stream);
 }
 
-int backward_blocks(const void *kern, int64_t warps) {
-  const int g = persistent_grid(kern, kNormThreads, warps);
+int backward_blocks(const void *kern, int threads, int64_t warps) {
+  const int g = persistent_grid(kern, threads, warps);
   return g < kNormMaxBlocks ? g : kNormMaxBlocks;
 }
 
-template <int C, int WPR, bool DSUM>
+template <int C, int WPR, bool DSUM, int WARPS = kNormWarps>
 cudaError_t launch_backward_rows(const NormBackwardParams &p, int &parts, cudaStream_t stream) {
-  const auto kern = norm_backward_kernel<C, WPR, DSUM>;
-  parts = backward_blocks((const void *)kern, (int64_t)p.N * WPR);
-  return launch_after_previous(kern, parts, kNormThreads, p, stream);
+  const auto kern = norm_backward_kernel<C, WPR, DSUM, WARPS>;
+  parts = backward_blocks((const void *)kern, 32 * WARPS, (int64_t)p.N * WPR);
+  return launch_after_previous(kern, parts, 32 * WARPS, p, stream);
 }
 
 template <bool DSUM>
@@ -442,9 +442,10 @@ cudaError_t launch_backward_width(const NormBackwardParams &p, int &parts, cudaS
   if (cpr <= 128) return launch_backward_rows<4, 1, DSUM>(p, parts, stream);
   if (cpr <= 256) return launch_backward_rows<4, 2, DSUM>(p, parts, stream);
   if (cpr <= 512) return launch_backward_rows<4, 4, DSUM>(p, parts, stream);
-  if (p.H <= kNormMaxRow) return launch_backward_rows<4, 8, DSUM>(p, parts, stream);
+  if (cpr <= 1024) return launch_backward_rows<4, 8, DSUM>(p, parts, stream);
+  if (cpr <= 2048) return launch_backward_rows<4, 16, DSUM, 16>(p, parts, stream);
   const auto kern = norm_backward_long_kernel<DSUM>;
-  parts = backward_blocks((const void *)kern, (int64_t)p.N * kNormWarps);
+  parts = backward_blocks((const void *)kern, kNormThreads, (int64_t)p.N * kNormWarps);
   return launch_after_previous(kern, parts, kNormThreads, p, stream);
 }
 

@@ -23,8 +23,9 @@ SENTINEL = -12345.0
 # that have nothing; more rows than the grid has places; rows that do not fit
 # the registers
 SHAPES = [(1, 8), (5, 16), (7, 256), (3, 264), (9, 512), (33, 520), (2, 1024), (17, 1032), (4, 2048),
-          (6, 2064), (3, 4096), (5, 4104), (2, 7168), (1, 8192), (3, 8208), (2, 16400), (6000, 64),
-          (2500, 1040), (1300, 7168), (700, 8448)]
+          (6, 2064), (3, 4096), (5, 4104), (2, 7168), (1, 8192), (3, 8208), (2, 16384), (2, 16400),
+          (5, 40000), (6000, 64),
+          (2500, 1040), (1300, 7168), (700, 8448), (400, 17408)]
 IDS = [f"N{n}-H{h}" for n, h in SHAPES]
 
 
@@ -105,7 +106,7 @@ def test_norm(N, H, residual):
             assert bool((q[N - 1] == 0).all()) and bool((scale[N - 1] == 0).all())
 
 
-@pytest.mark.parametrize("N,H", [(5, 264), (40, 4096), (3, 8208)])
+@pytest.mark.parametrize("N,H", [(5, 264), (40, 4096), (3, 8208), (3, 16400)])
 def test_in_place(N, H):
     """s over x or over the residual, and y over the other one."""
     import combine_moe_dispatch_gb300 as moe
