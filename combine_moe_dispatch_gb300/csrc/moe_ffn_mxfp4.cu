@@ -21,11 +21,37 @@
 //    accumulators of 256: they overlap by 32 columns.  The epilogue reads those
 //    first, and the next tile starts when it has.  Tiles of up to 224 columns do
 //    not overlap.
-//  - a is quantised where it is computed: a block's 32 features are 8 lanes' 4, so
-//    that its maximum is three shuffles.
+//  - a is quantised where it is computed: through shared memory a lane gets 16
+//    features of one token, so that a block is two lanes.
+//  - Tiles are four times shorter in time than bf16's, so that what happens once a
+//    tile counts.  A warp of its own waits for the stores of a and publishes
+//    them; the two epilogue groups agree only where a tile is cut; an expert's
+//    tokens are dealt out to its tiles in steps of 64 (a last tile of a few tokens
+//    takes 0.2 us a stage however few they are, a full one 0.28).  Batch of 8192
+//    rows, step by step: lanes per feature and a maximum by shuffles 536 us; no
+//    fence in the epilogue 479; lanes per token 447; groups apart and weights of y
+//    ahead of its wait 441; even tiles 433; whole sectors of codes 424.
 //
 // Rounding: products of E2M1 numbers and powers of two, summed in binary32; a is
 // rounded to MXFP4 from binary32, y to bf16, once each.
+//
+// What bounds it, measured on GB300 (copy 6.78 TB/s):
+//  - DeepSeek-V3-shaped decode (256 experts, 32 rows each, 6.0 GB of 4-bit
+//    weights): 890 us, 6.9 TB/s: the weights' reading (bf16: 3325 us).
+//  - Mixtral-shaped batch (8192 rows over 8 experts, H 4096, I 14336): 424 to 445
+//    us alone, 6.5 to 6.8 PFLOP/s; 477 to 485 after some tenths of a second, when
+//    the power limit lowers the clock (bf16: 1.79 to 1.87 ms).  A stage's
+//    instructions take 512 cycles (its bytes from the L2 come at 15 TB/s), 1132
+//    stages a pair 300 us; the rest is 0.6 us between two tiles, 9 us until the
+//    first is multiplied, 6 between a and y, and y's last round, in which half of
+//    the pairs have no tile.  Tensor pipe active 69 % of the cycles at a quarter of
+//    the rows.
+//  - One token over two Mixtral-shaped experts (187 MB): 42 us, of 27.6: the wait
+//    between a and y, and joining y's parts, about 5 us each, and the start.
+//    Bringing Wd into the L2 during the wait cost 1.5 us.
+//  - Few blocks of contraction (H or I below 1024) and many tokens: the epilogue,
+//    4 us for a tile of 256 x 256.  More epilogue warps (12 or 16) were slower.
+//  - Tiny calls: latency, as moe_ffn.cu.
 #include <mutex>
 
 #include "moe_mxfp4.cuh"

@@ -15,10 +15,17 @@
 // codes, no exchange for the maximum; four neighbouring lanes join their scale
 // bytes into one word.  Lanes are dealt out over the rows' blocks, each row's
 // rounded up to whole words of 4, so that short rows fill the warps as long ones
-// do; a lane has UNROLL blocks in flight.  Where counts say which rows exist,
+// do; a lane has kUnroll blocks in flight.  Where counts say which rows exist,
 // those are numbered through by a prefix sum in shared memory, so that empty
 // places cost nothing.  The dispatch reads a token's block once and writes its
 // bytes and scales to its K rows.
+//
+// Measured on GB300 (copy 6.78 TB/s): 939.5 M elements of gate and up weights
+// quantised in 346 us (6.9 TB/s), read back in 395 (6.0 TB/s); with one block in
+// flight per lane both 778 us together, with two 743, with four 757.  DeepSeek-V3-shaped
+// decode dispatch, 1024 tokens to 8 rows each: 11.5 us for 46 MB, its rows read back
+// 27 us for 148 MB.  With four lanes to a block (two shuffles for the maximum, 4-byte
+// stores) the same took 872 us and 47 us together.
 #include "moe_mxfp4.cuh"
 #include "moe_rows.cuh"
 
@@ -141,9 +148,9 @@ __device__ __forceinline__ Place first_place(int nbp) {
 }
 __device__ __forceinline__ int64_t grid_lanes() { return (int64_t)gridDim.x * kMxThreads; }
 
-// Calls body(places, exists, experts, rows) for UNROLL places of every lane at a
-// time until the warp has none left: rows of the experts' buffers, the populated
-// ones alone with counts.
+// Calls body(experts, rows, blocks, exists, blocks of a row) for kUnroll places of
+// every lane at a time until the warp has none left: rows of the experts' buffers,
+// the populated ones alone with counts.
 template <bool COUNTED, typename Body>
 __device__ __forceinline__ void for_rows(const Mxfp4Rows &m, const int32_t *counts, int E, const Body &body) {
   __shared__ int32_t s_prefix[COUNTED ? kMaxExperts + 1 : 1];
