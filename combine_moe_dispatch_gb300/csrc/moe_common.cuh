@@ -284,11 +284,6 @@ __device__ __forceinline__ void named_sync(uint32_t id, uint32_t n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
-// Arrive at barrier `id` of `n` threads without waiting.
-__device__ __forceinline__ void named_arrive(uint32_t id, uint32_t n) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
-
 // named_sync that also returns the AND of `pred` over the n threads.
 __device__ __forceinline__ bool named_sync_and(uint32_t id, uint32_t n, bool pred) {
   uint32_t r;

@@ -267,6 +267,11 @@ struct Schedule {
   }
 };
 
+// Arrive at barrier `id` of `n` threads without waiting.
+__device__ __forceinline__ void named_arrive(uint32_t id, uint32_t n) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
 // Wait for phase `parity` of the barrier, for `limit` ns at most and a
 // bounded number of polls.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t limit) {
