@@ -423,9 +423,8 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
         if (gate) {
           // Through shared memory, so that a lane gets 16 features of one token: half
           // of a block, whose largest magnitude is then one exchange away, and four
-          // lanes the token's 64, a whole sector of codes.  (With a
-          // lane per feature and the maximum over the warp's lanes the chunk took
-          // twice as long.)
+          // lanes the token's 64, a whole sector of codes.  (With a lane per feature
+          // and the maximum over the warp's lanes the chunk took twice as long.)
           float *const own = staged + wq * 32 + lane;
 #pragma unroll
           for (int i = 0; i < 32; ++i) own[i * kStagedRow] = __uint_as_float(v[i]);
@@ -486,7 +485,8 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
         }
       };
       if (more) {
-        ok = wait_bar(tm_full + 8 * buf, (it >> 1) & 1u, limit);
+        // (the warp decides as one: it reads tensor memory next)
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(tm_full + 8 * buf, (it >> 1) & 1u, limit));
         tc::fence_after();
       }
       const uint32_t src = tmem + ((uint32_t)(wq * 32) << 16) + (buf ? kAcc1 : kAcc0);
