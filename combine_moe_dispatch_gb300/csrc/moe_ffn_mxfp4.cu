@@ -38,8 +38,8 @@
 // What bounds it, measured on GB300 (copy 6.78 TB/s):
 //  - DeepSeek-V3-shaped decode (256 experts, 32 rows each, 6.0 GB of 4-bit
 //    weights): 890 us, 6.9 TB/s: the weights' reading (bf16: 3325 us).
-//  - Mixtral-shaped batch (8192 rows over 8 experts, H 4096, I 14336): 424 to 445
-//    us alone, 6.5 to 6.8 PFLOP/s; 477 to 485 after some tenths of a second, when
+//  - Mixtral-shaped batch (8192 rows over 8 experts, H 4096, I 14336): 416 to 445
+//    us alone, 6.5 to 7.0 PFLOP/s; 477 to 485 after some tenths of a second, when
 //    the power limit lowers the clock (bf16: 1.79 to 1.87 ms).  A stage's
 //    instructions take 512 cycles (its bytes from the L2 come at 15 TB/s), 1132
 //    stages a pair 300 us; the rest is 0.6 us between two tiles, 9 us until the
