@@ -113,18 +113,6 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&f)[8]) {
       : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
   return r;
 }
-// The same of 4 values.
-__device__ __forceinline__ uint32_t e2m1x4(const float (&f)[4]) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 a, b, z;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.u8.u32 z, 0;\n\t"
-      "mov.b32 %0, {a, b, z, z};\n\t}"
-      : "=r"(r)
-      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]));
-  return r;
-}
 #endif
 
 }  // namespace moe

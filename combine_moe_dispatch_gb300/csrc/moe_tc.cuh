@@ -235,7 +235,10 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
 // k, into columns [to, to + 4) and [to + 4, to + 8), and `tiles` (1 to 3) of B's,
 // 128 rows each, into [to + 8, to + 20) and [to + 20, to + 32), 4 columns a
 // tile.  In shared memory the tiles of 128 k follow one another, those of the next
-// 128 rows come after.  `second_k`: the stage has more than 128 k.
+// 128 rows come after.  `second_k`: the stage has more than 128 k.  Called by the
+// warp that issues the matrix instructions: the tensor core takes one thread's copies
+// and instructions in the order of their issue, so that the columns are written again
+// for the next stage without a wait.
 __device__ __forceinline__ void load_scales(uint32_t to, uint64_t a, uint64_t b, uint32_t second_k,
                                             uint32_t tiles) {
   asm volatile("{\n\t.reg .pred e, ek, e1, e2, f1, f2;\n\t"
