@@ -23,8 +23,8 @@
 // Measured on GB300 (copy 6.78 TB/s): 939.5 M elements of gate and up weights
 // quantised in 346 us (6.9 TB/s), read back in 395 (6.0 TB/s); with one block in
 // flight per lane both 778 us together, with two 743, with four 757.  DeepSeek-V3-shaped
-// decode dispatch, 1024 tokens to 8 rows each: 11.5 us for 46 MB, its rows read back
-// 27 us for 148 MB.  With four lanes to a block (two shuffles for the maximum, 4-byte
+// decode dispatch, 1024 tokens to 8 rows each: 11.2 us for 46 MB, its rows read back
+// 25 us for 148 MB.  With four lanes to a block (two shuffles for the maximum, 4-byte
 // stores) the same took 872 us and 47 us together.
 #include "moe_mxfp4.cuh"
 #include "moe_rows.cuh"
