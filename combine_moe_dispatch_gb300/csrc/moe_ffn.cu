@@ -123,7 +123,7 @@ struct RowMaps<kActGrad> {
 template <int KIND>
 struct PairParams {
   static constexpr int kKind = KIND, kBlock = kBlockK;
-  static constexpr int kTileStep = 32;
+  static constexpr int kTileStep = 32, kExpertGroups = 1;
   static constexpr int kJobs = KIND == kRest ? 3 : KIND == kForward ? 2 : 1;
   Job job[kJobs];          // kForward: a, y; kRest: dx, dWgu, dWd
   const int32_t *counts;   // [E], or null (cap rows each)

@@ -89,6 +89,13 @@ constexpr int kApart = kTileCols - kShared;                     // tiles of so m
 // 4: one token 41.9, 42.3 and 43.3 us, the Mixtral-shaped batch 462, 428 and 428.
 constexpr uint32_t kAhead = 3;
 static_assert(kAhead <= kRing, "a record's place is free when it is written");
+// Blocks of a tile of y from which on a pair holds one alone until all of a is
+// written.  Measured holding, not holding, and with all tiles of y waiting for all
+// of a: 56 blocks (Mixtral-shaped), 64 rows 117, 122 and 120 us, 1024 rows 127, 136
+// and 130, 2048 rows 158, 171 and 163; 8 blocks (DeepSeek-V3-shaped), 64 rows over
+// 256 experts 214, 206 and 211, decode 895, 887 and 891; 4 blocks, 31 uneven experts
+// 44.5, 39.1 and 43.5; one token (28 blocks) 40.8, 40.8 and 42.4.
+constexpr int kLongY = 16;
 static_assert(kShared == 32, "the epilogue reads the shared columns as one chunk");
 
 // Words of a tile's record that the matrix instructions need.
@@ -107,8 +114,18 @@ struct MxJob {
   int row_tiles, block_tiles;          // of a4's scales
 };
 
+// What is written of a, by groups of experts, so that the first experts' tiles of y
+// need not wait for the last experts' a.  In the header's reserved words past the
+// tickets; the counters of the other epoch are 0 between launches.
+constexpr int kGroupWord = kTicketWord + kMaxPairs * 2 * 4 / 32;
+struct GroupCounter {
+  uint32_t epoch;                      // which of `ready` counts this launch's
+  uint32_t ready[2][7];                // CTAs' halves of tiles of a that are written
+};
+static_assert(kGroupWord * 4 + sizeof(GroupCounter) <= sizeof(WsHeader::reserved), "the groups fit");
+
 struct MxParams {
-  static constexpr int kKind = kForward, kBlock = kBlockK, kJobs = 2;
+  static constexpr int kKind = kForward, kBlock = kBlockK, kJobs = 2, kExpertGroups = 7;
   static constexpr int kTileStep = 64;   // block scales come 128 rows at a time, from row 0 or 64 on
   MxJob job[kJobs];                    // a, y
   const int32_t *counts;               // [E], or null (cap rows each)
@@ -116,6 +133,7 @@ struct MxParams {
   float *part;                         // partial sums of split contractions
   uint32_t *tickets;                   // finished parts, 4 bits for each split tile and CTA of the pair
   UnitCounter *units;
+  GroupCounter *groups;
   int E, cap;
 };
 
@@ -197,8 +215,8 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
     // wait for it.
     Schedule<MxParams> sched(p);
     const uint32_t peer_full = tc::map_rank(rec_full, 1), peer_ring = tc::map_rank(smem + kRingOff, 1);
-    bool written = false;                    // all of a
-    const uint32_t epoch = rank == 0 ? __ldcg(&p.units->epoch) & 1u : 0u;
+    int written = -1;                        // the group of the last tile of y whose a is there, or all
+    const uint32_t epoch = rank == 0 ? __ldcg(&p.groups->epoch) & 1u : 0u;
     uint32_t c = 0;
     for (; live && rank == 0; ++c) {
       const uint32_t s = c % kRing;
@@ -209,9 +227,18 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
         ok = __all_sync(0xFFFFFFFFu, wait_bar(rec_empty + 8 * (r % kRing), (r / kRing) & 1u, limit));
         if (!ok) break;
       }
-      // one tile of y for each pair until all of a is written
-      if (c > 0 && t.need != 0 && !written) {
-        written = ok = __all_sync(0xFFFFFFFFu, wait_count(p.units->ready + epoch, (uint32_t)t.need, limit));
+      // One tile of y for each pair until its a is written, or, where y's tiles are
+      // long, all of a: a second one would be missing where a pair is still busy
+      // with a.
+      if (c > 0 && t.need != 0) {
+        if (t.nk >= kLongY) {
+          for (int g = 0; ok && written < 0 && g < MxParams::kExpertGroups; ++g)
+            ok = __all_sync(0xFFFFFFFFu, wait_count(&p.groups->ready[epoch][g], (uint32_t)sched.count_group(g), limit));
+          written = 0;
+        } else if (group_of(p, t.e) != written) {
+          written = group_of(p, t.e);
+          ok = __all_sync(0xFFFFFFFFu, wait_count(&p.groups->ready[epoch][written], (uint32_t)t.need, limit));
+        }
         if (!ok) break;
       }
       unsigned long long n = 0;
@@ -236,18 +263,18 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
         ok = __all_sync(0xFFFFFFFFu, wait_bar(rec_empty + 8 * (r % kRing), (r / kRing) & 1u, limit));
     if (rank == 0 && lane == 0 && atomicAdd(&p.units->done, 1u) == (gridDim.x >> 1) - 1) {
       // every pair knows this launch's epoch by now: the next one counts in the
-      // other counter, which nobody uses any more
+      // other counters, which nobody uses any more
       p.units->next = 0;
       p.units->done = 0;
-      p.units->ready[epoch ^ 1u] = 0;
-      p.units->epoch = epoch ^ 1u;
+      for (int g = 0; g < MxParams::kExpertGroups; ++g) p.groups->ready[epoch ^ 1u][g] = 0;
+      p.groups->epoch = epoch ^ 1u;
     }
   } else if (live && warp == 0) {
     // ---- TMA: both CTAs load their halves; bytes complete on the leader's barrier
     int s = 0;
     uint32_t ph = 0;
     const uint32_t full0 = tc::map_rank(full, 0);
-    bool written = false;                    // all of a
+    int written = -1;                        // the group of the last tile of y whose a is there
     while (ok && feed.next_uniform<kCopyWords>(t, ok)) {
       const MxJob &j = p.job[t.job];
       const uint32_t half_n = t.n >> 1;
@@ -257,9 +284,9 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
       const int n0 = t.n0 + (int)(rank * half_n), rt = t.m * 2 + (int)rank;
       // 64 gate rows and the same 64 features of up in one copy, or 128 features
       const int a0 = rt * (t.job == 0 ? 64 : 128);
-      // The first tile of y takes its first stages' weights before it waits for all
-      // of a.
-      const int early = t.need != 0 && !written ? min(t.nk, kStages) : 0;
+      // A group's first tile of y takes its first stages' weights before it waits for
+      // the group's a.
+      const int early = t.need != 0 && group_of(p, t.e) != written ? min(t.nk, kStages) : 0;
       for (int kb = 0; ok && kb < early; ++kb) {
         const int at = s + kb < kStages ? s + kb : s + kb - kStages;
         ok = __all_sync(0xFFFFFFFFu, wait_bar(empty + 8 * at, ph ^ (s + kb < kStages ? 1u : 0u), limit));
@@ -271,7 +298,8 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
       }
       if (!ok) break;
       if (early > 0) {
-        written = ok = __all_sync(0xFFFFFFFFu, wait_count(p.units->ready + t.epoch, (uint32_t)t.need, limit));
+        written = group_of(p, t.e);
+        ok = __all_sync(0xFFFFFFFFu, wait_count(&p.groups->ready[t.epoch][written], (uint32_t)t.need, limit));
         if (!ok) break;
       }
       for (int kb = 0; kb < t.nk; ++kb) {
@@ -398,7 +426,7 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
         if (!ok) break;
         tc::fence_async_global();
         __threadfence();
-        if (lane == 0) atomicAdd(p.units->ready + t.epoch, 1u);
+        if (lane == 0) atomicAdd(&p.groups->ready[t.epoch][group_of(p, t.e)], 1u);
       }
       feed.leave();
     }
@@ -583,7 +611,7 @@ ffn_mxfp4_kernel(const __grid_constant__ MxParams p) {
         named_sync(3, 32 * kOutWarps);
         if (threadIdx.x == 128) {
           __threadfence();
-          atomicAdd(p.units->ready + t.epoch, 1u);
+          atomicAdd(&p.groups->ready[t.epoch][group_of(p, t.e)], 1u);
         }
       }
       ++it;
@@ -679,6 +707,7 @@ cudaError_t launch_ffn_mxfp4(const FfnMxfp4Params &f, cudaStream_t stream) {
   p.part = f.part;
   p.tickets = f.hdr->reserved + kTicketWord;
   p.units = reinterpret_cast<UnitCounter *>(f.hdr->reserved + kUnitWord);
+  p.groups = reinterpret_cast<GroupCounter *>(f.hdr->reserved + kGroupWord);
   p.E = f.E;
   p.cap = f.cap;
   MxJob &gu = p.job[0], &d = p.job[1];

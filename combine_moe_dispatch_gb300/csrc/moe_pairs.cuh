@@ -70,6 +70,15 @@ static_assert(kUnitWord * 4 + sizeof(UnitCounter) <= kTicketWord * 4, "the count
 static_assert(offsetof(WsHeader, reserved) % 8 == 4, "the unit counter is 8-byte aligned");
 static_assert(kMaxSplit < 16 && kTicketWord + kMaxPairs * 2 * 4 / 32 <= 55, "the tickets fit");
 
+// Where P::kExpertGroups is above 1, the experts form so many groups, in order, and
+// a tile of y waits for the tiles of a of its expert's group alone.
+template <class P>
+__device__ __forceinline__ int group_of(const P &p, int e) { return e * P::kExpertGroups / p.E; }
+template <class P>
+__device__ __forceinline__ int group_start(const P &p, int g) {
+  return (g * p.E + P::kExpertGroups - 1) / P::kExpertGroups;
+}
+
 template <class P>
 __device__ __forceinline__ int rows_of(const P &p, int e) {
   if (!p.counts) return p.cap;
@@ -118,8 +127,9 @@ struct Schedule {
   int split, part_cols;    // parts of the others, columns of a part's sums
   int row;                 // the row product that is being dealt out,
   int64_t first;           // its first unit,
-  int need;                // and what its tiles wait for
-  __device__ __forceinline__ explicit Schedule(const P &p_) : p(p_), row(0), first(0), need(0) {
+  int need;                // and what its tiles wait for (one group: all of a)
+  int group, group_need;   // several: the group counted last
+  __device__ __forceinline__ explicit Schedule(const P &p_) : p(p_), row(0), first(0), need(0), group(-1), group_need(0) {
     start();
   }
   __device__ __forceinline__ void start() {
@@ -226,6 +236,8 @@ struct Schedule {
     o.n = (o.cols + 31) & ~31;
     const int nk = (p.job[KIND == kForward ? row : 0].K + kBlockK - 1) / kBlockK;
     o.need = need;
+    if constexpr (P::kExpertGroups > 1)
+      if (row == 1) o.need = count_group(group_of(p, o.e));
     o.k0 = 0;
     o.nk = nk;
     o.split = cut ? split : 1;
@@ -239,6 +251,19 @@ struct Schedule {
       o.nk = nk * (o.part + 1) / split - o.k0;
     }
     return true;
+  }
+  // Halves of tiles of a of a group's experts.
+  __device__ __forceinline__ int count_group(int g) {
+    if (g != group) {
+      group = g;
+      const int end = group_start(p, group + 1);
+      int tiles = 0;
+      for (int x = group_start(p, group) + (threadIdx.x & 31); x < end; x += 32) tiles += token_tiles(rows_of(p, x));
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, d);
+      group_need = (int)(2u * (unsigned)tiles * (unsigned)p.job[0].mt);
+    }
+    return group_need;
   }
   __device__ __forceinline__ bool find_weight(int64_t t, Tile &o) {
     o.job = 1;
