@@ -5,11 +5,11 @@
 // (blocks of 32 elements with a power of two each):
 //   h = x Wgu^T (gate | up),  a = SiLU(gate) * up,  a4 = MXFP4(a),  y = a4 Wd^T.
 //
-// How: one launch.  The order of the work, the pairs of CTAs, their warps' roles
-// and the wait between a and y are moe_ffn.cu's (moe_pairs.cuh): weights' output
-// features on the 256-row side, the expert's tokens on the column side, a ring of
-// stages filled by TMA, tcgen05.mma.cta_group::2, accumulators in tensor memory
-// two tiles deep, eight epilogue warps.  What 4 bits change:
+// How: one launch.  The order of the work, the pairs of CTAs and their warps' roles
+// are moe_ffn.cu's (moe_pairs.cuh): weights' output features on the 256-row side,
+// the expert's tokens on the column side, a ring of stages filled by TMA,
+// tcgen05.mma.cta_group::2, accumulators in tensor memory two tiles deep, eight
+// epilogue warps.  What 4 bits change:
 //  - A stage is 256 k (128 bytes of a row, as 64 k of bf16 are): 16 KB of weights
 //    per CTA, up to 16 KB of tokens, 1 KB of the weights' scales and up to 3 KB of
 //    the tokens'.  The scales stand in memory in the tiles that a copy into tensor
@@ -28,27 +28,28 @@
 //    them; the two epilogue groups agree only where a tile is cut; an expert's
 //    tokens are dealt out to its tiles in steps of 64 (a last tile of a few tokens
 //    takes 0.2 us a stage however few they are, a full one 0.28).  Batch of 8192
-//    rows, step by step: lanes per feature and a maximum by shuffles 536 us; no
-//    fence in the epilogue 479; lanes per token 447; groups apart and weights of y
+//    rows, step by step: four features a lane and a maximum over eight lanes 536 us;
+//    no fence in the epilogue 479; lanes per token 447; groups apart and weights of y
 //    ahead of its wait 441; even tiles 433; whole sectors of codes 424.
+//  - Tiles of y wait for a of their own group of experts, of seven, instead of all of
+//    a (31 uneven experts 43.5 us, so 39.1; kLongY).
 //
 // Rounding: products of E2M1 numbers and powers of two, summed in binary32; a is
 // rounded to MXFP4 from binary32, y to bf16, once each.
 //
 // What bounds it, measured on GB300 (copy 6.78 TB/s):
 //  - DeepSeek-V3-shaped decode (256 experts, 32 rows each, 6.0 GB of 4-bit
-//    weights): 890 us, 6.9 TB/s: the weights' reading (bf16: 3325 us).
-//  - Mixtral-shaped batch (8192 rows over 8 experts, H 4096, I 14336): 416 to 445
-//    us alone, 6.5 to 7.0 PFLOP/s; 477 to 485 after some tenths of a second, when
+//    weights): 887 us, 6.9 TB/s: the weights' reading (bf16: 3325 us).
+//  - Mixtral-shaped batch (8192 rows over 8 experts, H 4096, I 14336): 414 to 430
+//    us alone, 6.7 to 7.0 PFLOP/s; 466 to 483 after some tenths of a second, when
 //    the power limit lowers the clock (bf16: 1.79 to 1.87 ms).  A stage's
 //    instructions take 512 cycles (its bytes from the L2 come at 15 TB/s), 1132
 //    stages a pair 300 us; the rest is 0.6 us between two tiles, 9 us until the
-//    first is multiplied, 6 between a and y, and y's last round, in which half of
-//    the pairs have no tile.  Tensor pipe active 69 % of the cycles at a quarter of
-//    the rows.
-//  - One token over two Mixtral-shaped experts (187 MB): 42 us, of 27.6: the wait
-//    between a and y, and joining y's parts, about 5 us each, and the start.
-//    Bringing Wd into the L2 during the wait cost 1.5 us.
+//    first is multiplied, and y's last round, in which half of the pairs have no
+//    tile.  Tensor pipe active 69 % of the cycles at a quarter of the rows.
+//  - One token over two Mixtral-shaped experts (187 MB): 40.7 us, of 27.6: the
+//    second expert's wait between a and y, and joining y's parts, 4 to 5 us each,
+//    and the start.  Bringing Wd into the L2 during the wait changed nothing.
 //  - Few blocks of contraction (H or I below 1024) and many tokens: the epilogue,
 //    4 us for a tile of 256 x 256.  More epilogue warps (12 or 16) were slower.
 //  - Tiny calls: latency, as moe_ffn.cu.
@@ -86,7 +87,8 @@ constexpr int kShared = (int)(kAcc0 + kTileCols - kAcc1);       // a multiple of
 constexpr int kApart = kTileCols - kShared;                     // tiles of so many columns share none
 // Tiles announced ahead, less than the ring holds: one taken early cannot go to a
 // pair that is free sooner, one taken late comes too late.  Measured with 2, 3 and
-// 4: one token 41.9, 42.3 and 43.3 us, the Mixtral-shaped batch 462, 428 and 428.
+// 4: one token 41.9, 42.3 and 43.3 us, the Mixtral-shaped batch 462, 428 and 428 (all
+// of a waited for).
 constexpr uint32_t kAhead = 3;
 static_assert(kAhead <= kRing, "a record's place is free when it is written");
 // Blocks of a tile of y from which on a pair holds one alone until all of a is
