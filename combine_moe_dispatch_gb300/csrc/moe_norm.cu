@@ -5,7 +5,7 @@
 //   s = bf16(x + residual)                    (s = x without a residual)
 //   y = s rstd gain,  rstd = 1 / sqrt(mean(s^2) + eps)
 // y rounded to bf16 and, from the same unrounded values, to E4M3 with one scale
-// per 128 elements (amax/448, the rule of the fp8 dispatch); and
+// per 128 elements (amax/448, the rule of the fp8 dispatch; NaN if one of them is); and
 //   u = s rstd,  g = dy gain
 //   d_x = rstd (g - u mean(g u)) + d_sum,     d_gain = sum over rows of dy u
 // from dy, the gradient d_sum that arrives at s by the residual stream, and s.
@@ -94,10 +94,28 @@ __device__ __forceinline__ float row_sum(float v, float *s, int warp) {
   return t;
 }
 
-// A half-warp's 128 values -> E4M3 bytes and their scale.  All 32 lanes call it.
+// Largest |f| of a half-warp's 128 values, NaN if one of them is: one NaN in a row
+// makes all of its y NaN, which the 8 bits have to say as the bf16 output does.  (The
+// shared half_warp_amax passes over NaN.)  All 32 lanes call it.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float half_warp_amax_nan(const float (&f)[8]) {
+  float amax = fabsf(f[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) amax = max_nan(amax, fabsf(f[i]));
+#pragma unroll
+  for (int off = 8; off >= 1; off >>= 1) amax = max_nan(amax, __shfl_xor_sync(kFull, amax, off));
+  return amax;
+}
+
+// A half-warp's 128 values -> E4M3 bytes and their scale; with a NaN among them
+// the scale and every byte (0x7F, any sign) are NaN.  All 32 lanes call it.
 __device__ __forceinline__ void store_fp8(const NormParams &p, int64_t row, int chunk, bool in, int nb,
                                           const float (&f)[8]) {
-  const float amax = half_warp_amax(f);
+  const float amax = half_warp_amax_nan(f);
   const bool fast = amax >= 0x1p-120f && amax <= 3.4028234e38f;
   const float scale[1] = {fast ? div448_fast(amax) : __fdiv_rn(amax, 448.0f)};
   const bool zero[1] = {amax == 0.0f};

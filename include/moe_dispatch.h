@@ -477,7 +477,10 @@ moe_status moe_clip_grad_norm(const moe_grad_tensor *tensors, int32_t num_tensor
  * computed; y is rounded once, to bf16, and from the same unrounded values to
  * E4M3 by the rule of moe_dispatch ("Lower latency and higher throughput with
  * multi-node DeepSeek deployment", Quantization: scale = amax / 448 per 128
- * elements, all-zero block: scale 0 and q = 0).
+ * elements, all-zero block: scale 0 and q = 0).  A NaN or an infinity in a row of
+ * s makes y NaN where the formula does (a NaN everywhere, an infinity at its own
+ * place, the rest of that row being 0); a block with a NaN among its y has the
+ * scale NaN and NaN bytes, in 8 bits too.
  * In:   x [N, H] bf16; residual [N, H] bf16, or NULL; gain [H] bf16; eps >= 0.
  * Out:  sum [N, H] bf16, receives s: NULL without a residual, or when it is not
  *       wanted; may be x or residual itself (in place).
