@@ -21,10 +21,10 @@
 // stored once per block, and a second launch adds the blocks' shares, all in an
 // order that depends on the sizes and the device alone.  Rows of more than 16384
 // elements do not fit the registers: a block then reads its row twice (the second
-// time from the caches; 2048 x 20480: forward 70 us, backward 142).
+// time from the caches; 2048 x 20480: forward 70 us, backward 134).
 //
 // What bounds it, measured on GB300 (copy 6.78 TB/s): memory.  8192 x 7168 with a
-// residual and both outputs 86.4 us, 6.1 TB/s; backward with d_sum 83.7 us, of which
+// residual and both outputs 88 us, 6.0 TB/s; backward with d_sum 84 us, of which
 // the rows are 76 (6.2 TB/s) and adding 304 shares of 7168 columns 6.  Blocks
 // per SM: 4 of 64 registers forward (3 of 80: 87.8 us, 5 of 48: 96.5), 2 of 128
 // backward (1: 108 us, 3: 168, which spill).  One token: 2.0 us on the GPU, 4.2 through
@@ -94,6 +94,59 @@ __device__ __forceinline__ float row_sum(float v, float *s, int warp) {
   return t;
 }
 
+// Squares of elements below 2^-63 lose bits in binary32, and vanish below 2^-75.  With
+// eps of 2^-90 or more that is below mean(s^2) + eps's rounding; a smaller eps (0 among
+// them) leaves such a row to its own elements.  Then every row is first multiplied by
+// a power of two, `lift`, that brings its largest magnitude to 1 to 2 (to 2^-7 at
+// least, from bf16's subnormals), or stops where eps lift^2 is about 1.  That is
+// exact, and with eps lift^2 for eps u and y are the same; the backward pass
+// multiplies by lift once more.  Rows of 1 and more stay as they are (lift 1), so
+// that all calls end at the same sum of squares.  eps is the launch's: every thread
+// takes this branch, or none.  8192 x 7168, both outputs: 98.5 us, 88 with an ordinary
+// eps; backward with d_sum 92 and 84.
+constexpr float kSmallEps = 0x1p-90f;
+__device__ __forceinline__ float row_lift(uint32_t most, float eps) {
+  const int row = max((int)(most >> 7), 1) - 127;        // exponent of the largest magnitude
+  const int half = eps > 0.0f ? ((int)(__float_as_uint(eps) >> 23) - 127) >> 1 : -126;
+  return __uint_as_float((uint32_t)(127 - min(max(row, half), 0)) << 23);
+}
+__device__ __forceinline__ uint32_t most8(uint32_t m, const uint4 &v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
+  return m;
+}
+// The largest of a row's WPR warps.
+template <int WPR>
+__device__ __forceinline__ uint32_t row_most(uint32_t m, uint32_t *s, int warp) {
+  m = __reduce_max_sync(kFull, m);
+  if (WPR == 1) return m;
+  __syncthreads();                           // the row before has been read
+  if ((threadIdx.x & 31) == 0) s[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < WPR; ++i) m = max(m, s[warp / WPR * WPR + i]);
+  return m;
+}
+// The row's chunks multiplied by its lift, which is returned; eps becomes eps lift^2.
+template <int C, int WPR>
+__device__ __forceinline__ float lift_row(uint4 (&v)[C], float &eps, uint32_t *s, int warp) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int u = 0; u < C; ++u) m = most8(m, v[u]);
+  const float lift = row_lift(row_most<WPR>(m, s, warp), eps);
+  eps = eps * lift * lift;
+#pragma unroll
+  for (int u = 0; u < C; ++u) {
+    float f[8];
+    unpack8(v[u], f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= lift;
+    v[u] = pack8(f);
+  }
+  return lift;
+}
+
 // Largest |f| of a half-warp's 128 values, NaN if one of them is: one NaN in a row
 // makes all of its y NaN, which the 8 bits have to say as the bf16 output does.  (The
 // shared half_warp_amax passes over NaN.)  All 32 lanes call it.
@@ -136,6 +189,7 @@ __global__ void __launch_bounds__(32 * WARPS, C == 1 ? 6 : 32 / WARPS)
 norm_kernel(NormParams p) {
   constexpr int kRows = WARPS / WPR;
   __shared__ float s_sum[2][WARPS];
+  __shared__ uint32_t s_most[WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = (warp % WPR) * 32 + lane, cpr = p.H / 8, nb = (p.H + 127) / 128;
   pdl_wait_for_previous();
@@ -165,6 +219,8 @@ norm_kernel(NormParams p) {
         s[u] = row < p.N && c < cpr ? load16(p.x, row * cpr + c) : make_uint4(0, 0, 0, 0);
       }
     }
+    float eps = p.eps;
+    if (p.eps < kSmallEps) lift_row<C, WPR>(s, eps, s_most, warp);
     float sq = 0.0f;
 #pragma unroll
     for (int u = 0; u < C; ++u) {
@@ -173,7 +229,7 @@ norm_kernel(NormParams p) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) sq = fmaf(f[i], f[i], sq);
     }
-    const float rstd = rsqrtf(row_sum<WPR>(sq, s_sum[buf], warp) / (float)p.H + p.eps);
+    const float rstd = rsqrtf(row_sum<WPR>(sq, s_sum[buf], warp) / (float)p.H + eps);
     buf ^= 1;
 #pragma unroll
     for (int u = 0; u < C; ++u) {
@@ -195,6 +251,7 @@ template <bool RES, bool FP8>
 __global__ void __launch_bounds__(kNormThreads)
 norm_long_kernel(NormParams p) {
   __shared__ float s_sum[2][kNormWarps];
+  __shared__ uint32_t s_most[kNormWarps];
   const int warp = threadIdx.x >> 5;
   const int cpr = p.H / 8, nb = (p.H + 127) / 128;
   pdl_wait_for_previous();
@@ -205,15 +262,24 @@ norm_long_kernel(NormParams p) {
       if (RES) s = add8(s, reinterpret_cast<const uint4 *>(p.residual)[row * cpr + c]);
       return s;
     };
+    float lift = 1.0f;
+    if (p.eps < kSmallEps) {
+      uint32_t m = 0;
+      for (int c = threadIdx.x; c < cpr; c += kNormThreads) m = most8(m, read(c));
+      lift = row_lift(row_most<kNormWarps>(m, s_most, warp), p.eps);
+    }
     float sq = 0.0f;
 #pragma unroll 4
     for (int c = threadIdx.x; c < cpr; c += kNormThreads) {
       float f[8];
       unpack8(read(c), f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sq = fmaf(f[i], f[i], sq);
+      for (int i = 0; i < 8; ++i) {
+        const float v = f[i] * lift;
+        sq = fmaf(v, v, sq);
+      }
     }
-    const float rstd = rsqrtf(row_sum<kNormWarps>(sq, s_sum[buf], warp) / (float)p.H + p.eps);
+    const float rstd = rsqrtf(row_sum<kNormWarps>(sq, s_sum[buf], warp) / (float)p.H + p.eps * lift * lift);
     buf ^= 1;
     for (int cb = 0; cb < cpr; cb += kNormThreads) {      // all lanes, for the half-warps' maxima
       const int c = cb + threadIdx.x;
@@ -223,7 +289,7 @@ norm_long_kernel(NormParams p) {
       unpack8(s, f);
       unpack8(in ? __ldg(reinterpret_cast<const uint4 *>(p.gain) + c) : make_uint4(0, 0, 0, 0), g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * g[i];
+      for (int i = 0; i < 8; ++i) f[i] = f[i] * lift * rstd * g[i];
       if (RES && p.sum && in) reinterpret_cast<uint4 *>(p.sum)[row * cpr + c] = s;
       if ((!FP8 || p.y) && in) reinterpret_cast<uint4 *>(p.y)[row * cpr + c] = pack8(f);
       if (FP8) store_fp8(p, row, c, in, nb, f);
@@ -231,11 +297,15 @@ norm_long_kernel(NormParams p) {
   }
 }
 
-template <int C, int WPR, bool DSUM, int WARPS = kNormWarps>
+// LIFT: eps is below kSmallEps.  A variant of its own, since this kernel has no
+// register left: with the branch and the factor in the one kernel 2048 x 16384 took 60.8
+// us, so 53.5; 8192 x 4096 51.8, so 49.6.
+template <int C, int WPR, bool DSUM, bool LIFT, int WARPS = kNormWarps>
 __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
 norm_backward_kernel(NormBackwardParams p) {
   constexpr int kRows = WARPS / WPR;
   __shared__ float s_sum[2][2][WARPS];
+  __shared__ uint32_t s_most[LIFT ? WARPS : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = (warp % WPR) * 32 + lane, cpr = p.H / 8;
   pdl_wait_for_previous();
@@ -256,6 +326,8 @@ norm_backward_kernel(NormBackwardParams p) {
       dy[u] = in ? load16(p.d_y, row * cpr + c) : make_uint4(0, 0, 0, 0);
       if (DSUM) ds[u] = in ? load16(p.d_sum, row * cpr + c) : make_uint4(0, 0, 0, 0);
     }
+    float eps = p.eps, lift = 1.0f;
+    if (LIFT) lift = lift_row<C, WPR>(s, eps, s_most, warp);
     float sq = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int u = 0; u < C; ++u) {
@@ -286,7 +358,7 @@ norm_backward_kernel(NormBackwardParams p) {
       }
       buf ^= 1;
     }
-    const float rstd = rsqrtf(sq / (float)p.H + p.eps);
+    const float rstd = rsqrtf(sq / (float)p.H + eps);
     const float mean = dot * rstd / (float)p.H;             // of g u
 #pragma unroll
     for (int u = 0; u < C; ++u) {
@@ -300,7 +372,9 @@ norm_backward_kernel(NormBackwardParams p) {
       for (int i = 0; i < 8; ++i) {
         const float un = f[i] * rstd;
         if (row < p.N) acc[u][i] = fmaf(d[i], un, acc[u][i]);
-        f[i] = rstd * (d[i] * g[i] - un * mean);
+        f[i] = d[i] * g[i] - un * mean;
+        if (LIFT) f[i] *= lift;
+        f[i] *= rstd;
         if (DSUM) f[i] += e[i];
       }
       if (row < p.N && c < cpr) reinterpret_cast<uint4 *>(p.d_x)[row * cpr + c] = pack8(f);
@@ -341,6 +415,7 @@ template <bool DSUM>
 __global__ void __launch_bounds__(kNormThreads)
 norm_backward_long_kernel(NormBackwardParams p) {
   __shared__ float s_sum[2][2][kNormWarps];
+  __shared__ uint32_t s_most[kNormWarps];
   const int warp = threadIdx.x >> 5, cpr = p.H / 8;
   float4 *part = reinterpret_cast<float4 *>(p.part + (int64_t)blockIdx.x * p.H);
   pdl_wait_for_previous();
@@ -349,6 +424,12 @@ norm_backward_long_kernel(NormBackwardParams p) {
     const uint4 *s = reinterpret_cast<const uint4 *>(p.sum) + row * cpr;
     const uint4 *dy = reinterpret_cast<const uint4 *>(p.d_y) + row * cpr;
     const uint4 *gain = reinterpret_cast<const uint4 *>(p.gain);
+    float lift = 1.0f;
+    if (p.eps < kSmallEps) {
+      uint32_t m = 0;
+      for (int c = threadIdx.x; c < cpr; c += kNormThreads) m = most8(m, s[c]);
+      lift = row_lift(row_most<kNormWarps>(m, s_most, warp), p.eps);
+    }
     float sq = 0.0f, dot = 0.0f;
 #pragma unroll 4
     for (int c = threadIdx.x; c < cpr; c += kNormThreads) {
@@ -358,14 +439,15 @@ norm_backward_long_kernel(NormBackwardParams p) {
       unpack8(__ldg(gain + c), g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        sq = fmaf(f[i], f[i], sq);
-        dot = fmaf(d[i] * g[i], f[i], dot);
+        const float v = f[i] * lift;
+        sq = fmaf(v, v, sq);
+        dot = fmaf(d[i] * g[i], v, dot);
       }
     }
     sq = row_sum<kNormWarps>(sq, s_sum[buf][0], warp);
     dot = row_sum<kNormWarps>(dot, s_sum[buf][1], warp);
     buf ^= 1;
-    const float rstd = rsqrtf(sq / (float)p.H + p.eps);
+    const float rstd = rsqrtf(sq / (float)p.H + p.eps * lift * lift);
     const float mean = dot * rstd / (float)p.H;
     for (int c = threadIdx.x; c < cpr; c += kNormThreads) {
       float f[8], d[8], g[8], e[8];
@@ -381,9 +463,9 @@ norm_backward_long_kernel(NormBackwardParams p) {
       float *acc = reinterpret_cast<float *>(a);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float un = f[i] * rstd;
+        const float un = f[i] * lift * rstd;
         acc[i] = fmaf(d[i], un, acc[i]);
-        f[i] = rstd * (d[i] * g[i] - un * mean);
+        f[i] = rstd * ((d[i] * g[i] - un * mean) * lift);
         if (DSUM) f[i] += e[i];
       }
       part[2 * c] = a[0];
@@ -454,7 +536,8 @@ int backward_blocks(const void *kern, int threads, int64_t warps) {
 
 template <int C, int WPR, bool DSUM, int WARPS = kNormWarps>
 cudaError_t launch_backward_rows(const NormBackwardParams &p, int &parts, cudaStream_t stream) {
-  const auto kern = norm_backward_kernel<C, WPR, DSUM, WARPS>;
+  const auto kern = p.eps < kSmallEps ? norm_backward_kernel<C, WPR, DSUM, true, WARPS>
+                                      : norm_backward_kernel<C, WPR, DSUM, false, WARPS>;
   parts = backward_blocks((const void *)kern, 32 * WARPS, (int64_t)p.N * WPR);
   return launch_after_previous(kern, parts, 32 * WARPS, p, stream);
 }

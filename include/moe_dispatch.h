@@ -488,9 +488,11 @@ moe_status moe_clip_grad_norm(const moe_grad_tensor *tensors, int32_t num_tensor
  *       it is not wanted: payload FP8 only.
  *       y_q [N, H] E4M3 and y_scale [N, nb] fp32 ([nb, N] for FP8_E4M3_TSCALE),
  *       nb = ceil(H / 128): payload FP8 only, not touched for BF16.
- * Uses N, H and the payload of `shape`.  A row whose squares overflow binary32
- * (elements beyond 1.8e19) comes out 0.  The bf16 arrays and y_q are 16-byte
- * aligned, y_scale 4-byte.
+ * Uses N, H and the payload of `shape`.  A row whose sum of squares passes
+ * binary32 (2^128: a root mean square of 1.8e19 / sqrt(H), 2.2e17 at H = 7168)
+ * comes out 0.  There is no such end below: elements of any size and eps down to 0
+ * give what the formula does.  (A row of zeros with eps = 0 is 0 / 0, NaN.)  The
+ * bf16 arrays and y_q are 16-byte aligned, y_scale 4-byte.
  * Errors: INVALID_ARG (null pointer, eps negative or NaN, sum without a
  *       residual, sum = y), UNSUPPORTED, ALIGNMENT, CUDA.  No workspace. */
 moe_status moe_add_rms_norm(const moe_shape *shape, const void *x, const void *residual,
@@ -503,7 +505,8 @@ moe_status moe_add_rms_norm(const moe_shape *shape, const void *x, const void *r
  *   d_gain = sum over the rows of d_y * u
  * d_x is the gradient of x and of the residual alike.  Sums are binary32, in an
  * order that depends on the sizes and the device alone.  The 8-bit output has no
- * gradient of its own.
+ * gradient of its own.  A row whose sum of squares passes binary32 has rstd 0, as
+ * in the forward call: d_x is d_sum there.
  * In:   d_y [N, H] bf16; d_sum [N, H] bf16, the gradient that arrives at s
  *       along the residual stream, or NULL; sum [N, H] bf16, the s of the
  *       forward call (x, if that had no residual); gain [H] bf16; eps.
