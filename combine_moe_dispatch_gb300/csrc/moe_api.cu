@@ -522,10 +522,16 @@ moe_status moe_clip_grad_norm(const moe_grad_tensor *tensors, int32_t num_tensor
                                (cudaStream_t)stream));
 }
 
+// The kernels count a row's elements, chunks and scale blocks in 32 bits, rounded up.
+static moe_status norm_check(const moe_shape *shape) {
+  const moe_status st = check_shape(shape);
+  return st == MOE_OK && shape->hidden >= (1 << 30) ? MOE_ERR_UNSUPPORTED : st;
+}
+
 moe_status moe_add_rms_norm(const moe_shape *shape, const void *x, const void *residual,
                             const void *gain, float eps, void *sum, void *y, void *y_q,
                             float *y_scale, void *stream) {
-  moe_status st = check_shape(shape);
+  moe_status st = norm_check(shape);
   if (st != MOE_OK) return st;
   if (!(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
   if (shape->tokens_per_rank == 0) return MOE_OK;   // empty batch: nothing to read or write
@@ -551,7 +557,7 @@ moe_status moe_add_rms_norm(const moe_shape *shape, const void *x, const void *r
 }
 
 size_t moe_norm_workspace_size(const moe_shape *shape) {
-  if (check_shape(shape) != MOE_OK) return 0;
+  if (norm_check(shape) != MOE_OK) return 0;
   const int64_t N = (int64_t)shape->num_ranks * shape->tokens_per_rank;
   const int64_t parts = N < 1 ? 1 : N < kNormMaxBlocks ? N : kNormMaxBlocks;
   return (size_t)parts * shape->hidden * sizeof(float);
@@ -561,7 +567,7 @@ moe_status moe_add_rms_norm_backward(const moe_shape *shape, const void *d_y, co
                                      const void *sum, const void *gain, float eps, void *d_x,
                                      float *d_gain, void *workspace, size_t workspace_bytes,
                                      void *stream) {
-  moe_status st = check_shape(shape);
+  moe_status st = norm_check(shape);
   if (st != MOE_OK) return st;
   if (shape->payload != MOE_PAYLOAD_BF16) return MOE_ERR_UNSUPPORTED;
   const bool empty = shape->tokens_per_rank == 0;

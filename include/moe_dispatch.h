@@ -493,6 +493,7 @@ moe_status moe_clip_grad_norm(const moe_grad_tensor *tensors, int32_t num_tensor
  * comes out 0.  There is no such end below: elements of any size and eps down to 0
  * give what the formula does.  (A row of zeros with eps = 0 is 0 / 0, NaN.)  The
  * bf16 arrays and y_q are 16-byte aligned, y_scale 4-byte.
+ * Limits: H < 2^30.
  * Errors: INVALID_ARG (null pointer, eps negative or NaN, sum without a
  *       residual, sum = y), UNSUPPORTED, ALIGNMENT, CUDA.  No workspace. */
 moe_status moe_add_rms_norm(const moe_shape *shape, const void *x, const void *residual,
@@ -514,6 +515,7 @@ moe_status moe_add_rms_norm(const moe_shape *shape, const void *x, const void *r
  *       element written (0 for an empty batch).
  * Work: moe_norm_workspace_size(shape) bytes, 16-byte aligned, of any content.
  * Two launches.  Uses N and H of `shape`; payload BF16 (UNSUPPORTED otherwise).
+ * Limits: H < 2^30.
  * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA. */
 size_t moe_norm_workspace_size(const moe_shape *shape);
 moe_status moe_add_rms_norm_backward(const moe_shape *shape, const void *d_y, const void *d_sum,
