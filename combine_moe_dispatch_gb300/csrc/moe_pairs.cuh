@@ -13,6 +13,7 @@
 #include <stddef.h>
 
 #include "moe_tc.cuh"
+#include "moe_tiles.cuh"
 
 namespace moe {
 
@@ -84,17 +85,6 @@ __device__ __forceinline__ int rows_of(const P &p, int e) {
   if (!p.counts) return p.cap;
   const int c = __ldg(p.counts + e);
   return c < 0 ? 0 : (c > p.cap ? p.cap : c);
-}
-
-// Tiles of `rows` tokens, and the columns of each but the last: as few tiles as
-// 256 columns allow, equal, a multiple of 32 (the granularity of a matrix
-// instruction's columns).  With n tiles rows > 256 (n - 1) and the columns are
-// at most 256, so that the last tile is never empty.  Where tiles start on
-// multiples of kTileStep > 32, the steps are dealt out evenly: some tiles have one
-// more than the others.
-__device__ __forceinline__ int token_tiles(int rows) { return (int)(((unsigned)rows + 255u) >> 8); }
-__device__ __forceinline__ int tile_cols(int rows, int tiles) {
-  return (int)((((unsigned)rows + tiles - 1) / tiles + 31) & ~31u);
 }
 
 struct alignas(16) Tile {
@@ -223,15 +213,9 @@ struct Schedule {
     if (nt > 1) {
       o.m = r / nt;
       const int i = r - o.m * nt;
-      if constexpr (P::kTileStep == 32) {
-        const int c = tile_cols(o.rows, nt);
-        o.n0 = i * c;
-        o.cols = min(c, o.rows - o.n0);
-      } else {
-        const int steps = (o.rows + P::kTileStep - 1) / P::kTileStep, each = steps / nt, more = steps - each * nt;
-        o.n0 = P::kTileStep * (i * each + min(i, more));
-        o.cols = min(P::kTileStep * (each + (i < more)), o.rows - o.n0);
-      }
+      const TokenTile tokens = token_tile<P::kTileStep>(o.rows, nt, i);
+      o.n0 = tokens.first;
+      o.cols = tokens.count;
     }
     o.n = (o.cols + 31) & ~31;
     const int nk = (p.job[KIND == kForward ? row : 0].K + kBlockK - 1) / kBlockK;
