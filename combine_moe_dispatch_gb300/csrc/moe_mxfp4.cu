@@ -118,8 +118,13 @@ __device__ __forceinline__ Quantised quantise(const uint32_t (&w)[16]) {
   return r;
 }
 
+// Whether the plan before failed, one answer for the whole warp: another block may
+// set the word while it is read (a dispatch's, on an entry out of range), and lanes
+// that left alone would be missing at the exchanges that follow.  One lane reads.
 __device__ __forceinline__ bool plan_failed(const WsHeader *hdr) {
-  return hdr && read_status(hdr) != MOE_OK;
+  int32_t st = MOE_OK;
+  if (hdr && (threadIdx.x & 31) == 0) st = read_status(hdr);
+  return __shfl_sync(kFull, st, 0) != MOE_OK;
 }
 
 // A lane's place among the rows' blocks, `nbp` to a row, and how it moves on by
@@ -154,12 +159,17 @@ __device__ __forceinline__ int64_t grid_lanes() { return (int64_t)gridDim.x * kM
 // the places side by side.  With them each thread block has a stretch of its own, so that a
 // lane's next expert is this one or the next few: looked up from the start for
 // every place, the rows of the DeepSeek-V3-shaped decode took 27 us to read back.
+// After a failed plan there are none.
 template <bool COUNTED, typename Body>
-__device__ __forceinline__ void for_rows(const Mxfp4Rows &m, const int32_t *counts, int E, const Body &body) {
+__device__ __forceinline__ void for_rows(const Mxfp4Rows &m, const int32_t *counts, const WsHeader *hdr, int E,
+                                         const Body &body) {
   __shared__ int32_t s_prefix[COUNTED ? kMaxExperts + 1 : 1];
+  __shared__ int32_t s_status;
   const int nb = m.cols / 32, nbp = (nb + 3) & ~3;
   if (COUNTED) {
-    count_prefix<kMxThreads>(counts, E, m.rows, s_prefix);
+    if (threadIdx.x == 0) s_status = hdr ? read_status(hdr) : MOE_OK;
+    count_prefix<kMxThreads>(counts, E, m.rows, s_prefix);   // ends with a barrier
+    if (s_status != MOE_OK) return;
     const int total = s_prefix[E];
     const int64_t places = (int64_t)total * nbp, share = (places + gridDim.x - 1) / gridDim.x;
     const int64_t rounds = (share + kMxThreads - 1) / kMxThreads;
@@ -184,6 +194,7 @@ __device__ __forceinline__ void for_rows(const Mxfp4Rows &m, const int32_t *coun
       body(e, row, b, in, nb);
     }
   } else {
+    if (plan_failed(hdr)) return;
     const int64_t total = (int64_t)E * m.rows;
     const Steps steps(grid_lanes(), nbp);
     Place p = first_place(nbp);
@@ -208,10 +219,9 @@ template <bool COUNTED, bool WIDE>
 __global__ void __launch_bounds__(kMxThreads)
 quant_kernel(QuantParams p) {
   pdl_wait_for_previous();
-  if (plan_failed(p.hdr)) return;
   const Mxfp4Rows &m = p.out;
-  for_rows<COUNTED>(m, p.counts, p.E, [&](const int (&e)[kUnroll], const int (&row)[kUnroll],
-                                          const int (&b)[kUnroll], const bool (&in)[kUnroll], int nb) {
+  for_rows<COUNTED>(m, p.counts, p.hdr, p.E, [&](const int (&e)[kUnroll], const int (&row)[kUnroll],
+                                                 const int (&b)[kUnroll], const bool (&in)[kUnroll], int nb) {
     uint32_t w[kUnroll][16];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -259,10 +269,9 @@ template <bool COUNTED, bool WIDE>
 __global__ void __launch_bounds__(kMxThreads)
 dequant_kernel(DequantParams p) {
   pdl_wait_for_previous();
-  if (plan_failed(p.hdr)) return;
   const Mxfp4Rows &m = p.in;
-  for_rows<COUNTED>(m, p.counts, p.E, [&](const int (&e)[kUnroll], const int (&row)[kUnroll],
-                                          const int (&b)[kUnroll], const bool (&in)[kUnroll], int nb) {
+  for_rows<COUNTED>(m, p.counts, p.hdr, p.E, [&](const int (&e)[kUnroll], const int (&row)[kUnroll],
+                                                 const int (&b)[kUnroll], const bool (&in)[kUnroll], int nb) {
     uint4 q[kUnroll];
     uint32_t s[kUnroll];
 #pragma unroll
