@@ -423,11 +423,44 @@ def mxfp4_scale_bytes(num_experts: int, rows: int, cols: int) -> int:
     return load_library().moe_mxfp4_scale_bytes(num_experts, rows, cols)
 
 
+_mxfp4_types = []                        # bf16, int32: torch's, looked up once
+
+
+def _mxfp4_sizes(wide, counts, q, scale):
+    """Sizes (E, rows, cols) of a call of moe_quant_mxfp4 or its inverse, which are
+    those of ``wide``; None where it would walk some array wrongly, by type, layout,
+    size or device.  (An array that is None is the library's to refuse.)"""
+    if not _mxfp4_types:
+        import torch
+        _mxfp4_types.extend((torch.bfloat16, torch.int32))
+    bf16, int32 = _mxfp4_types
+    shape, device = wide.shape, wide.get_device()         # -1: not on a GPU
+    if len(shape) != 3 or device < 0 or wide.dtype is not bf16 or not wide.is_contiguous():
+        return None
+    E, rows, cols = shape
+    if q is not None and (q.get_device() != device or q.element_size() != 1 or not q.is_contiguous() or
+                          2 * q.numel() < E * rows * cols):
+        return None
+    if scale is not None and (scale.get_device() != device or scale.element_size() != 1 or
+                              not scale.is_contiguous() or
+                              scale.numel() < (rows + 127) // 128 * ((cols + 127) // 128) * 512 * E):
+        return None
+    if counts is not None and (counts.get_device() != device or counts.dtype is not int32 or
+                               not counts.is_contiguous() or counts.numel() < E):
+        return None
+    return E, rows, cols
+
+
 def quant_mxfp4(src, expert_num_tokens, q, scale, flags: int = 0, workspace=None, stream=None,
                 check=True) -> Status:
     """moe_quant_mxfp4 of ``src`` [E, rows, cols]; ``expert_num_tokens`` (every
-    row exists) and ``workspace`` (no plan behind the counts) may be None."""
-    st = load_library().moe_quant_mxfp4(*src.shape, _ptr(src), _ptr(expert_num_tokens), flags, _ptr(q),
+    row exists) and ``workspace`` (no plan behind the counts) may be None.
+    ``src`` is bf16, ``q`` and ``scale`` of one byte an element, the counts int32,
+    all contiguous, large enough and on one GPU: others raise MoEError(INVALID_ARG)."""
+    sizes = _mxfp4_sizes(src, expert_num_tokens, q, scale)
+    if sizes is None:
+        return _check(Status.INVALID_ARG, "moe_quant_mxfp4", check)
+    st = load_library().moe_quant_mxfp4(*sizes, _ptr(src), _ptr(expert_num_tokens), flags, _ptr(q),
                                         _ptr(scale), _ptr(workspace), _stream(stream))
     return _check(st, "moe_quant_mxfp4", check)
 
@@ -435,7 +468,10 @@ def quant_mxfp4(src, expert_num_tokens, q, scale, flags: int = 0, workspace=None
 def dequant_mxfp4(q, scale, expert_num_tokens, out, flags: int = 0, workspace=None, stream=None,
                   check=True) -> Status:
     """moe_dequant_mxfp4 into ``out`` [E, rows, cols]; the rest as quant_mxfp4."""
-    st = load_library().moe_dequant_mxfp4(*out.shape, _ptr(q), _ptr(scale), _ptr(expert_num_tokens),
+    sizes = _mxfp4_sizes(out, expert_num_tokens, q, scale)
+    if sizes is None:
+        return _check(Status.INVALID_ARG, "moe_dequant_mxfp4", check)
+    st = load_library().moe_dequant_mxfp4(*sizes, _ptr(q), _ptr(scale), _ptr(expert_num_tokens),
                                           flags, _ptr(out), _ptr(workspace), _stream(stream))
     return _check(st, "moe_dequant_mxfp4", check)
 
