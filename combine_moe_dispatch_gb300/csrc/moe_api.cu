@@ -4,12 +4,11 @@
 // the stream and the caller's buffers untouched.
 #include <stdint.h>
 
-#include <mutex>
-
 #include "moe_common.cuh"
 #include "moe_ffn.cuh"
 #include "moe_mxfp4.cuh"
 #include "moe_norm.cuh"
+#include "moe_occupancy.cuh"
 #include "moe_train.cuh"
 
 namespace moe {
@@ -28,29 +27,17 @@ int device_sm_count() {
 }
 
 int occupancy_blocks(const void *kern, int threads, size_t smem) {
-  struct Entry {
-    const void *kern;
-    int dev, threads;
-    size_t smem;
-    int blocks;
-  };
-  static Entry cache[64];
-  static int used = 0;
-  static std::mutex mu;
+  static OccupancyTable table;
   int dev = 0;
   cudaGetDevice(&dev);
-  std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < used; ++i)
-    if (cache[i].kern == kern && cache[i].dev == dev && cache[i].threads == threads &&
-        cache[i].smem == smem)
-      return cache[i].blocks;
-  int v = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kern, threads, smem) != cudaSuccess || v < 1) {
-    cudaGetLastError();
-    v = 1;
-  }
-  if (used < 64) cache[used++] = Entry{kern, dev, threads, smem, v};
-  return v;
+  return table.get(kern, dev, threads, smem, [&] {
+    int v = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, kern, threads, smem) != cudaSuccess || v < 1) {
+      cudaGetLastError();
+      v = 1;
+    }
+    return v;
+  });
 }
 
 int persistent_grid(const void *kern, int threads, int64_t warp_tasks) {
