@@ -92,12 +92,18 @@ constexpr int kApart = kTileCols - kShared;                     // tiles of so m
 constexpr uint32_t kAhead = 3;
 static_assert(kAhead <= kRing, "a record's place is free when it is written");
 // Blocks of a tile of y from which on a pair holds one alone until all of a is
-// written.  Measured holding, not holding, and with all tiles of y waiting for all
-// of a: 56 blocks (Mixtral-shaped), 64 rows 117, 122 and 120 us, 1024 rows 127, 136
-// and 130, 2048 rows 158, 171 and 163; 8 blocks (DeepSeek-V3-shaped), 64 rows over
-// 256 experts 214, 206 and 211, decode 895, 887 and 891; 4 blocks, 31 uneven experts
-// 44.5, 39.1 and 43.5; one token (28 blocks) 40.8, 40.8 and 42.4.
-constexpr int kLongY = 16;
+// written: its second one would be missing where a pair is still busy with a, but
+// begins sooner.  Measured holding and not, 8 experts, H 4096, with 64, 1024, 2048 and
+// 4096 rows: 9 blocks 31.2 and 27.2, 35.6 and 31.7, 44.9 and 39.5 us; 16 blocks 43.6
+// and 41.5, 48.5 and 46.1, 61.7 and 58.6; 24 blocks 58.1 and 55.5, 63.3 and 60.8, 78.8
+// and 79.1, 110.2 and 106.6; 28 blocks 62.9 and 64.6, 69.0 and 71.2, 87.5 and 89.8, 125.2
+// and 122.3; 40 blocks 87.1 and 90.1, 94.6 and 100.9, 117.5 and 124.5, 172.4 and 172.2;
+// 56 blocks 117 and 121, 126 and 134, 157 and 170, 259 and 261.  (48 blocks go either
+// way by 1 %.)  H 7168, 64 and 1024 rows: 16 blocks 68.1 and 63.3, 75.2 and 70.3; 28
+// blocks 103.3 and 108.3, 111.2 and 115.4.  8 blocks (DeepSeek-V3-shaped), 64 rows over
+// 256 experts 214 and 206, decode 895 and 887; 4 blocks, 31 uneven experts 44.5 and
+// 39.1; one token the same at every length.
+constexpr int kLongY = 28;
 static_assert(kShared == 32, "the epilogue reads the shared columns as one chunk");
 
 // Words of a tile's record that the matrix instructions need.
@@ -120,6 +126,10 @@ struct MxJob {
 // need not wait for the last experts' a.  In the header's reserved words past the
 // tickets; the counters of the other epoch are 0 between launches.
 constexpr int kGroupWord = kTicketWord + kMaxPairs * 2 * 4 / 32;
+// Seven groups are what those words hold.  Measured with 1 (all of a), 2, 4 and 7:
+// 31 uneven experts 43.8, 40.0, 39.5 and 39.1 us; 64 rows over 256 experts 211, 205, 205
+// and 206; decode 891, 885, 886 and 887; one token 42.4, 41.3, 40.7 and 40.7; 4096 rows
+// over 128 experts (H 2048, I 768) 66.9, 64.3, 64.9 and 66.5.
 struct GroupCounter {
   uint32_t epoch;                      // which of `ready` counts this launch's
   uint32_t ready[2][7];                // CTAs' halves of tiles of a that are written
