@@ -32,7 +32,7 @@
 //    no fence in the epilogue 479; lanes per token 447; groups apart and weights of y
 //    ahead of its wait 441; even tiles 433; whole sectors of codes 424.
 //  - Tiles of y wait for a of their own group of experts, of seven, instead of all of
-//    a (31 uneven experts 43.5 us, so 39.1; kLongY).
+//    a (31 uneven experts 43.8 us, so 39.1; GroupCounter, kLongY).
 //
 // Rounding: products of E2M1 numbers and powers of two, summed in binary32; a is
 // rounded to MXFP4 from binary32, y to bf16, once each.
@@ -40,18 +40,23 @@
 // What bounds it, measured on GB300 (copy 6.78 TB/s):
 //  - DeepSeek-V3-shaped decode (256 experts, 32 rows each, 6.0 GB of 4-bit
 //    weights): 887 us, 6.9 TB/s: the weights' reading (bf16: 3325 us).
-//  - Mixtral-shaped batch (8192 rows over 8 experts, H 4096, I 14336): 414 to 430
+//  - Mixtral-shaped batch (8192 rows over 8 experts, H 4096, I 14336): 412 to 430
 //    us alone, 6.7 to 7.0 PFLOP/s; 466 to 483 after some tenths of a second, when
-//    the power limit lowers the clock (bf16: 1.79 to 1.87 ms).  A stage's
-//    instructions take 512 cycles (its bytes from the L2 come at 15 TB/s), 1132
-//    stages a pair 300 us; the rest is 0.6 us between two tiles, 9 us until the
-//    first is multiplied, and y's last round, in which half of the pairs have no
-//    tile.  Tensor pipe active 69 % of the cycles at a quarter of the rows.
-//  - One token over two Mixtral-shaped experts (187 MB): 40.7 us, of 27.6: the
+//    the power limit lowers the clock (bf16: 1.79 to 1.87 ms).  The products alone,
+//    nothing copied and no results written, take 360 of 415 us, 318 ns for each of a
+//    pair's 1132 stages: 300 us of instructions (512 cycles a stage), 0.6 us between
+//    two tiles, 9 us until the first is multiplied, and y's last round, in which half
+//    of the pairs have no tile.  Without the copies 369 us, without the results 382,
+//    without the products 323: the three delay one another by 55 us, on what is not
+//    established.  (A full stage is 72 KB a pair: 15 TB/s from the L2 on average.)
+//    Tensor pipe active 68 % of the cycles at a quarter of the rows.
+//  - One token over two Mixtral-shaped experts (187 MB): 40.5 us, of 27.6: the
 //    second expert's wait between a and y, and joining y's parts, 4 to 5 us each,
 //    and the start.  Bringing Wd into the L2 during the wait changed nothing.
-//  - Few blocks of contraction (H or I below 1024) and many tokens: the epilogue,
-//    4 us for a tile of 256 x 256.  More epilogue warps (12 or 16) were slower.
+//  - Many tokens and contractions below about 3700: the epilogue, 3 to 4 us for a
+//    tile of a of 256 x 256, as long as 11 to 14 stages.  65536 rows over 128 experts,
+//    H 2048, I 768: 210 us, 118 without its results; 8192 rows over 16, H and I 2048:
+//    59 and 43.  More epilogue warps (12 or 16) were slower.
 //  - Tiny calls: latency, as moe_ffn.cu.
 #include <mutex>
 

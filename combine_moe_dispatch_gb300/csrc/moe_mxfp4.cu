@@ -21,11 +21,14 @@
 // bytes and scales to its K rows.
 //
 // Measured on GB300 (copy 6.78 TB/s): 939.5 M elements of gate and up weights
-// quantised in 346 us (6.9 TB/s), read back in 395 (6.0 TB/s); with one block in
-// flight per lane both 778 us together, with two 743, with four 757.  DeepSeek-V3-shaped
-// decode dispatch, 1024 tokens to 8 rows each: 11.2 us for 46 MB, its rows read back
-// 25 us for 148 MB.  With four lanes to a block (two shuffles for the maximum, 4-byte
-// stores) the same took 872 us and 47 us together.
+// quantised in 347 us (6.9 TB/s), read back in 395 (6.0 TB/s); with one block in
+// flight per lane both 778 us together, with two 743, with four 757.  Rows by counts,
+// 8192 of 7168 over 256 experts: quantised in 28.8 us, read back in 29.1, 148 MB each
+// (5.1 TB/s; 65536 rows 197 and 206 us, 6 TB/s).  DeepSeek-V3-shaped decode dispatch,
+// 1024 tokens to 8 rows each, x from memory: 13.2 us for 46 MB, not memory but a chain
+// of latencies (x, then the routes in rounds of four); 8192 tokens 81 us, 4.5 TB/s.
+// With four lanes to a block (two shuffles for the maximum, 4-byte stores) weights
+// there and back took 872 us, decode's dispatch and its rows read back 47, now 37.5.
 #include "moe_mxfp4.cuh"
 #include "moe_rows.cuh"
 

@@ -20,12 +20,13 @@ namespace moe {
 namespace {
 
 // What one launch computes.  kForward: a (and h), then y, whose tiles wait until
-// every tile of a is written.  kRest: dx, dWgu and dWd, which need nothing of one
+// every tile of a is written, or every one of their group of experts.  kRest: dx, dWgu and dWd, which need nothing of one
 // another, as one list of tiles.
 enum Kind { kForward = 0, kActGrad = 1, kRest = 2 };
 
 constexpr int kEpiWarps = 8;           // two groups of four; each takes every other chunk of columns
-// Tiles announced ahead: kRing, and 2 where they are of kLongTile blocks or
+// The feed's places for tiles, and how many are announced ahead in the bf16
+// kernels (the 4-bit one has a figure of its own): kRing, and 2 where they are of kLongTile blocks or
 // more, since a unit taken early is a unit that cannot go to a pair that is
 // free sooner.  Measured: one token 116 us, with 4 ahead for all 122; uneven
 // experts' backward (2 to 32 blocks a tile) 213 us, with 2 ahead for all 217.
@@ -48,6 +49,7 @@ struct UnitCounter {
   uint32_t done;           // pairs that have taken all they will
   uint32_t epoch;          // kForward: which of `ready` counts this launch's
   uint32_t ready[2];       // CTAs' halves of tiles of a that are written; the other one is 0
+                           // (the 4-bit kernel counts them by groups of experts, in words of its own)
 };
 constexpr int kUnitWord = 1, kTicketWord = 8;            // in WsHeader::reserved
 // A wait that runs out leaves the counters and tickets unfinished, and the
@@ -93,7 +95,7 @@ struct alignas(16) Tile {
   int m;                   // tile of 256 accumulator rows
   int n0, n;               // first column, columns of the matrix instruction
   int cols;                // row products: tokens in the tile
-  int k0, nk;              // blocks of 64 of the contraction: [k0, k0 + nk); nk = 0: the result is 0
+  int k0, nk;              // blocks (P::kBlock) of the contraction: [k0, k0 + nk); nk = 0: the result is 0
   int split, part;         // parts of the tile's contraction, and which this is
   int slot;                // split > 1: tile among those that are cut
   int part_cols;           // and columns that each part's sums have room for
@@ -143,10 +145,11 @@ struct Schedule {
     }
   }
   // The tiles that would leave pairs idle in the last round are cut, if their
-  // contraction is of 1024 or more.  The estimate is in blocks of 64: a unit
-  // costs its blocks and about kUnitCost more (filling the ring, the epilogue),
-  // a tile that is cut kJoinCost and a block per part and 64 columns for the
-  // sums.  Measured with and without: one token (two experts, H 4096, I 14336)
+  // contraction is of 16 blocks or more (1024 elements of bf16, 4096 of 4 bits).  The
+  // estimate is in blocks: a unit costs its blocks and about kUnitCost more (filling
+  // the ring, the epilogue), a tile that is cut kJoinCost and a block per part and 64
+  // columns for the sums.  The costs and the 16 are those of bf16's blocks; with 4
+  // bits' they were not measured apart.  In bf16, with and without: one token (two experts, H 4096, I 14336)
   // 117 and 124 us; 128 rows of one expert, H 7168, I 2048: 36 and 41; 1109
   // rows, H 4416, I 2168: 71 and 74; uneven experts' backward 206 and 205;
   // ten rows over 95 experts 28 and 26 (counting the tiles takes 1 us).

@@ -90,8 +90,8 @@ size_t moe_workspace_size(const moe_shape *shape);
 /* Zero a workspace before its first use (enqueued on `stream`).  After
  * that the workspace keeps its counters consistent by itself, across shapes
  * and across calls that reported an error (the last thread block of every
- * moe_plan resets them); a TIMEOUT of moe_ffn or moe_ffn_backward alone needs
- * this call again.  A zero-filled allocation is already initialised.
+ * moe_plan resets them); a TIMEOUT of moe_ffn, moe_ffn_backward or
+ * moe_ffn_mxfp4 alone needs this call again.  A zero-filled allocation is already initialised.
  * Errors: INVALID_ARG (null), ALIGNMENT (not 16-byte aligned), CUDA. */
 moe_status moe_workspace_init(void *workspace, size_t workspace_bytes, void *stream);
 
@@ -355,9 +355,9 @@ moe_status moe_silu_mul_quant(const moe_shape *shape, int32_t intermediate, cons
  *       set, and a wait inside a kernel that runs out sets it to TIMEOUT.
  *       Its counters stand in the workspace's first 256 bytes, so that one
  *       workspace serves calls of different shapes in turn.  A wait of
- *       moe_ffn or moe_ffn_backward that ran out may leave them unfinished:
- *       from then on both write nothing and report TIMEOUT, also after another
- *       plan, until moe_workspace_init clears the workspace.
+ *       moe_ffn, moe_ffn_backward or moe_ffn_mxfp4 that ran out may leave them
+ *       unfinished: from then on the three write nothing and report TIMEOUT, also
+ *       after another plan, until moe_workspace_init clears the workspace.
  * Limits: payload BF16; intermediate % 8 == 0, intermediate < 2^29, H < 2^30;
  *       E * cap * 2 * intermediate and E * cap * H < 2^46; 4 * intermediate * H
  *       < 2^40.  All bf16 arrays 16-byte aligned.  No output may overlap an
